@@ -41,6 +41,25 @@ class Options(ctypes.Structure):
     _fields_ = [("split_k", ctypes.c_int32), ("tile_n", ctypes.c_int32)]
 
 
+# dense_gemm_act: the activations of the layer products
+ACTS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
+
+
+class Epilogue(ctypes.Structure):
+    """dense_gemm_epilogue: bias, residual and pre-activation (device pointers
+    with strides in elements), activation and form of dense_gemm_layer."""
+    _fields_ = [("bias", ctypes.c_void_p), ("bias_stride", ctypes.c_int64),
+                ("residual", ctypes.c_void_p), ("ldr", ctypes.c_int64),
+                ("preact", ctypes.c_void_p), ("ldz", ctypes.c_int64),
+                ("act", ctypes.c_int32), ("grad", ctypes.c_int32)]
+
+
+class Groups(ctypes.Structure):
+    """dense_gemm_groups: int32 group ends on the device, their number, and
+    the elements between the groups' matrices."""
+    _fields_ = [("ends", ctypes.c_void_p), ("count", ctypes.c_int64), ("stride", ctypes.c_int64)]
+
+
 class DenseGemmError(RuntimeError):
     def __init__(self, status: int, where: str):
         self.status = Status(status) if status in Status._value2member_map_ else status
@@ -76,6 +95,17 @@ SIGNATURES = {
     "gemm_nt_e4m3_mx_workspace_size": ([_i64, _i64, _i64, _i64, ctypes.POINTER(ctypes.c_size_t)],
                                        _i32),
     "gemm_nt_e4m3_mx_plan": ([_i64, _i64, _i64, _i64, ctypes.POINTER(_i64)], _i32),
+    "dense_gemm_layer": ([_i32] + _GEMM_ARGS[:-1] + [ctypes.POINTER(Epilogue),
+                                                    ctypes.POINTER(Groups), _vp, ctypes.c_size_t,
+                                                    _vp], _i32),
+    "dense_gemm_layer_workspace_size": ([_i32, _i64, _i64, _i64, _vp, _i64, _vp, _i64,
+                                         ctypes.POINTER(Groups), _i64,
+                                         ctypes.POINTER(ctypes.c_size_t)], _i32),
+    "dense_gemm_tn": ([_i32] + _GEMM_ARGS[:-1] + [_vp, ctypes.POINTER(Groups), _vp,
+                                                 ctypes.c_size_t, _vp], _i32),
+    "dense_gemm_tn_workspace_size": ([_i64, _i64, _i64, _vp, _i64, _vp, _i64,
+                                      ctypes.POINTER(Groups), _i64,
+                                      ctypes.POINTER(ctypes.c_size_t)], _i32),
     "gemm_nt_e4m3_mx_ex": ([_i64, _i64, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp,
                             _i64, _vp, ctypes.c_size_t, _vp], _i32),
 }
@@ -335,3 +365,252 @@ def gemm_nt_e4m3_mx(A, SA, B, SB, D=None, stream=None, workspace=None):
     if st != Status.OK:
         raise DenseGemmError(st, name)
     return D
+
+
+# ---- the products of a layer ------------------------------------------------
+
+def _formats():
+    import torch
+    return {torch.float16: ("f16", 0), torch.bfloat16: ("bf16", 1)}
+
+
+def _check_like(t, A, dims: int, what: str, shape=None):
+    """A device tensor of A's type and device with ``dims`` dimensions, a unit
+    last stride and (where given) this shape."""
+    if t.dtype != A.dtype:
+        raise TypeError("%s must be %s like A, got %s" % (what, A.dtype, t.dtype))
+    if t.device != A.device:
+        raise ValueError("operands on different devices: %s and %s" % (A.device, t.device))
+    if t.dim() != dims or (t.stride(-1) != 1 and t.shape[-1] > 1):
+        raise ValueError("%s must be %d-D with unit stride in its last dimension" % (what, dims))
+    if shape is not None and tuple(t.shape) != shape:
+        raise ValueError("%s has shape %s, expected %s" % (what, tuple(t.shape), shape))
+
+
+def _check_first(A):
+    """A's format, as (name, dense_gemm_fmt)."""
+    fmt = _formats().get(A.dtype)
+    if fmt is None:
+        raise TypeError("A must be float16 or bfloat16, got %s" % A.dtype)
+    if not A.is_cuda:
+        raise ValueError("A must be a device tensor")
+    if A.dim() != 2 or (A.stride(1) != 1 and A.shape[1] > 1):
+        raise ValueError("A must be 2-D with unit column stride")
+    return fmt
+
+
+def _check_ends(ends, A):
+    import torch
+    if ends.dtype != torch.int32:
+        raise TypeError("ends must be int32, got %s" % ends.dtype)
+    if ends.device != A.device:
+        raise ValueError("operands on different devices: %s and %s" % (A.device, ends.device))
+    if ends.dim() != 1 or (ends.shape[0] > 1 and ends.stride(0) != 1):
+        raise ValueError("ends must be 1-D and contiguous")
+
+
+def _stack(t):
+    """(elements between the matrices, leading dimension) of a 3-D tensor with
+    unit last stride."""
+    ld = t.stride(1) if t.shape[1] > 1 else max(t.shape[2], 1)
+    return (t.stride(0) if t.shape[0] > 1 else 0), ld
+
+
+def _run_with_workspace(name, call, size_of, workspace, stream, dev):
+    """Runs ``call(pointer, bytes, stream handle)``.  Without a workspace of
+    the caller's, one is taken from torch's allocator if the call turns out
+    to need it."""
+    import contextlib
+    import torch
+    here = torch.cuda.current_device() == dev.index
+    with contextlib.nullcontext() if here else torch.cuda.device(dev):
+        sh = _stream_handle(stream, dev)
+        if workspace is None or workspace is True:
+            st = call(None, 0, sh)
+            if st == Status.WORKSPACE_TOO_SMALL:
+                need = ctypes.c_size_t()
+                st = size_of(ctypes.byref(need))
+                if st == Status.OK:
+                    ws = _used_by(torch.empty(need.value, dtype=torch.uint8, device=dev), stream,
+                                  dev)
+                    st = call(ws.data_ptr(), need.value, sh)
+        else:
+            if not workspace.is_cuda or workspace.device != dev:
+                raise ValueError("workspace must be a device tensor on %s" % dev)
+            st = call(workspace.data_ptr(), workspace.numel() * workspace.element_size(), sh)
+    if st != Status.OK:
+        raise DenseGemmError(st, name)
+
+
+def _layer(layout, A, B, ends, bias, act, residual, preact, grad, D, stream, workspace):
+    import torch
+    lib = load_library()
+    fmt, _ = _check_first(A)
+    if act not in ACTS:
+        raise ValueError("act must be one of %s, got %r" % (", ".join(ACTS), act))
+    M, K = A.shape
+    _check_like(B, A, 2 if ends is None else 3, "B")
+    Kb, N = B.shape[-2:] if layout == "nn" else (B.shape[-1], B.shape[-2])
+    if Kb != K:
+        raise ValueError("inner dimensions differ: A is %s, B is %s"
+                         % (tuple(A.shape), tuple(B.shape)))
+    groups = None
+    if ends is None:
+        ldb, G = _ld(B), ()
+    else:
+        _check_ends(ends, A)
+        if ends.shape[0] != B.shape[0]:
+            raise ValueError("%d group ends for %d matrices B" % (ends.shape[0], B.shape[0]))
+        stride, ldb = _stack(B)
+        G = (B.shape[0],)
+        groups = Groups(ends.data_ptr(), B.shape[0], stride)
+    epi = Epilogue(act=ACTS[act], grad=grad)
+    if bias is not None:
+        _check_like(bias, A, 1 + len(G), "bias", G + (N,))
+        epi.bias = bias.data_ptr()
+        epi.bias_stride = bias.stride(0) if G and G[0] > 1 else 0
+    if residual is not None:
+        _check_like(residual, A, 2, "residual", (M, N))
+        epi.residual, epi.ldr = residual.data_ptr(), _ld(residual)
+    if preact is not None:
+        _check_like(preact, A, 2, "preact", (M, N))
+        epi.preact, epi.ldz = preact.data_ptr(), _ld(preact)
+    dev = A.device
+    if D is None:
+        D = _used_by(torch.empty((M, N), dtype=A.dtype, device=dev), stream, dev)
+    else:
+        _check_like(D, A, 2, "D", (M, N))
+    op = OPS[(layout, fmt)]
+    a, b, lda = A.data_ptr(), B.data_ptr(), _ld(A)
+
+    def call(ws, nbytes, sh):
+        return lib.dense_gemm_layer(op, M, N, K, a, lda, b, ldb, D.data_ptr(), _ld(D), epi, groups,
+                                    ws, nbytes, sh)
+
+    def size_of(out):
+        return lib.dense_gemm_layer_workspace_size(op, M, N, K, a, lda, b, ldb, groups, 0, out)
+
+    _run_with_workspace("dense_gemm_layer", call, size_of, workspace, stream, dev)
+    return D
+
+
+def gemm_nt_fused(A, B, bias=None, act="none", residual=None, preact=None, D=None, stream=None,
+                  workspace=None):
+    """D = act(Z) + residual with Z = A @ B.T + bias, FP16 or BF16 with FP32
+    accumulation and one rounding; A is M x K, B is N x K, bias has N values,
+    residual is M x N and may be D itself.  ``act``: "none", "relu", "gelu",
+    "gelu_tanh" or "silu".  ``preact``: an M x N tensor that receives Z (for
+    :func:`gemm_nn_dact`).  ``workspace``: a device tensor (256-byte aligned,
+    dense_gemm_layer_workspace_size bytes), or None to take one from torch's
+    allocator where the call needs it.  The call is asynchronous on
+    ``stream`` (None: the current stream)."""
+    return _layer("nt", A, B, None, bias, act, residual, preact, 0, D, stream, workspace)
+
+
+def gemm_nn_fused(A, B, bias=None, act="none", residual=None, preact=None, D=None, stream=None,
+                  workspace=None):
+    """:func:`gemm_nt_fused` with B K x N: Z = A @ B + bias."""
+    return _layer("nn", A, B, None, bias, act, residual, preact, 0, D, stream, workspace)
+
+
+def gemm_nt_dact(A, B, preact, act, D=None, stream=None, workspace=None):
+    """D = (A @ B.T) * act'(preact): the gradient of a layer's input carried
+    through the activation that produced it.  A is M x K, B is N x K, preact
+    (M x N, may be D itself) is what the forward call stored; ``act`` as
+    there, but not "none".  Other arguments as for :func:`gemm_nt_fused`."""
+    return _layer("nt", A, B, None, None, act, None, preact, 1, D, stream, workspace)
+
+
+def gemm_nn_dact(A, B, preact, act, D=None, stream=None, workspace=None):
+    """:func:`gemm_nt_dact` with B K x N: D = (A @ B) * act'(preact)."""
+    return _layer("nn", A, B, None, None, act, None, preact, 1, D, stream, workspace)
+
+
+def gemm_nt_grouped(A, B, ends, bias=None, act="none", residual=None, preact=None, D=None,
+                    stream=None, workspace=None):
+    """:func:`gemm_nt_fused` for rows sorted into G groups (the experts of a
+    layer): rows ends[g - 1] .. ends[g] - 1 of A (M x K) are multiplied with
+    B[g] (G x N x K) and take bias[g] (G x N).  ``ends``: G int32 values on
+    the device, not decreasing; the host never reads them.  Rows at or past
+    the last end are neither read nor written (with D None they hold
+    whatever the allocator returned)."""
+    return _layer("nt", A, B, ends, bias, act, residual, preact, 0, D, stream, workspace)
+
+
+def gemm_nn_grouped(A, B, ends, bias=None, act="none", residual=None, preact=None, D=None,
+                    stream=None, workspace=None):
+    """:func:`gemm_nt_grouped` with B G x K x N."""
+    return _layer("nn", A, B, ends, bias, act, residual, preact, 0, D, stream, workspace)
+
+
+def gemm_nt_grouped_dact(A, B, ends, preact, act, D=None, stream=None, workspace=None):
+    """:func:`gemm_nt_dact` for rows sorted into groups, with B G x N x K."""
+    return _layer("nt", A, B, ends, None, act, None, preact, 1, D, stream, workspace)
+
+
+def gemm_nn_grouped_dact(A, B, ends, preact, act, D=None, stream=None, workspace=None):
+    """:func:`gemm_nn_dact` for rows sorted into groups, with B G x K x N."""
+    return _layer("nn", A, B, ends, None, act, None, preact, 1, D, stream, workspace)
+
+
+def _tn(A, B, ends, D, colsum, stream, workspace):
+    import torch
+    lib = load_library()
+    _, fmt = _check_first(A)
+    K, M = A.shape
+    _check_like(B, A, 2, "B")
+    N = B.shape[1]
+    if B.shape[0] != K:
+        raise ValueError("row counts differ: A is %s, B is %s" % (tuple(A.shape), tuple(B.shape)))
+    dev = A.device
+    G = ()
+    if ends is not None:
+        _check_ends(ends, A)
+        G = (ends.shape[0],)
+    if D is None:
+        D = _used_by(torch.empty(G + (M, N), dtype=A.dtype, device=dev), stream, dev)
+    else:
+        _check_like(D, A, 2 + len(G), "D", G + (M, N))
+    sums = None
+    if colsum is True:
+        sums = _used_by(torch.empty(G + (M,), dtype=A.dtype, device=dev), stream, dev)
+    elif colsum is not None and colsum is not False:
+        sums = colsum
+        _check_like(sums, A, 1 + len(G), "colsum", G + (M,))
+        if not sums.is_contiguous():
+            raise ValueError("colsum must be contiguous")
+    groups = None
+    if ends is None:
+        ldd = _ld(D)
+    else:
+        stride, ldd = _stack(D)
+        groups = Groups(ends.data_ptr(), G[0], stride)
+    a, b, lda, ldb = A.data_ptr(), B.data_ptr(), _ld(A), _ld(B)
+    sums_ptr = None if sums is None else sums.data_ptr()
+
+    def call(ws, nbytes, sh):
+        return lib.dense_gemm_tn(fmt, M, N, K, a, lda, b, ldb, D.data_ptr(), ldd, sums_ptr, groups,
+                                 ws, nbytes, sh)
+
+    def size_of(out):
+        return lib.dense_gemm_tn_workspace_size(M, N, K, a, lda, b, ldb, groups, 0, out)
+
+    _run_with_workspace("dense_gemm_tn", call, size_of, workspace, stream, dev)
+    return D if sums is None else (D, sums)
+
+
+def gemm_tn(A, B, D=None, colsum=None, stream=None, workspace=None):
+    """D = A.T @ B (M x N, FP16 or BF16, FP32 accumulation): a layer's weight
+    gradient from the gradient of its output, A (K x M, a row per token), and
+    its input, B (K x N).  ``colsum``: True, or a tensor of M values, for the
+    sums of A's columns too (the bias gradient): returns (D, colsum).
+    ``workspace`` (dense_gemm_tn_workspace_size bytes) and ``stream`` as for
+    :func:`gemm_nt_fused`."""
+    return _tn(A, B, None, D, colsum, stream, workspace)
+
+
+def gemm_tn_grouped(A, B, ends, D=None, colsum=None, stream=None, workspace=None):
+    """:func:`gemm_tn` for rows sorted into G groups (``ends`` as for
+    :func:`gemm_nt_grouped`): D is G x M x N and colsum G x M, each group's
+    sums over its own rows, zero for an empty group."""
+    return _tn(A, B, ends, D, colsum, stream, workspace)

@@ -139,6 +139,30 @@ __device__ __forceinline__ uint32_t pack2<__bf16>(float lo, float hi) {
   return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2){lo, hi}, bf16x2));
 }
 
+// s plus the eight 16-bit values of an MFMA fragment's lane, in FP32 (two
+// values per v_dot2c, with ones).
+template <typename T>
+__device__ __forceinline__ float sum8(float s, u32x4 f);
+template <>
+__device__ __forceinline__ float sum8<_Float16>(float s, u32x4 f) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const uint32_t w = f[k];  // (the bit cast of the element itself takes element 0)
+    s = __builtin_amdgcn_fdot2(__builtin_bit_cast(f16x2, w), (f16x2){1.0f, 1.0f}, s, false);
+  }
+  return s;
+}
+template <>
+__device__ __forceinline__ float sum8<__bf16>(float s, u32x4 f) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const uint32_t w = f[k];
+    s = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, w),
+                                        (bf16x2){(__bf16)1.0f, (__bf16)1.0f}, s, false);
+  }
+  return s;
+}
+
 // Transposing LDS read: within each 16-lane block, lane i receives element
 // i % 4 of the 8 bytes addressed by lanes 4j + i / 4, for j = 0..3.
 __device__ __forceinline__ u32x2 read_tr(const char* p) {

@@ -1,6 +1,6 @@
-// gemm_kernel.h -- the FP16/BF16 tiled GEMM kernels for the MI355X (gfx950):
-// the persistent GEMM kernel and the operand repack (the split-K reduction
-// is in split_reduce.h).
+// gemm_kernel.h -- the FP16/BF16 tiled GEMM kernel for the MI355X (gfx950):
+// the persistent GEMM kernel (the split-K reduction is in split_reduce.h,
+// the operand repack in repack.h).
 //
 // Kernel structure (one persistent workgroup per CU):
 //   * a persistent loop over output tiles in the grouped, XCD-aware order of
@@ -36,7 +36,11 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "cdna_ops.h"
+#include "epilogue.h"
+#include "groups.h"
 #include "tile_config.h"
 #include "tile_sched.h"
 
@@ -82,6 +86,18 @@ struct Params {
   float* ws;
 };
 
+// What the products of a layer (layer.hip) add: the epilogue's operands
+// (epilogue.h), the row groups (groups.h) and the column sums of A (SUMS;
+// groups x M in the output type): stored by the tiles of the first tile
+// column; a part of a split tile writes its TM sums in FP32 at colsum_ws +
+// (its partial tile's index) * TM.
+struct LayerParams : Params {
+  Epilogue e;
+  Groups g;
+  uint16_t* colsum;
+  float* colsum_ws;
+};
+
 template <int MA, int NB>
 struct Frags {
   u32x4 a[MA];
@@ -93,10 +109,25 @@ struct Frags {
 // half-padded 256-wide tile), and for twice the tiles where 256-wide ones
 // would leave half the CUs idle, at more operand traffic per FLOP.  Tile
 // rows TM: 256, or 128 where M <= 128 (four 64-row wave tiles).
-template <typename T, int LAYOUT, bool SPLIT, int TN, int TM>
-__global__ __launch_bounds__(THREADS) void gemm_kernel(Params p) {
+//
+// Three further parameters serve the products of a layer:
+//   LAYOUT TA  D = A.T @ B with A K x M and B K x N, both row-major: both
+//              tiles are 64 k rows of 512 B, read with transposing LDS reads;
+//   EPI        bias, activation, residual or activation gradient applied to
+//              the accumulators before the one rounding (epilogue.h);
+//   GROUP      rows sorted into groups (groups.h): for A @ B.T and A @ B a
+//              matrix B per group of rows of A and D; for A.T @ B a sum over
+//              each group's rows, and an output matrix per group;
+//   SUMS       (TA) also the sums of A's columns over k.
+template <typename T, int LAYOUT, bool SPLIT, int TN, int TM, bool EPI = false, bool GROUP = false,
+          bool SUMS = false>
+__global__ __launch_bounds__(THREADS) void gemm_kernel(
+    std::conditional_t<EPI || GROUP || LAYOUT == TA, LayerParams, Params> p) {
   static_assert(TN == BN || (TN == BN / 2 && LAYOUT == NT), "tile widths 256, and 128 for A @ B.T");
-  static_assert(TM == BM || TM == BM / 2, "tile rows 256 or 128");
+  static_assert(TM == BM || (TM == BM / 2 && LAYOUT != TA), "tile rows 256 or 128");
+  static_assert(!(EPI && LAYOUT == TA), "no epilogue on A.T @ B");
+  static_assert(!SUMS || LAYOUT == TA, "column sums of A where its rows are k");
+  static_assert(!(GROUP && SPLIT && LAYOUT != TA), "row groups are not split in K");
   constexpr int WTM = wave_rows<TM>();             // wave tile rows
   constexpr int MI = WTM / 16;                     // 16 x 16 blocks per wave, M direction
   constexpr int A_BYTES = TM * BK * 2;             // bytes of an A tile (TM rows x 128 B)
@@ -110,7 +141,8 @@ __global__ __launch_bounds__(THREADS) void gemm_kernel(Params p) {
   // earlier (0 = A, 1 = B): B for A @ B, whose row-major tile (64 rows of
   // 512 B, far apart in memory) is the costlier one to load (measured: 1.4%
   // faster than A there); A for A @ B.T (the two are alike).
-  constexpr int EARLY = LAYOUT == NN ? 1 : 0;
+  constexpr int EARLY = LAYOUT == NT ? 0 : 1;
+  constexpr bool ROWS = GROUP && LAYOUT != TA;  // groups of rows of A and D
   constexpr int DMA_E = EARLY == 0 ? DMA_PER_OPERAND : DMA_B;   // loads of the early tile
   constexpr int DMA_L = EARLY == 0 ? DMA_B : DMA_PER_OPERAND;   // and of the other
   constexpr int E_BYTES = EARLY == 0 ? A_BYTES : B_TILE;
@@ -125,22 +157,50 @@ __global__ __launch_bounds__(THREADS) void gemm_kernel(Params p) {
   const int wm = wave >> 1;  // wave tile row (0..1)
   const int wn = wave & 1;   // wave tile column (0..1)
 
-  const int nk = (p.K + BK - 1) / BK;
   const int slot0 = xcd_slot(blockIdx.x, gridDim.x, p.num_xcds);
+  [[maybe_unused]] GroupWalk walk;
+  if constexpr (ROWS) walk.start(p.g);
 
-  for (int task = slot0; task < p.num_tasks; task += gridDim.x) {
+  for (int task = slot0; ROWS || task < p.num_tasks; task += gridDim.x) {
     int tm, tn;
     const bool part = SPLIT && task >= p.full_tasks;
     const int u = task - p.full_tasks;
     const int tile = part ? p.full_tasks + u % p.tiles : task;
     const int split = part ? u / p.tiles : 0;
-    tile_of_task(tile, p.tiles_m, p.tiles_n, p.group_m, &tm, &tn);
+    // the operands, rows and K of the task's product: the call's, or with
+    // groups those of the tile's group
+    const uint16_t *gA = p.A, *gB = p.B;
+    uint16_t* gD = p.D;
+    int row0 = 0, M = p.M, K = p.K, steps = p.split_steps;
+    [[maybe_unused]] int group = 0;
+    if constexpr (ROWS) {
+      if (!walk.find(p.g, task, TM, p.tiles_n)) break;
+      group = walk.g;
+      row0 = walk.beg;
+      M = walk.end;
+      gB += group * p.g.stride;
+      const int tiles_m = (M - row0 + TM - 1) / TM;
+      tile_of_task(task - walk.first, tiles_m, p.tiles_n, min(tiles_m, p.group_m), &tm, &tn);
+    } else if constexpr (GROUP) {
+      const int per = p.tiles_m * p.tiles_n;
+      group = tile / per;
+      tile_of_task(tile - group * per, p.tiles_m, p.tiles_n, p.group_m, &tm, &tn);
+      const int beg = group > 0 ? group_end(p.g, group - 1) : 0;
+      K = max(group_end(p.g, group) - beg, 0);
+      gA += (int64_t)beg * p.lda;
+      gB += (int64_t)beg * p.ldb;
+      gD += group * p.g.stride;
+      if (SPLIT) steps = ((K + BK - 1) / BK + p.splits - 1) / p.splits;
+    } else {
+      tile_of_task(tile, p.tiles_m, p.tiles_n, p.group_m, &tm, &tn);
+    }
     // this task's K steps
-    const int kbeg = split * p.split_steps;
-    const int kend = part ? min(nk, kbeg + p.split_steps) : nk;
-    const int m0 = tm * TM;
+    const int nk = (K + BK - 1) / BK;
+    const int kbeg = split * steps;
+    const int kend = part ? min(nk, kbeg + steps) : nk;
+    const int m0 = row0 + tm * TM;
     const int n0 = tn * TN;
-    const int vm = min(TM, p.M - m0);  // valid rows of the A tile
+    const int vm = min(TM, M - m0);    // valid rows of the A tile (A.T @ B: columns)
     const int vn = min(TN, p.N - n0);  // valid columns of D in this tile
 
     // MFMA operand layout (16 x 16 x 32): lane l holds row l % 16 of a
@@ -167,13 +227,14 @@ __global__ __launch_bounds__(THREADS) void gemm_kernel(Params p) {
     // thread covers rows (L w + i) * 8 ... +7, lane -> row lane/8 of the
     // group and a logical chunk by the swizzle (which depends on the row's
     // low four bits, i.e. on i's parity, L being even).
-    // NN B tile: each wave instruction fills 2 k rows of 512 B.
+    // NN and TA B tile, TA A tile: each wave instruction fills 2 k rows of 512 B.
     const int nn_row_lo = lane >> 5;
 
     // Fragment read offsets (bytes within a stage).  Fragment f of a
     // K-contiguous tile (16 rows) sits 16 * 128 bytes after fragment 0: the
     // swizzle depends only on the row's low four bits.
     int fa[SUB], fb[SUB], fbn[NI];
+    [[maybe_unused]] int fan[MI];
 #pragma unroll
     for (int s = 0; s < SUB; ++s) {
       fa[s] = (wm * WTM + l16) * 128 + (((4 * s + lq) ^ swz_k(l16)) << 4);
@@ -191,6 +252,11 @@ __global__ __launch_bounds__(THREADS) void gemm_kernel(Params p) {
 #pragma unroll
       for (int j = 0; j < NI; ++j)
         fbn[j] = klane * 512 + (((wn * 16 + 2 * j + ((lane & 3) >> 1)) ^ fl) << 4) + (lane & 1) * 8;
+      if constexpr (LAYOUT == TA) {
+#pragma unroll
+        for (int i = 0; i < MI; ++i)
+          fan[i] = klane * 512 + (((wm * 16 + 2 * i + ((lane & 3) >> 1)) ^ fl) << 4) + (lane & 1) * 8;
+      }
     }
 
     // Per-lane load offsets, fixed for the tile; the buffer descriptor of
@@ -203,8 +269,8 @@ __global__ __launch_bounds__(THREADS) void gemm_kernel(Params p) {
     // up to 8; where K8 > K the operand is a zero-padded copy, or for the NN
     // B the descriptor ends at row K-1).  Only the first step reaches outside
     // [0, K8) -- below 0 -- so only its loads, issued in the prologue, need
-    // per-lane masks.
-    const int K8 = (p.K + 7) & ~7;
+    // per-lane masks.  (TA: k is a row of both operands, so no rounding.)
+    const int K8 = LAYOUT == TA ? K : (K + 7) & ~7;
     const int koff = (BK - (K8 & (BK - 1))) & (BK - 1);
     uint32_t a_off[DMA_PER_OPERAND], b_off[DMA_B];
     int kc[2];  // logical chunk of this lane for even / odd instruction index
@@ -212,8 +278,13 @@ __global__ __launch_bounds__(THREADS) void gemm_kernel(Params p) {
     for (int h = 0; h < 2; ++h) kc[h] = (lane & 7) ^ swz_k(h * 8 + (lane >> 3));
 #pragma unroll
     for (int i = 0; i < DMA_PER_OPERAND; ++i) {
-      const int r = (DMA_PER_OPERAND * wave + i) * 8 + (lane >> 3);
-      a_off[i] = r < vm ? (uint32_t)(r * p.lda * 2 + kc[i & 1] * 16) : OOB;
+      if constexpr (LAYOUT == TA) {
+        const int k = 2 * (8 * wave + i) + nn_row_lo;
+        a_off[i] = (uint32_t)(k * p.lda * 2 + ((lane & 31) ^ swz_n(k)) * 16);
+      } else {
+        const int r = (DMA_PER_OPERAND * wave + i) * 8 + (lane >> 3);
+        a_off[i] = r < vm ? (uint32_t)(r * p.lda * 2 + kc[i & 1] * 16) : OOB;
+      }
     }
     if (LAYOUT == NT) {
 #pragma unroll
@@ -251,30 +322,35 @@ __global__ __launch_bounds__(THREADS) void gemm_kernel(Params p) {
       h.k0 = k0;
       h.base = lds0 + (half == EARLY ? 0 : RING2) + slot * (half == 0 ? A_BYTES : B_TILE) +
                ((half == 0 ? DMA_PER_OPERAND : DMA_B) * wave) * 1024;
-      if (half == 0 || LAYOUT == NT) {
+      if ((half == 0 && LAYOUT != TA) || LAYOUT == NT) {
         // columns k0 .. K8 of the tile's rows
-        const uint64_t src = half == 0 ? (uint64_t)(uintptr_t)(p.A + (int64_t)m0 * p.lda)
-                                       : (uint64_t)(uintptr_t)(p.B + (int64_t)n0 * p.ldb);
+        const uint64_t src = half == 0 ? (uint64_t)(uintptr_t)(gA + (int64_t)m0 * p.lda)
+                                       : (uint64_t)(uintptr_t)(gB + (int64_t)n0 * p.ldb);
         const int span = half == 0 ? (vm - 1) * p.lda : (vn - 1) * p.ldb;
         const uint32_t bytes = (uint32_t)(span + K8 - k0) * 2u;
         h.r = make_rsrc(src + 2 * (int64_t)k0, live ? bytes : 0u);
+      } else if (half == 0) {
+        // (TA) rows k0 .. min(k0 + BK, K) - 1 of A, columns m0 .. M (rounded up to 8)
+        const int rows = min(BK, K - k0);
+        const uint32_t bytes = (uint32_t)((rows - 1) * p.lda + ((M - m0 + 7) & ~7)) * 2u;
+        h.r = make_rsrc((uint64_t)(uintptr_t)(gA + m0) + 2 * (int64_t)k0 * p.lda, live ? bytes : 0u);
       } else {
         // rows k0 .. min(k0 + BK, K) - 1 of B, columns n0 .. N (rounded up to 8)
-        const int rows = min(BK, p.K - k0);
+        const int rows = min(BK, K - k0);
         const uint32_t bytes = (uint32_t)((rows - 1) * p.ldb + ((p.N - n0 + 7) & ~7)) * 2u;
-        h.r = make_rsrc((uint64_t)(uintptr_t)(p.B + n0) + 2 * (int64_t)k0 * p.ldb, live ? bytes : 0u);
+        h.r = make_rsrc((uint64_t)(uintptr_t)(gB + n0) + 2 * (int64_t)k0 * p.ldb, live ? bytes : 0u);
       }
       return h;
     };
     // One load of a refill.  MASKED (prologue only): chunks or rows before
     // k = 0 read zeros.
     auto refill_one = [&](const Half& h, int half, int i, bool masked) {
-      if (half == 0 || LAYOUT == NT) {
-        const uint32_t off = half == 0 ? a_off[i] : b_off[i];
+      const uint32_t off = half == 0 ? a_off[i] : b_off[i];
+      if ((half == 0 && LAYOUT != TA) || LAYOUT == NT) {
         dma16_at(h.r, !masked || h.k0 + (kc[i & 1] << 3) >= 0 ? off : OOB, h.base, i * 1024);
       } else {
         const int k = 2 * (8 * wave + i) + nn_row_lo;
-        dma16_at(h.r, !masked || h.k0 + k >= 0 ? b_off[i] : OOB, h.base, i * 1024);
+        dma16_at(h.r, !masked || h.k0 + k >= 0 ? off : OOB, h.base, i * 1024);
       }
       fence();
     };
@@ -288,19 +364,28 @@ __global__ __launch_bounds__(THREADS) void gemm_kernel(Params p) {
     };
 
     // Fragment reads of k-substep s of the stage in slot `slot`, one LDS
-    // instruction at a time: item f < MI reads A fragment f; the rest read the
-    // B fragments (NT: one ds_read_b128 each; NN: two transposing reads each).
-    constexpr int READS = MI + (LAYOUT == NT ? NI : 2 * NI);
+    // instruction at a time: the first A_READS items read the A fragments, the
+    // rest the B fragments (one ds_read_b128 each from a K-contiguous tile,
+    // two transposing reads from a tile of k rows).
+    constexpr int A_READS = LAYOUT == TA ? 2 * MI : MI;
+    constexpr int READS = A_READS + (LAYOUT == NT ? NI : 2 * NI);
     auto read_item = [&](int es, int ls, int s, Frags& F, int f) {
       const char* abase = smem + (EARLY == 0 ? es * A_BYTES : RING2 + ls * A_BYTES);
       const char* bbase = smem + (EARLY == 1 ? es * B_TILE : RING2 + ls * B_TILE);
-      if (f < MI) {
-        F.a[f] = *(const u32x4*)(abase + fa[s] + f * 2048);
+      if (f < A_READS) {
+        if constexpr (LAYOUT == TA) {
+          const int i = f >> 1, h = f & 1;
+          const u32x2 v = read_tr(abase + fan[i] + (s * 32 + 4 * h) * 512);
+          F.a[i][2 * h] = v[0];
+          F.a[i][2 * h + 1] = v[1];
+        } else {
+          F.a[f] = *(const u32x4*)(abase + fa[s] + f * 2048);
+        }
       } else if (LAYOUT == NT) {
-        const int j = f - MI;
+        const int j = f - A_READS;
         F.b[j] = *(const u32x4*)(bbase + fb[s] + j * 2048);
       } else {
-        const int j = (f - MI) >> 1, h = (f - MI) & 1;
+        const int j = (f - A_READS) >> 1, h = (f - A_READS) & 1;
         const u32x2 v = read_tr(bbase + fbn[j] + (s * 32 + 4 * h) * 512);
         F.b[j][2 * h] = v[0];
         F.b[j][2 * h + 1] = v[1];
@@ -360,6 +445,15 @@ __global__ __launch_bounds__(THREADS) void gemm_kernel(Params p) {
     wait_vm_barrier<DMA_PER_OPERAND + DMA_B>();
     read_frags(0, 0, 0, F0);
 
+    // Column sums of A: lane (l16, lq) adds the eight k of its part of each A
+    // fragment, in the shadow of the MFMAs that use it.  Every tile does so
+    // though only the first tile column keeps the sums: a branch in the loop
+    // would end the basic block that the fences order.
+    [[maybe_unused]] float cs[MI];
+    if constexpr (SUMS) {
+#pragma unroll
+      for (int i = 0; i < MI; ++i) cs[i] = 0.0f;
+    }
     int es = 0;  // early-ring slot of stage ks
     for (int ks = kbeg; ks < kend; ++ks) {
       const int ls = (ks - kbeg) & 1;           // two-slot-ring slot of stage ks
@@ -370,6 +464,7 @@ __global__ __launch_bounds__(THREADS) void gemm_kernel(Params p) {
       for (int q = 0; q < PAIRS; ++q) {
         share(q, PAIRS, READS, [&](int f) { read_item(es, ls, 1, F1, f); });
         mfma_pair(F0, q);
+        if constexpr (SUMS) share(q, PAIRS, MI, [&](int i) { cs[i] = sum8<T>(cs[i], F0.a[i]); });
         fence();
         // (the descriptor's scalar work goes behind the first MFMAs)
         if (q == 0) he = half_setup(ks + 2, es2, EARLY);
@@ -386,6 +481,7 @@ __global__ __launch_bounds__(THREADS) void gemm_kernel(Params p) {
         if (q >= BAR_PAIR)
           share(q - BAR_PAIR, PAIRS - BAR_PAIR, READS, [&](int f) { read_item(es1, ls ^ 1, 0, F0, f); });
         mfma_pair(F1, q);
+        if constexpr (SUMS) share(q, PAIRS, MI, [&](int i) { cs[i] = sum8<T>(cs[i], F1.a[i]); });
         fence();
         if (q >= BAR_PAIR)
           share(q - BAR_PAIR, PAIRS - BAR_PAIR, DMA_L,
@@ -399,7 +495,26 @@ __global__ __launch_bounds__(THREADS) void gemm_kernel(Params p) {
     asm volatile("s_nop 7\n\ts_nop 7\n\ts_nop 7\n\ts_nop 7" ::: "memory");
     fence();
 
-    if (part) {
+    if constexpr (SUMS) {
+      if (tn == 0 && wn == 0) {
+        // the four lane groups' parts of each column, added in a fixed order
+#pragma unroll
+        for (int i = 0; i < MI; ++i) {
+          float s = cs[i];
+          s += __shfl_xor(s, 16);
+          s += __shfl_xor(s, 32);
+          const int c = wm * WTM + 16 * i + l16;  // column of the tile
+          if (lq == 0 && c < vm) {
+            if (part)
+              p.colsum_ws[(size_t)(split * p.tiles + u % p.tiles) * TM + c] = s;
+            else
+              p.colsum[(int64_t)group * p.M + m0 + c] = (uint16_t)pack2<T>(s, 0.0f);
+          }
+        }
+      }
+    }
+
+    if (!EPI && part) {
       // FP32 partial tile, row-major 256 x 256: lane holds row l16 of each
       // 16-row block and columns j*16 + 4*lq .. +3 (16 contiguous bytes);
       // 16 x 16 blocks wholly outside D are skipped (nothing reads them)
@@ -416,6 +531,138 @@ __global__ __launch_bounds__(THREADS) void gemm_kernel(Params p) {
         }
         __builtin_amdgcn_sched_barrier(0);
       }
+      continue;
+    }
+
+    if constexpr (EPI) {
+      // Epilogue of a layer's product (epilogue.h): per 32-row band (two
+      // 16-row blocks), the band's FP32 accumulators of this wave are staged
+      // in LDS (rows of CHF 16-byte chunks), so that each lane gets eight
+      // consecutive columns of a row and reads the residual or Z, and writes
+      // Z and D, in 16-byte accesses.  (Staged in 16 bits, as below, the
+      // residual could only be added after a first rounding.)  Chunk c of
+      // row r is stored at c ^ (c >> 3 & 1) ^ (r & 7): the writes (one chunk
+      // of eight rows) and the reads (every other chunk of a row) both touch
+      // distinct banks.  The loop over the bands is not unrolled: the code of
+      // eight activations and slopes stays small enough for the instruction
+      // cache beside the K loop.
+      constexpr int CH = WTN / 8;      // lanes per staged row
+      constexpr int CHF = WTN / 4;     // 16-byte chunks per staged row
+      constexpr int RPI = 64 / CH;     // rows per wave instruction
+      constexpr int R = 4;             // row instructions per pass
+      constexpr int PASSES = 32 / (RPI * R);  // passes per band
+      static_assert(WAVES * 32 * WTN * 4 <= LDS_BYTES, "a band of every wave fits the rings");
+      const Epilogue& ep = p.e;
+      char* stg = smem + wave * (32 * CHF * 16);
+      const int cc = lane % CH, rl = lane / CH;
+      const int col = n0 + wn * WTN + cc * 8;
+      const int rowb = m0 + wm * WTM + rl;  // this lane's first row of the wave's
+      uint32_t bias[4] = {0u, 0u, 0u, 0u};
+      if (!ep.grad && ep.bias != nullptr && col < p.N)
+        load_row<4>(ep.bias + group * ep.bias_stride, col, p.N, ep.bias_vec, bias);
+      // the operand each output needs: the residual, or the gradient's Z
+      const uint16_t* side = ep.grad ? ep.z : ep.res;
+      const int64_t lds_ = ep.grad ? ep.ldz : ep.ldr;
+      const int side_vec = ep.grad ? ep.z_vec : ep.res_vec;
+      auto fetch = [&](int pass, uint32_t(&w)[R][4]) {
+#pragma unroll
+        for (int t = 0; t < R; ++t) {
+          const int row = rowb + (pass * R + t) * RPI;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) w[t][k] = 0u;
+          if (side != nullptr && !part && row < M && col < p.N)
+            load_row<4>(side + row * lds_, col, p.N, side_vec, w[t]);
+        }
+      };
+      auto stage = [&](int band) {
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          const int r = half * 16 + l16;
+#pragma unroll
+          for (int j = 0; j < NI; ++j) {
+            const int c = 4 * j + lq;
+            *(f32x4*)(stg + ((r * CHF + (c ^ ((c >> 3) & 1) ^ (r & 7))) << 4)) =
+                acc[2 * band + half][j];
+          }
+        }
+      };
+      uint32_t w[R][4], w_next[R][4];
+      fetch(0, w);
+#pragma unroll 1
+      for (int pass = 0; pass < (MI / 2) * PASSES; ++pass) {
+        if (pass % PASSES == 0) {
+          switch (pass / PASSES) {
+            case 0: stage(0); break;
+            case 1: stage(1); break;
+            case 2: if constexpr (MI > 4) stage(2); break;
+            default: if constexpr (MI > 4) stage(3); break;
+          }
+        }
+        if (pass + 1 < (MI / 2) * PASSES) fetch(pass + 1, w_next);
+        float v[R][8];
+#pragma unroll
+        for (int t = 0; t < R; ++t) {
+          const int r = (pass % PASSES * R + t) * RPI + rl;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int c = 2 * cc + h;
+            const f32x4 x = *(const f32x4*)(stg + ((r * CHF + (c ^ ((c >> 3) & 1) ^ (r & 7))) << 4));
+#pragma unroll
+            for (int k = 0; k < 4; ++k) v[t][4 * h + k] = x[k];
+          }
+        }
+        if (part) {
+          // the part's FP32 partial tile, row-major TM x TN (elements outside
+          // D are skipped: nothing reads them)
+          float* part_ws = p.ws + (size_t)(split * p.tiles + u % p.tiles) * (TM * TN) +
+                           wn * WTN + cc * 8;
+#pragma unroll
+          for (int t = 0; t < R; ++t) {
+            const int r = wm * WTM + rl + (pass * R + t) * RPI;
+            if (m0 + r < M && col < p.N) {
+              *(f32x4*)(part_ws + r * TN) = (f32x4){v[t][0], v[t][1], v[t][2], v[t][3]};
+              *(f32x4*)(part_ws + r * TN + 4) = (f32x4){v[t][4], v[t][5], v[t][6], v[t][7]};
+            }
+          }
+        } else if (ep.grad) {
+          apply_slope<T>(ep.act, v, w);
+        } else {
+#pragma unroll
+          for (int t = 0; t < R; ++t)
+#pragma unroll
+            for (int k = 0; k < 8; ++k) v[t][k] += unpack<T>(bias[k >> 1], k & 1);
+          if (ep.z != nullptr) {
+#pragma unroll
+            for (int t = 0; t < R; ++t) {
+              const int row = rowb + (pass * R + t) * RPI;
+              uint32_t o[4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k) o[k] = pack2<T>(v[t][2 * k], v[t][2 * k + 1]);
+              if (row < M && col < p.N)
+                store_row<4>(ep.z + (int64_t)row * ep.ldz, col, p.N, ep.z_vec, o);
+            }
+          }
+          apply_act(ep.act, v);
+          if (ep.res != nullptr) {
+#pragma unroll
+            for (int t = 0; t < R; ++t)
+#pragma unroll
+              for (int k = 0; k < 8; ++k) v[t][k] += unpack<T>(w[t][k >> 1], k & 1);
+          }
+        }
+#pragma unroll
+        for (int t = 0; t < R; ++t) {
+          const int row = rowb + (pass * R + t) * RPI;
+          uint32_t o[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) o[k] = pack2<T>(v[t][2 * k], v[t][2 * k + 1]);
+          if (!part && row < M && col < p.N)
+            store_row<4>(gD + (int64_t)row * p.ldd, col, p.N, p.d_vec, o);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) w[t][k] = w_next[t][k];
+        }
+      }
+      wait_lds_barrier();
       continue;
     }
 
@@ -454,7 +701,7 @@ __global__ __launch_bounds__(THREADS) void gemm_kernel(Params p) {
         }
       }
       __builtin_amdgcn_sched_barrier(0);
-      const int row0 = m0 + wm * WTM + band * 32;
+      const int rowb = m0 + wm * WTM + band * 32;
       const int col0 = n0 + wn * WTN;
       const int cc = lane % CH;
       u32x4 r[NR];
@@ -471,16 +718,16 @@ __global__ __launch_bounds__(THREADS) void gemm_kernel(Params p) {
 #pragma unroll
         for (int t = 0; t < NR; ++t) {
           const int rr = t * RPI + lane / CH;
-          __builtin_nontemporal_store(r[t], (u32x4*)(p.D + (int64_t)(row0 + rr) * p.ldd + col0 + cc * 8));
+          __builtin_nontemporal_store(r[t], (u32x4*)(gD + (int64_t)(rowb + rr) * p.ldd + col0 + cc * 8));
         }
       } else {
 #pragma unroll
         for (int t = 0; t < NR; ++t) {
           const int rr = t * RPI + lane / CH;
-          const int row = row0 + rr;
+          const int row = rowb + rr;
           const int col = col0 + cc * 8;
-          if (row < p.M && col < p.N) {
-            uint16_t* dst = p.D + (int64_t)row * p.ldd + col;
+          if (row < M && col < p.N) {
+            uint16_t* dst = gD + (int64_t)row * p.ldd + col;
             if (p.d_vec && col + 8 <= p.N) {
               __builtin_nontemporal_store(r[t], (u32x4*)dst);
             } else {
@@ -496,32 +743,6 @@ __global__ __launch_bounds__(THREADS) void gemm_kernel(Params p) {
     // staging reads done before the next tile refills the ring; the stores
     // drain while the next tile's first loads are in flight
     wait_lds_barrier();
-  }
-}
-
-// Copy of a rows x cols matrix of 16-bit elements (any leading dimension,
-// 2-byte alignment) into a dense, 16-byte aligned rows x dcols matrix
-// (dcols = cols rounded up to 8), zero-filling columns cols .. dcols-1: the
-// layout the tiled kernel's 16-byte chunk loads need.  Each thread handles
-// 8-element chunks of the destination, striding over the grid.
-constexpr int64_t REPACK_MAX_BLOCKS = 1 << 16;
-__global__ __launch_bounds__(256) void repack(const uint16_t* __restrict__ src, int64_t rows,
-                                              int64_t cols, int64_t ld, uint16_t* __restrict__ dst,
-                                              int64_t dcols) {
-  const int64_t chunks = dcols / 8, total = rows * chunks;
-  const int64_t stride = (int64_t)gridDim.x * blockDim.x;
-  for (int64_t gid = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; gid < total; gid += stride) {
-    const int64_t r = gid / chunks;
-    const int64_t c0 = (gid % chunks) * 8;
-    const uint16_t* s = src + r * ld + c0;
-    uint32_t w[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const uint32_t lo = c0 + 2 * e < cols ? s[2 * e] : 0u;
-      const uint32_t hi = c0 + 2 * e + 1 < cols ? s[2 * e + 1] : 0u;
-      w[e] = lo | (hi << 16);
-    }
-    *(u32x4*)(dst + r * dcols + c0) = (u32x4){w[0], w[1], w[2], w[3]};
   }
 }
 

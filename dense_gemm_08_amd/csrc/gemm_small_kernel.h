@@ -46,7 +46,11 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "cdna_ops.h"
+#include "epilogue.h"
+#include "groups.h"
 #include "tile_config.h"
 #include "tile_sched.h"
 
@@ -66,6 +70,13 @@ struct SmallParams {
   int tiles_m, tiles_n;  // tiles of the launch's shape in M and N
   int num_xcds;          // XCDs of the device, for the tile order
   int d_vec;     // D rows are 8-byte aligned (4-element stores allowed)
+};
+
+// The products of a layer (layer.hip): the epilogue (epilogue.h) and the row
+// groups (groups.h).
+struct SmallLayerParams : SmallParams {
+  Epilogue e;
+  Groups g;
 };
 
 // LDS position of row k of a chunk's A @ B tile (64 rows of 32 bytes): the
@@ -90,9 +101,13 @@ __device__ __forceinline__ f32x4 mfma16_chain<__bf16>(f32x4 c, u32x4 b, u32x4 a)
                                                   __builtin_bit_cast(bf16x8, a), c, 0, 0, 0);
 }
 
-// TMB x TNB blocks of 16 x 16 per tile (A @ B: one).
-template <typename T, int LAYOUT, int TMB, int TNB>
-__global__ __launch_bounds__(SMALL_THREADS) void gemm_small(SmallParams p) {
+// TMB x TNB blocks of 16 x 16 per tile (A @ B: one).  EPI: the epilogue of a
+// layer's product on the summed blocks.  GROUP: a matrix B for each group of
+// rows; the launch holds as many workgroups as there can be tiles, and those
+// beyond the tiles there are leave at once.
+template <typename T, int LAYOUT, int TMB, int TNB, bool EPI = false, bool GROUP = false>
+__global__ __launch_bounds__(SMALL_THREADS) void gemm_small(
+    std::conditional_t<EPI || GROUP, SmallLayerParams, SmallParams> p) {
   static_assert(LAYOUT == NT || (TMB == 1 && TNB == 1), "A @ B takes 16 x 16 tiles");
   // Chunks in flight per wave.  Two (72 KiB of LDS per workgroup with 16 x
   // 16 tiles, so two workgroups fit a CU) measured faster than four (136
@@ -117,11 +132,26 @@ __global__ __launch_bounds__(SMALL_THREADS) void gemm_small(SmallParams p) {
   // a column strip, which read the same rows of B, run on one XCD (with one
   // tile row: consecutive strips of B per XCD); A @ B row by row, so that
   // the four tiles side by side that share B's 128-byte lines run on one XCD.
-  const int tile = xcd_slot((int)blockIdx.x, (int)gridDim.x, p.num_xcds);
-  const int tm = LAYOUT == NT ? tile % p.tiles_m : tile / p.tiles_n;
-  const int tn = LAYOUT == NT ? tile / p.tiles_m : tile % p.tiles_n;
-  const int m0 = tm * TR, n0 = tn * TC;
-  const int vm = min(TR, p.M - m0), vn = min(TC, p.N - n0);
+  // With groups, tiles are numbered group by group, each group in this order.
+  int tile, tiles_m = p.tiles_m, row0 = 0, M = p.M;
+  const uint16_t* gB = p.B;
+  [[maybe_unused]] int group = 0;
+  if constexpr (GROUP) {
+    GroupTile t;
+    if (!find_tile(p.g, (int)blockIdx.x, p.num_xcds, TR, p.tiles_n, &t)) return;
+    tile = t.tile;
+    group = t.group;
+    row0 = t.beg;
+    M = t.end;
+    tiles_m = (M - row0 + TR - 1) / TR;
+    gB += group * p.g.stride;
+  } else {
+    tile = xcd_slot((int)blockIdx.x, (int)gridDim.x, p.num_xcds);
+  }
+  const int tm = LAYOUT == NT ? tile % tiles_m : tile / p.tiles_n;
+  const int tn = LAYOUT == NT ? tile / tiles_m : tile % p.tiles_n;
+  const int m0 = row0 + tm * TR, n0 = tn * TC;
+  const int vm = min(TR, M - m0), vn = min(TC, p.N - n0);
 
   // Loads: descriptors over the tile's valid rows and columns [0, K8).
   // Load instruction i of an operand fills rows 8 i .. 8 i + 7 of its TR
@@ -130,7 +160,7 @@ __global__ __launch_bounds__(SMALL_THREADS) void gemm_small(SmallParams p) {
   // or N and chunks at or past K8 get an offset past the range: zeros.
   const i32x4 ra = make_rsrc((uint64_t)(uintptr_t)(p.A + (int64_t)m0 * p.lda),
                              (uint32_t)(((vm - 1) * p.lda + p.K8) * 2));
-  const i32x4 rb = make_rsrc((uint64_t)(uintptr_t)(p.B + (int64_t)n0 * p.ldb),
+  const i32x4 rb = make_rsrc((uint64_t)(uintptr_t)(gB + (int64_t)n0 * p.ldb),
                              (uint32_t)(((vn - 1) * p.ldb + p.K8) * 2));
   uint32_t aoff[2 * TMB], boff[2 * TNB];
   int kca[2 * TMB], kcb[2 * TNB];
@@ -180,7 +210,7 @@ __global__ __launch_bounds__(SMALL_THREADS) void gemm_small(SmallParams p) {
       // load takes
       const int k0 = c * 64;
       const int rows = min(64, p.K - k0);
-      const uint64_t a = (uint64_t)(uintptr_t)(p.B + (int64_t)k0 * p.ldb + n0);
+      const uint64_t a = (uint64_t)(uintptr_t)(gB + (int64_t)k0 * p.ldb + n0);
       i32x4 rbn = make_rsrc(a, rows > 0 ? (uint32_t)(((rows - 1) * p.ldb + (p.N8 - n0)) * 2) : 0u);
 #pragma unroll
       for (int e = 0; e < 4; ++e) rbn[e] = __builtin_amdgcn_readfirstlane(rbn[e]);
@@ -272,7 +302,34 @@ __global__ __launch_bounds__(SMALL_THREADS) void gemm_small(SmallParams p) {
   for (int w = 1; w < SMALL_WAVES; ++w) s += part[w][wave][lane];
   const int row = m0 + SMALL_TILE * (wave / TNB) + l16;
   const int col = n0 + SMALL_TILE * (wave % TNB) + 4 * lq;
-  if (row >= p.M || col >= p.N) return;
+  if (row >= M || col >= p.N) return;
+  if constexpr (EPI) {
+    const Epilogue& ep = p.e;
+    float x[1][4] = {{s[0], s[1], s[2], s[3]}};
+    uint32_t w[1][2] = {{0u, 0u}};
+    if (ep.grad) {
+      load_row<2>(ep.z + (int64_t)row * ep.ldz, col, p.N, ep.z_vec, w[0]);
+      apply_slope<T>(ep.act, x, w);
+    } else {
+      if (ep.bias != nullptr) {
+        load_row<2>(ep.bias + group * ep.bias_stride, col, p.N, ep.bias_vec, w[0]);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) x[0][k] += unpack<T>(w[0][k >> 1], k & 1);
+      }
+      if (ep.z != nullptr) {
+        const uint32_t o[2] = {pack2<T>(x[0][0], x[0][1]), pack2<T>(x[0][2], x[0][3])};
+        store_row<2>(ep.z + (int64_t)row * ep.ldz, col, p.N, ep.z_vec, o);
+      }
+      apply_act(ep.act, x);
+      if (ep.res != nullptr) {
+        load_row<2>(ep.res + (int64_t)row * ep.ldr, col, p.N, ep.res_vec, w[0]);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) x[0][k] += unpack<T>(w[0][k >> 1], k & 1);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) s[k] = x[0][k];
+  }
   u32x2 v;
   v[0] = pack2<T>(s[0], s[1]);
   v[1] = pack2<T>(s[2], s[3]);

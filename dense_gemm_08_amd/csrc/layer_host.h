@@ -1,0 +1,103 @@
+// layer_host.h -- what the host sides of a layer's products share
+// (layer.hip, grouped.hip, tn.hip): the call's arguments, and the kernel
+// parameters made from them.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "dense_gemm.h"
+#include "gemm_kernel.h"
+#include "gemm_small_kernel.h"
+#include "plan_layer.h"
+
+namespace dg {
+
+dense_gemm_status device_topology(int* cus, int* xcds);
+
+// Enqueues a copy of `count` matrices of rows x cols 16-bit elements, ld
+// between their rows and stride between the matrices, into dense zero-padded
+// ones (repack_groups in layer.hip); returns the copies' leading dimension.
+int64_t enqueue_repack(const void* src, int64_t count, int64_t rows, int64_t cols, int64_t ld,
+                       int64_t stride, void* dst, hipStream_t stream);
+
+inline dense_gemm_status launched() {
+  return hipGetLastError() == hipSuccess ? DENSE_GEMM_OK : DENSE_GEMM_LAUNCH_FAILED;
+}
+
+// Rows of p, ld elements apart, that an access of `bytes` (a power of two)
+// may touch at multiples of its size.
+inline int wide(const void* p, int64_t ld, int bytes) {
+  return ((uintptr_t)p & (bytes - 1)) == 0 && ((ld * 2) & (bytes - 1)) == 0;
+}
+
+inline Epilogue device_epilogue(const dense_gemm_epilogue* e, int bytes) {
+  Epilogue d = {};
+  if (e == nullptr) return d;
+  d.bias = (const uint16_t*)e->bias;
+  d.bias_stride = e->bias != nullptr ? e->bias_stride : 0;
+  d.res = (const uint16_t*)e->residual;
+  d.z = (uint16_t*)e->preact;
+  d.ldr = (int)e->ldr;
+  d.ldz = (int)e->ldz;
+  d.act = e->act;
+  d.grad = e->grad;
+  d.bias_vec = wide(e->bias, e->bias_stride, bytes);
+  d.res_vec = wide(e->residual, e->ldr, bytes);
+  d.z_vec = wide(e->preact, e->ldz, bytes);
+  return d;
+}
+
+// One call's arguments, operands as the kernels read them (after repacks).
+struct LayerCall {
+  int64_t M, N, K;
+  const uint16_t* A;
+  int64_t lda;
+  const uint16_t* B;
+  int64_t ldb;
+  uint16_t* D;
+  int64_t ldd;
+  const dense_gemm_epilogue* e;
+  int cus, xcds;
+  hipStream_t stream;
+};
+
+inline void set_operands(Params& p, const LayerCall& c) {
+  p.A = c.A;
+  p.B = c.B;
+  p.D = c.D;
+  p.M = (int)c.M;
+  p.N = (int)c.N;
+  p.K = (int)c.K;
+  p.lda = (int)c.lda;
+  p.ldb = (int)c.ldb;
+  p.ldd = (int)c.ldd;
+  p.num_xcds = c.xcds;
+  p.d_vec = wide(c.D, c.ldd, 16);
+}
+
+inline SmallLayerParams small_params(const LayerCall& c) {
+  SmallLayerParams p = {};
+  p.A = c.A;
+  p.B = c.B;
+  p.D = c.D;
+  p.M = (int)c.M;
+  p.N = (int)c.N;
+  p.K = (int)c.K;
+  p.K8 = (int)((c.K + 7) & ~(int64_t)7);
+  p.N8 = (int)((c.N + 7) & ~(int64_t)7);
+  p.lda = (int)c.lda;
+  p.ldb = (int)c.ldb;
+  p.ldd = (int)c.ldd;
+  p.num_xcds = c.xcds;
+  p.d_vec = wide(c.D, c.ldd, 8);
+  p.e = device_epilogue(c.e, 8);
+  return p;
+}
+
+// grouped.hip: a call with row groups.
+template <typename T, int LAYOUT>
+dense_gemm_status run_grouped(LayerCall c, const dense_gemm_groups& groups, void* ws,
+                              size_t ws_bytes);
+
+}  // namespace dg

@@ -10,7 +10,10 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "cdna_ops.h"
+#include "epilogue.h"
 #include "tile_sched.h"
 
 namespace dg {
@@ -29,6 +32,18 @@ struct ReduceParams {
   int d_vec;  // D rows are 16-byte aligned (16-byte stores allowed)
 };
 
+// For a layer's products (layer.hip): the epilogue applied to the sums, and
+// for A.T @ B over row groups (`groups` of them; tile t of the order is tile
+// t % (tiles_m * tiles_n) of group t / that, in a D of its own) the column
+// sums of A: each part of a split tile in the first tile column left TM
+// FP32 sums at colsum_ws + (part * tiles + st) * TM.
+struct LayerReduceParams : ReduceParams {
+  Epilogue e;
+  int64_t stride;        // elements between the groups' D
+  const float* colsum_ws;
+  uint16_t* colsum;      // groups x M, or null
+};
+
 // One thread per 8 consecutive columns of a row, RT threads per workgroup:
 // a workgroup covers RT / (TN / 8) rows, a split tile TM * TN / (8 RT)
 // workgroups.  The launch takes RT = 64 (one wave) when 256-thread
@@ -38,15 +53,32 @@ struct ReduceParams {
 // slower on the split products of the M = 8192 sweep).
 template <int TN, int RT, int TM>
 constexpr int reduce_blocks_per_tile() { return TM * TN / (8 * RT); }
-template <typename T, int TN, int RT, int TM>
-__global__ __launch_bounds__(RT) void split_reduce(ReduceParams p) {
+template <typename T, int TN, int RT, int TM, bool LAYER = false>
+__global__ __launch_bounds__(RT) void split_reduce(
+    std::conditional_t<LAYER, LayerReduceParams, ReduceParams> p) {
   constexpr int TPR = TN / 8;      // threads per row
   constexpr int RPW = RT / TPR;    // rows per workgroup
   constexpr int WPT = TM / RPW;    // workgroups per split tile
   static_assert(RT % TPR == 0 && WPT == reduce_blocks_per_tile<TN, RT, TM>(), "whole rows per workgroup");
   const int st = blockIdx.x / WPT;      // split tile (0 .. tiles-1)
   int tm, tn;
-  tile_of_task(p.full_tasks + st, p.tiles_m, p.tiles_n, p.group_m, &tm, &tn);
+  uint16_t* D = p.D;
+  if constexpr (LAYER) {
+    const int per = p.tiles_m * p.tiles_n;
+    const int group = (p.full_tasks + st) / per;
+    tile_of_task(p.full_tasks + st - group * per, p.tiles_m, p.tiles_n, p.group_m, &tm, &tn);
+    D += group * p.stride;
+    if (p.colsum != nullptr && tn == 0 && blockIdx.x % WPT == 0) {
+      for (int c = (int)threadIdx.x; c < TM && tm * TM + c < p.M; c += RT) {
+        float s = 0.0f;
+        for (int k = 0; k < p.splits; ++k)
+          s += p.colsum_ws[((size_t)k * p.tiles + st) * TM + c];
+        p.colsum[(int64_t)group * p.M + tm * TM + c] = (uint16_t)pack2<T>(s, 0.0f);
+      }
+    }
+  } else {
+    tile_of_task(p.full_tasks + st, p.tiles_m, p.tiles_n, p.group_m, &tm, &tn);
+  }
   const int r = (blockIdx.x % WPT) * RPW + (int)threadIdx.x / TPR;
   const int c = ((int)threadIdx.x % TPR) * 8;
   const int row = tm * TM + r;
@@ -80,10 +112,41 @@ __global__ __launch_bounds__(RT) void split_reduce(ReduceParams p) {
       }
     }
   }
+  if constexpr (LAYER) {
+    const Epilogue& ep = p.e;
+    float x[1][8];
+    uint32_t w[1][4] = {{0u, 0u, 0u, 0u}};
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[0][e] = s[e];
+    if (ep.grad) {
+      load_row<4>(ep.z + (int64_t)row * ep.ldz, col, p.N, ep.z_vec, w[0]);
+      apply_slope<T>(ep.act, x, w);
+    } else {
+      if (ep.bias != nullptr) {
+        load_row<4>(ep.bias, col, p.N, ep.bias_vec, w[0]);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[0][e] += unpack<T>(w[0][e >> 1], e & 1);
+      }
+      if (ep.z != nullptr) {
+        uint32_t o[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[e] = pack2<T>(x[0][2 * e], x[0][2 * e + 1]);
+        store_row<4>(ep.z + (int64_t)row * ep.ldz, col, p.N, ep.z_vec, o);
+      }
+      apply_act(ep.act, x);
+      if (ep.res != nullptr) {
+        load_row<4>(ep.res + (int64_t)row * ep.ldr, col, p.N, ep.res_vec, w[0]);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[0][e] += unpack<T>(w[0][e >> 1], e & 1);
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) s[e] = x[0][e];
+  }
   u32x4 v;
 #pragma unroll
   for (int e = 0; e < 4; ++e) v[e] = pack2<T>(s[2 * e], s[2 * e + 1]);
-  uint16_t* dst = p.D + (int64_t)row * p.ldd + col;
+  uint16_t* dst = D + (int64_t)row * p.ldd + col;
   if (p.d_vec && col + 8 <= p.N) {
     __builtin_nontemporal_store(v, (u32x4*)dst);
   } else {
@@ -96,15 +159,17 @@ __global__ __launch_bounds__(RT) void split_reduce(ReduceParams p) {
 // The reduction's launch on `stream`, after the partial tiles' kernel on
 // the same stream (one-wave workgroups where 256-thread ones would not
 // cover the CUs).
-template <typename T, int TN, int TM>
-static inline void enqueue_split_reduce(const ReduceParams& r, int cus, hipStream_t stream) {
+template <typename T, int TN, int TM, typename P>
+static inline void enqueue_split_reduce(const P& r, int cus, hipStream_t stream) {
+  constexpr bool LAYER = std::is_same_v<P, LayerReduceParams>;
   const int64_t wide = r.tiles * (int64_t)reduce_blocks_per_tile<TN, 256, TM>();
   if (wide < cus)
-    hipLaunchKernelGGL((split_reduce<T, TN, 64, TM>),
+    hipLaunchKernelGGL((split_reduce<T, TN, 64, TM, LAYER>),
                        dim3((unsigned)(r.tiles * reduce_blocks_per_tile<TN, 64, TM>())), dim3(64), 0,
                        stream, r);
   else
-    hipLaunchKernelGGL((split_reduce<T, TN, 256, TM>), dim3((unsigned)wide), dim3(256), 0, stream, r);
+    hipLaunchKernelGGL((split_reduce<T, TN, 256, TM, LAYER>), dim3((unsigned)wide), dim3(256), 0,
+                       stream, r);
 }
 
 }  // namespace dg

@@ -7,7 +7,8 @@
 
 namespace dg {
 
-enum Layout { NT = 0, NN = 1 };
+// D = A @ B.T, D = A @ B, and D = A.T @ B (a layer's weight gradient).
+enum Layout { NT = 0, NN = 1, TA = 2 };
 
 constexpr int BM = 256;              // tile rows (M)
 constexpr int BN = 256;              // tile columns (N); A @ B.T also has a 128-wide

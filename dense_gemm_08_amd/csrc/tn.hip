@@ -1,0 +1,131 @@
+// tn.hip -- a layer's weight and bias gradients on the MI355X (gfx950): D =
+// A.T @ B and the column sums of A, for one matrix or one per group of rows
+// (dense_gemm_tn, include/dense_gemm.h).  Host side: the plan (tn_plan in
+// plan_layer.cpp), the launches and the C ABI entry points.  The kernel is
+// the tiled one with layout TA (gemm_kernel.h): A and B both have k as their
+// row, so their tiles are 64 k rows of 512 bytes and both operands' MFMA
+// fragments come from transposing LDS reads.
+#include "layer_host.h"
+#include "split_reduce.h"
+
+namespace dg {
+
+template <typename T, bool GROUP, bool SUMS>
+static dense_gemm_status enqueue_tn(const LayerParams& p, const LayerReduceParams& r, int cus,
+                                    hipStream_t stream) {
+  const dim3 grid((unsigned)(p.num_tasks < cus ? p.num_tasks : cus)), block(THREADS);
+  if (p.splits > 1) {
+    hipLaunchKernelGGL((gemm_kernel<T, TA, true, BN, BM, false, GROUP, SUMS>), grid, block, 0, stream,
+                       p);
+    enqueue_split_reduce<T, BN, BM>(r, cus, stream);
+  } else {
+    hipLaunchKernelGGL((gemm_kernel<T, TA, false, BN, BM, false, GROUP, SUMS>), grid, block, 0, stream,
+                       p);
+  }
+  return launched();
+}
+
+template <typename T>
+static dense_gemm_status run_tn(LayerCall c, void* colsum, const dense_gemm_groups* groups,
+                                void* ws, size_t ws_bytes) {
+  TnPlan tp;
+  const dense_gemm_status st = tn_plan(c.M, c.N, c.K, c.A, c.lda, c.B, c.ldb, groups, c.cus, &tp);
+  if (st != DENSE_GEMM_OK) return st;
+  if (tp.total() > 0) {
+    if (ws == nullptr || ws_bytes < tp.total()) return DENSE_GEMM_WORKSPACE_TOO_SMALL;
+    if (((uintptr_t)ws & 255) != 0) return DENSE_GEMM_MISALIGNED;
+  }
+  char* at = (char*)ws;
+  if (!tp.a_direct) {
+    c.lda = enqueue_repack(c.A, 1, c.K, c.M, c.lda, 0, at, c.stream);
+    c.A = (const uint16_t*)at;
+  }
+  at += tp.a_bytes;
+  if (!tp.b_direct) {
+    c.ldb = enqueue_repack(c.B, 1, c.K, c.N, c.ldb, 0, at, c.stream);
+    c.B = (const uint16_t*)at;
+  }
+  at += tp.b_bytes;
+  LayerParams p = {};
+  set_operands(p, c);
+  p.tiles_m = (int)tp.tiles_m;
+  p.tiles_n = (int)tp.tiles_n;
+  p.group_m = choose_group_m(tp.tiles_m);
+  p.full_tasks = (int)tp.full_tasks;
+  p.tiles = (int)tp.split_tiles;
+  p.splits = (int)tp.splits;
+  p.split_steps = (int)tp.steps;
+  p.num_tasks = (int)(tp.full_tasks + tp.split_tiles * tp.splits);
+  p.colsum = (uint16_t*)colsum;
+  if (tp.splits > 1) {
+    p.ws = (float*)at;
+    p.colsum_ws = (float*)(at + tp.split_bytes);
+  }
+  if (groups != nullptr) {
+    p.g = {(const int32_t*)groups->ends, (int)groups->count, (int)c.K, groups->stride};
+    p.d_vec = p.d_vec && wide(c.D, groups->stride, 16);
+  }
+  LayerReduceParams r = {};
+  (ReduceParams&)r = {p.D, p.ws, p.M, p.N, p.ldd, p.tiles_m, p.tiles_n, p.group_m,
+                      p.full_tasks, p.splits, p.tiles, p.d_vec};
+  r.stride = p.g.stride;
+  r.colsum = p.colsum;
+  r.colsum_ws = p.colsum_ws;
+  if (groups != nullptr)
+    return colsum != nullptr ? enqueue_tn<T, true, true>(p, r, c.cus, c.stream)
+                             : enqueue_tn<T, true, false>(p, r, c.cus, c.stream);
+  return colsum != nullptr ? enqueue_tn<T, false, true>(p, r, c.cus, c.stream)
+                           : enqueue_tn<T, false, false>(p, r, c.cus, c.stream);
+}
+
+}  // namespace dg
+
+using namespace dg;
+
+extern "C" {
+
+dense_gemm_status dense_gemm_tn(int fmt, int64_t M, int64_t N, int64_t K, const void* A,
+                                int64_t lda, const void* B, int64_t ldb, void* D, int64_t ldd,
+                                void* colsum, const dense_gemm_groups* groups, void* workspace,
+                                size_t workspace_bytes, hipStream_t stream) {
+  bool done;
+  dense_gemm_status st = tn_validate(fmt, M, N, K, A, lda, B, ldb, D, ldd, colsum, groups, &done);
+  if (st != DENSE_GEMM_OK || done) return st;
+  LayerCall c = {M, N, K, (const uint16_t*)A, lda, (const uint16_t*)B, ldb, (uint16_t*)D, ldd,
+                 nullptr, 0, 1, stream};
+  st = device_topology(&c.cus, &c.xcds);
+  if (st != DENSE_GEMM_OK) return st;
+  return fmt == DENSE_GEMM_BF16 ? run_tn<__bf16>(c, colsum, groups, workspace, workspace_bytes)
+                                : run_tn<_Float16>(c, colsum, groups, workspace, workspace_bytes);
+}
+
+dense_gemm_status dense_gemm_tn_workspace_size(int64_t M, int64_t N, int64_t K, const void* A,
+                                               int64_t lda, const void* B, int64_t ldb,
+                                               const dense_gemm_groups* groups, int64_t num_cus,
+                                               size_t* bytes) {
+  if (bytes == nullptr || num_cus < 0) return DENSE_GEMM_BAD_ARG;
+  const void* any = (const void*)(uintptr_t)16;
+  dense_gemm_groups g = {any, 0, 0};
+  if (groups != nullptr) {
+    g.count = groups->count;
+    // (the stride concerns D alone: any that keeps the outputs apart will do)
+    if (M > 0 && N > 0 && M < kMaxDim && N < kMaxDim) g.stride = M * N;
+  }
+  bool done;
+  dense_gemm_status st = tn_validate(DENSE_GEMM_F16, M, N, K, A, lda, B, ldb, any, N, nullptr,
+                                     groups != nullptr ? &g : nullptr, &done);
+  if (st != DENSE_GEMM_OK) return st;
+  *bytes = 0;
+  if (done) return DENSE_GEMM_OK;
+  int cus = (int)(num_cus < kMaxDim ? num_cus : kMaxDim - 1), xcds;
+  if (num_cus == 0) {
+    st = device_topology(&cus, &xcds);
+    if (st != DENSE_GEMM_OK) return st;
+  }
+  TnPlan tp;
+  st = tn_plan(M, N, K, A, lda, B, ldb, groups != nullptr ? &g : nullptr, cus, &tp);
+  if (st == DENSE_GEMM_OK) *bytes = tp.total();
+  return st;
+}
+
+}  // extern "C"

@@ -312,6 +312,119 @@ dense_gemm_status gemm_nt_e4m3_mx_ex(int64_t M, int64_t N, int64_t K, const void
                                      void* workspace, size_t workspace_bytes,
                                      hipStream_t stream);
 
+/* ---- the products of a layer ---------------------------------------------
+ * What a transformer's dense and expert layers need around the product: bias,
+ * activation and residual applied before the one rounding, the gradients, and
+ * one weight matrix per group of rows (a mixture of experts).  All of them
+ * take the caller's workspace, as dense_gemm_ex does (the queries give its
+ * size, often 0; the same rules hold for it), and allocate nothing.  Layouts,
+ * alignment, ownership, stream order, reproducibility and errors are those
+ * stated at the top of this file: an operand that the 16-byte loads cannot
+ * read in place is repacked into the workspace, every other matrix or vector
+ * needs only the alignment of its elements.
+ *
+ * Activations, computed in FP32 (F is the standard normal distribution
+ * function, s(w) = 1 / (1 + exp(-w))); at infinite z they and their
+ * derivatives take their limits, and NaN gives NaN:
+ *   RELU max(z, 0), derivative 0 at 0;  GELU z F(z);  SILU z s(z);
+ *   GELU_TANH z s(2 u) with u = sqrt(2 / pi) (z + 0.044715 z^3). */
+typedef enum dense_gemm_act {
+  DENSE_GEMM_ACT_NONE = 0,
+  DENSE_GEMM_ACT_RELU = 1,
+  DENSE_GEMM_ACT_GELU = 2,
+  DENSE_GEMM_ACT_GELU_TANH = 3,
+  DENSE_GEMM_ACT_SILU = 4
+} dense_gemm_act;
+
+/* The element type of dense_gemm_tn's operands and results. */
+typedef enum dense_gemm_fmt { DENSE_GEMM_F16 = 0, DENSE_GEMM_BF16 = 1 } dense_gemm_fmt;
+
+/* What dense_gemm_layer does to the accumulated product P.
+ *   grad 0   Z = P + bias,  D = act(Z) + residual
+ *   grad 1   D = P * act'(Z)
+ * bias       N values added to every row, or null.  With groups, group g's
+ *            start at bias + g * bias_stride elements.
+ * residual   M x N, leading dimension ldr, or null.  It may be D itself
+ *            (same pointer and leading dimension).
+ * preact     Z, M x N with leading dimension ldz.  grad 0: receives Z rounded
+ *            to the output type, or null; grad 1: read, and may be D itself.
+ * act        a dense_gemm_act; grad 1 takes any but NONE, and no bias and no
+ *            residual (DENSE_GEMM_BAD_ARG).
+ * Z, the activation and the residual's sum are formed in FP32 from the
+ * unrounded product; D is rounded once.  bias, residual and preact have the
+ * type of D. */
+typedef struct dense_gemm_epilogue {
+  const void* bias;
+  int64_t bias_stride;
+  const void* residual;
+  int64_t ldr;
+  void* preact;
+  int64_t ldz;
+  int32_t act;
+  int32_t grad;
+} dense_gemm_epilogue;
+
+/* Rows sorted into groups.  ends: `count` int32 values on the device (4-byte
+ * aligned, not decreasing): group g holds rows ends[g - 1] .. ends[g] - 1,
+ * group 0 from row 0.  Groups may be empty.  stride: elements between the
+ * matrices of neighbouring groups: of B for dense_gemm_layer (0: one matrix
+ * for all), of D for dense_gemm_tn.  The ends are read by the kernels, after
+ * the work before the call on `stream`; the host never sees them.  Each is
+ * clamped to the number of rows, so no array of ends leads outside the
+ * operands; where the ends decrease, the rows that several groups name hold
+ * one of those groups' results or another, and rows may be left out. */
+typedef struct dense_gemm_groups {
+  const void* ends;
+  int64_t count;
+  int64_t stride;
+} dense_gemm_groups;
+
+/* The product `op` (a dense_gemm_op) with an epilogue (null: none) and, where
+ * groups is not null, one matrix B for each group of rows:
+ *     D[i] = epilogue(A[i] @ Bhat_g),  i in group g
+ * with B_g = B + g * groups->stride, N x K or K x N by op, leading dimension
+ * ldb.  M is the number of rows of A, D, residual and preact; rows that no
+ * group holds (those from ends[count - 1] on) are neither read nor written.
+ * count 0 does nothing.  Without groups the plan is that of dense_gemm_ex
+ * without options; with groups it depends on M, N, K, the count and the
+ * device alone, not on the ends.  Fewer than 2^31 output tiles are accepted
+ * (DENSE_GEMM_TOO_LARGE), counting one more row of tiles per group. */
+dense_gemm_status dense_gemm_layer(int op, int64_t M, int64_t N, int64_t K, const void* A,
+                                   int64_t lda, const void* B, int64_t ldb, void* D, int64_t ldd,
+                                   const dense_gemm_epilogue* epilogue,
+                                   const dense_gemm_groups* groups, void* workspace,
+                                   size_t workspace_bytes, hipStream_t stream);
+
+/* Bytes of workspace dense_gemm_layer needs (groups may be null; its `ends`
+ * is not read).  num_cus as for dense_gemm_workspace_size. */
+dense_gemm_status dense_gemm_layer_workspace_size(int op, int64_t M, int64_t N, int64_t K,
+                                                  const void* A, int64_t lda, const void* B,
+                                                  int64_t ldb, const dense_gemm_groups* groups,
+                                                  int64_t num_cus, size_t* bytes);
+
+/* A layer's weight and bias gradients: D = A.T @ B, and the sums of A's
+ * columns, over K rows (tokens):
+ *     D[i][j] = round( sum_{k < K} A[k][i] * B[k][j] )
+ *     colsum[i] = round( sum_{k < K} A[k][i] )
+ * fmt: a dense_gemm_fmt.  A is K x M, element (k, i) at A[k * lda + i]; B is
+ * K x N, element (k, j) at B[k * ldb + j]; D is M x N; colsum is M values or
+ * null (it needs N > 0: DENSE_GEMM_BAD_ARG).  Sums are accumulated in FP32 in
+ * a fixed order.  With groups, the sums of group g run over its rows alone
+ * and go to D + g * groups->stride and colsum + g * M (an empty group's are
+ * zero); the stride must keep the outputs apart (DENSE_GEMM_BAD_LD).  Rows
+ * that no group holds contribute to nothing. */
+dense_gemm_status dense_gemm_tn(int fmt, int64_t M, int64_t N, int64_t K, const void* A,
+                                int64_t lda, const void* B, int64_t ldb, void* D, int64_t ldd,
+                                void* colsum, const dense_gemm_groups* groups, void* workspace,
+                                size_t workspace_bytes, hipStream_t stream);
+
+/* Bytes of workspace dense_gemm_tn needs: repacked operands, and FP32 partial
+ * tiles (with their column sums) where K is split.  `ends` is not read. */
+dense_gemm_status dense_gemm_tn_workspace_size(int64_t M, int64_t N, int64_t K, const void* A,
+                                               int64_t lda, const void* B, int64_t ldb,
+                                               const dense_gemm_groups* groups, int64_t num_cus,
+                                               size_t* bytes);
+
 /* A static, human-readable name for a status code (never NULL). */
 const char* dense_gemm_status_string(int status);
 

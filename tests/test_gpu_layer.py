@@ -1,0 +1,624 @@
+"""The layer products (fused epilogue, activation gradient, weight and bias
+gradient, row groups) on the GPU against plain forms in 64 bits
+(tests/_layer.py, which derives the bounds)."""
+import itertools
+
+import pytest
+import torch
+
+import dense_gemm_08_amd as dg
+from dense_gemm_08_amd import binding
+from tests import _layer as L
+
+pytestmark = pytest.mark.gpu
+
+ACTS = ("none", "relu", "gelu", "gelu_tanh", "silu")
+NT_F = {"nt": dg.gemm_nt_fused, "nn": dg.gemm_nn_fused}
+DACT = {"nt": dg.gemm_nt_dact, "nn": dg.gemm_nn_dact}
+GRP = {"nt": dg.gemm_nt_grouped, "nn": dg.gemm_nn_grouped}
+GRP_DACT = {"nt": dg.gemm_nt_grouped_dact, "nn": dg.gemm_nn_grouped_dact}
+CANARY = 77.0
+
+
+def rand(gen, *shape, dt, sigma=1.0, pad=0, off=0):
+    """Normal values; with ``pad`` the rows lie that many elements further
+    apart, with ``off`` the matrix starts that many elements into its
+    buffer (the rest of which holds NaN)."""
+    if not pad and not off:
+        return (torch.randn(shape, generator=gen, device="cuda") * sigma).to(dt)
+    rows = 1
+    for s in shape[:-1]:
+        rows *= s
+    ld = shape[-1] + pad
+    buf = torch.full((off + rows * ld,), float("nan"), dtype=dt, device="cuda")
+    t = buf[off:].view(*shape[:-1], ld)[..., :shape[-1]]
+    t.copy_(torch.randn(shape, generator=gen, device="cuda") * sigma)
+    return t
+
+
+def canary(*shape, dt, pad=0):
+    buf = torch.full(shape[:-1] + (shape[-1] + pad,), CANARY, dtype=dt, device="cuda")
+    return buf, buf[..., :shape[-1]]
+
+
+def padding_untouched(buf, n):
+    assert bool((buf[..., n:] == CANARY).all())
+
+
+def generator(seed):
+    return torch.Generator(device="cuda").manual_seed(seed)
+
+
+# sizes of the small-output kernel's tile shapes, of every tile of the tiled
+# kernel (128 and 256 rows, 128 and 256 columns), of split-K (a few tiles, long
+# K; a last partial wave) and of the edges between them
+FUSED = [
+    (1, 8, 8), (1, 1, 1), (7, 40, 64), (1, 4096, 2048), (16, 520, 1000), (33, 256, 320),
+    (64, 2048, 512), (128, 128, 4096), (128, 16384, 256), (130, 120, 2048), (100, 16000, 640),
+    (300, 264, 200), (257, 513, 72), (256, 128, 8192), (513, 255, 4100), (1000, 1001, 130),
+    (4096, 4352, 512),
+]
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("layout", ["nt", "nn"])
+@pytest.mark.parametrize("M,N,K", FUSED)
+def test_fused_full_check(M, N, K, layout, dtype):
+    dt = L.GEN[dtype]
+    gen = generator(M * 7 + N * 3 + K)
+    A = rand(gen, M, K, dt=dt)
+    B = rand(gen, *((N, K) if layout == "nt" else (K, N)), dt=dt, sigma=K ** -0.5)
+    bias, res = rand(gen, N, dt=dt), rand(gen, M, N, dt=dt)
+    # each activation once, the other operands in turn
+    for n, act in enumerate(ACTS):
+        b = bias if n % 2 == 0 else None
+        r = res if n in (0, 3, 4) else None
+        Z = torch.empty((M, N), dtype=dt, device="cuda") if n in (1, 2, 4) else None
+        D = NT_F[layout](A, B, bias=b, act=act, residual=r, preact=Z)
+        L.check_forward(D, Z, A, B, layout, b, act, r, "%s %s %dx%dx%d %s" % (
+            layout, dtype, M, N, K, act))
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("layout", ["nt", "nn"])
+@pytest.mark.parametrize("M,N,K", FUSED)
+def test_dact_full_check(M, N, K, layout, dtype):
+    dt = L.GEN[dtype]
+    gen = generator(M * 5 + N + K * 11)
+    A = rand(gen, M, K, dt=dt)
+    B = rand(gen, *((N, K) if layout == "nt" else (K, N)), dt=dt, sigma=K ** -0.5)
+    Z = rand(gen, M, N, dt=dt, sigma=2.0)
+    for act in ACTS[1:]:
+        D = DACT[layout](A, B, Z, act)
+        L.check_dact(D, A, B, layout, Z, act, "%s %s %dx%dx%d %s" % (layout, dtype, M, N, K, act))
+
+
+STRIDED = [  # (M, N, K, pads of A, B, D, residual, Z; offsets of A, B)
+    (70, 90, 100, 3, 5, 1, 7, 2, 0, 0), (300, 520, 264, 8, 16, 8, 24, 8, 0, 0),
+    (300, 520, 264, 0, 0, 3, 0, 1, 1, 3), (16, 1000, 333, 0, 0, 0, 5, 0, 0, 1),
+    (129, 300, 4097, 0, 1, 0, 0, 8, 5, 0),
+]
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("layout", ["nt", "nn"])
+@pytest.mark.parametrize("case", STRIDED, ids=lambda c: "_".join(map(str, c)))
+def test_fused_strides_offsets_and_untouched_padding(case, layout, dtype):
+    M, N, K, pa, pb, pd, pr, pz, oa, ob = case
+    dt = L.GEN[dtype]
+    gen = generator(sum(case))
+    A = rand(gen, M, K, dt=dt, pad=pa, off=oa)
+    B = rand(gen, *((N, K) if layout == "nt" else (K, N)), dt=dt, sigma=K ** -0.5, pad=pb, off=ob)
+    bias = rand(gen, N + 1, dt=dt)[1:]
+    R = rand(gen, M, N, dt=dt, pad=pr)
+    dbuf, D = canary(M, N, dt=dt, pad=pd)
+    zbuf, Z = canary(M, N, dt=dt, pad=pz)
+    out = NT_F[layout](A, B, bias=bias, act="gelu", residual=R, preact=Z, D=D)
+    assert out is D
+    L.check_forward(D, Z, A, B, layout, bias, "gelu", R, str(case))
+    padding_untouched(dbuf, N)
+    padding_untouched(zbuf, N)
+    E = rand(gen, M, N, dt=dt, pad=pr)
+    dbuf.fill_(CANARY)
+    DACT[layout](A, B, E, "silu", D=D)
+    L.check_dact(D, A, B, layout, E, "silu", str(case))
+    padding_untouched(dbuf, N)
+
+
+@pytest.mark.parametrize("layout", ["nt", "nn"])
+@pytest.mark.parametrize("M,N,K", [(9, 64, 128), (300, 300, 96), (128, 256, 8192)])
+def test_residual_and_preact_in_place(M, N, K, layout):
+    dt = torch.bfloat16
+    gen = generator(5)
+    A = rand(gen, M, K, dt=dt)
+    B = rand(gen, *((N, K) if layout == "nt" else (K, N)), dt=dt, sigma=K ** -0.5)
+    R = rand(gen, M, N, dt=dt)
+    D = R.clone()
+    NT_F[layout](A, B, act="silu", residual=D, D=D)
+    assert torch.equal(D, NT_F[layout](A, B, act="silu", residual=R))
+    D = R.clone()
+    DACT[layout](A, B, D, "gelu", D=D)
+    assert torch.equal(D, DACT[layout](A, B, R, "gelu"))
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_no_epilogue_gives_the_plain_product_bits(dtype):
+    dt = L.GEN[dtype]
+    gen = generator(12)
+    plain = {("nt", "f16"): dg.gemm_nt_f16, ("nn", "f16"): dg.gemm_nn_f16,
+             ("nt", "bf16"): dg.gemm_nt_bf16, ("nn", "bf16"): dg.gemm_nn_bf16}
+    for layout, (M, N, K) in itertools.product(("nt", "nn"), [(5, 100, 64), (120, 700, 1000),
+                                                              (700, 600, 3001), (256, 128, 4096)]):
+        A = rand(gen, M, K, dt=dt)
+        B = rand(gen, *((N, K) if layout == "nt" else (K, N)), dt=dt)
+        assert torch.equal(NT_F[layout](A, B), plain[(layout, dtype)](A, B)), (layout, M, N, K)
+
+
+@pytest.mark.parametrize("layout", ["nt", "nn"])
+@pytest.mark.parametrize("M", [3, 300])
+def test_zero_k_and_empty_outputs(M, layout):
+    dt = torch.float16
+    gen = generator(1)
+    N = 40
+    A = torch.empty((M, 0), dtype=dt, device="cuda")
+    B = torch.empty((N, 0) if layout == "nt" else (0, N), dtype=dt, device="cuda")
+    bias, R = rand(gen, N, dt=dt), rand(gen, M, N, dt=dt)
+    D = NT_F[layout](A, B, bias=bias, act="silu", residual=R)
+    z = bias.double().expand(M, N)
+    d = L.act64(z, "silu") + R.double()
+    L.assert_close(D, d, 2.0 ** -14 + L.rounding(d, dt), "K = 0")
+    assert NT_F[layout](torch.empty((0, 8), dtype=dt, device="cuda"),
+                        torch.empty((N, 8) if layout == "nt" else (8, N), dtype=dt,
+                                    device="cuda")).shape == (0, N)
+    assert torch.equal(DACT[layout](A, B, R, "relu"), torch.zeros_like(R))
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("M", [4, 300])
+def test_activations_at_special_values(M, dtype):
+    # one K value of 1: Z is A's value exactly
+    dt = L.GEN[dtype]
+    inf, nan = float("inf"), float("nan")
+    big = torch.finfo(dt).max
+    z = torch.tensor([0.0, -0.0, inf, -inf, nan, big, -big, 1e-4, -1e-4, 20.0, -20.0, 60000.0,
+                      -60000.0, torch.finfo(dt).tiny, 5.0, -5.0], dtype=dt, device="cuda")
+    N = z.numel()
+    A = torch.ones((M, 1), dtype=dt, device="cuda")
+    limits = {"relu": (inf, 0.0), "gelu": (inf, 0.0), "gelu_tanh": (inf, 0.0), "silu": (inf, 0.0)}
+    zd = z.double()
+    finite = torch.isfinite(zd)
+    for act in ACTS[1:]:
+        D = NT_F["nt"](A, z.view(N, 1), act=act)
+        for row in (0, M - 1):
+            got = D[row].double()
+            want = torch.where(finite, L.act64(torch.where(finite, zd, torch.zeros_like(zd)), act), zd)
+            want[3] = limits[act][1]
+            assert torch.isnan(got[4])
+            keep = torch.tensor([i for i in range(N) if i not in (2, 4)], device="cuda")
+            assert got[2] == inf
+            L.assert_close(got[keep], want[keep], 2.0 ** -14 * want[keep].abs() +
+                           L.rounding(want[keep], dt) * 1.01, "%s value" % act)
+        # its slopes, of A.B = 1
+        one = torch.ones((N, 1), dtype=dt, device="cuda")
+        D = DACT["nt"](A, one, z.expand(M, N).contiguous(), act)
+        for row in (0, M - 1):
+            got = D[row].double()
+            assert torch.isnan(got[4]), act
+            assert got[2] == 1.0 and got[3] == 0.0, act
+            idx = torch.nonzero(finite).view(-1)
+            want, mag = L.slope64(zd[idx].clamp(-1e3, 1e3), act)
+            L.assert_close(got[idx], want, 2.0 ** -15 * mag + 2.0 ** -21 +
+                           L.rounding(want, dt) * 1.01, "%s slope" % act)
+
+
+# ---- D = A.T @ B ------------------------------------------------------------
+
+TN = [  # (M, N, K): tiles at and past their edges; split and last-wave split K
+    (1, 1, 1), (8, 8, 3), (22, 34, 200), (256, 256, 64), (257, 300, 65), (264, 520, 1000),
+    (120, 1000, 20000), (512, 640, 5003), (1001, 77, 4096), (4096, 4352, 600), (1500, 700, 63),
+]
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("M,N,K", TN)
+def test_tn_full_check(M, N, K, dtype):
+    dt = L.GEN[dtype]
+    gen = generator(M + N + K)
+    A, B = rand(gen, K, M, dt=dt), rand(gen, K, N, dt=dt)
+    D, c = dg.gemm_tn(A, B, colsum=True)
+    what = "tn %s %dx%dx%d" % (dtype, M, N, K)
+    L.check_tn(D, c, A, B, what)
+    assert torch.equal(dg.gemm_tn(A, B), D)  # (with or without the sums)
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("M,N,K,pa,pb,pd,oa,ob", [
+    (100, 90, 300, 3, 0, 1, 0, 0), (264, 520, 500, 8, 16, 8, 0, 0), (264, 520, 500, 0, 0, 0, 1, 7),
+    (513, 40, 9000, 7, 24, 2, 0, 0)])
+def test_tn_strides_offsets_and_untouched_padding(M, N, K, pa, pb, pd, oa, ob, dtype):
+    dt = L.GEN[dtype]
+    gen = generator(M + pa)
+    A = rand(gen, K, M, dt=dt, pad=pa, off=oa)
+    B = rand(gen, K, N, dt=dt, pad=pb, off=ob)
+    dbuf, D = canary(M, N, dt=dt, pad=pd)
+    c = torch.full((M + 2,), CANARY, dtype=dt, device="cuda")
+    dg.gemm_tn(A, B, D=D, colsum=c[1:-1])
+    L.check_tn(D, c[1:-1], A, B, "strided")
+    padding_untouched(dbuf, N)
+    assert c[0] == CANARY and c[-1] == CANARY
+
+
+def test_tn_zero_rows():
+    A = torch.empty((0, 40), dtype=torch.bfloat16, device="cuda")
+    B = torch.empty((0, 300), dtype=torch.bfloat16, device="cuda")
+    D, c = dg.gemm_tn(A, B, colsum=True)
+    assert torch.equal(D, torch.zeros_like(D)) and torch.equal(c, torch.zeros_like(c))
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_tn_small_integers_exact_and_subnormal_sums(dtype):
+    dt = L.GEN[dtype]
+    gen = generator(3)
+    A = torch.randint(-3, 4, (700, 300), generator=gen, device="cuda").to(dt)
+    B = torch.randint(-3, 4, (700, 260), generator=gen, device="cuda").to(dt)
+    D, c = dg.gemm_tn(A, B, colsum=True)
+    want = (A.double().t().contiguous() @ B.double())
+    assert torch.equal(D.double(), want.to(dt).double())
+    assert torch.equal(c, A.double().sum(0).to(dt))
+    # subnormal values keep their place in the sums
+    tiny = torch.finfo(dt).smallest_normal * 2.0 ** -(6 if dt == torch.float16 else 5)
+    A = (torch.randint(-3, 4, (128, 64), generator=gen, device="cuda").double() * tiny).to(dt)
+    D, c = dg.gemm_tn(A, torch.ones((128, 8), dtype=dt, device="cuda"), colsum=True)
+    want = A.double().sum(0)
+    assert torch.equal(c.double(), want)
+    assert torch.equal(D.double(), want.view(-1, 1).expand(64, 8))
+
+
+# ---- row groups -------------------------------------------------------------
+
+def ends_of(sizes):
+    out, s = [], 0
+    for n in sizes:
+        s += n
+        out.append(s)
+    return out
+
+
+def spread(G, rows, seed, idle=0.3):
+    g = torch.Generator().manual_seed(seed)
+    w = torch.rand(G, generator=g) ** 2 * (torch.rand(G, generator=g) > idle)
+    if float(w.sum()) == 0.0:
+        w[G // 2] = 1.0
+    n = torch.floor(w / w.sum() * rows).long()
+    n[int(torch.argmax(w))] += rows - int(n.sum())
+    return [int(x) for x in n]
+
+
+GROUPS = [  # (sizes, rows behind the last, N, K)
+    ([1], 0, 40, 64),
+    ([0, 3, 0], 2, 100, 72),
+    ([1, 1, 0, 2, 1, 0, 0, 3], 5, 264, 512),
+    ([17, 0, 40, 16, 1], 3, 96, 200),
+    ([0, 0, 0], 6, 64, 64),
+    ([600], 0, 520, 128),
+    ([255, 256, 257, 0, 1], 7, 300, 264),
+    ([0] * 7 + [900] + [0] * 8, 100, 264, 136),
+    (spread(100, 1500, 1), 9, 200, 96),
+    (spread(200, 260, 2), 0, 56, 128),
+    (spread(12, 5000, 3), 33, 1100, 160),
+    (spread(5, 77, 4), 0, 1001, 333),
+    (spread(9, 2000, 5), 12, 301, 75),
+]
+IDS = ["G%d_rows%d_N%d_K%d" % (len(s), sum(s), n, k) for s, _, n, k in GROUPS]
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("layout", ["nt", "nn"])
+@pytest.mark.parametrize("case", GROUPS, ids=IDS)
+def test_grouped_full_check(case, layout, dtype):
+    sizes, behind, N, K = case
+    dt = L.GEN[dtype]
+    G, rows = len(sizes), sum(sizes)
+    M = rows + behind
+    gen = generator(M + N)
+    ends = ends_of(sizes)
+    e = torch.tensor(ends, dtype=torch.int32, device="cuda")
+    A = rand(gen, M, K, dt=dt)
+    A[rows:] = float("nan")
+    B = rand(gen, *((G, N, K) if layout == "nt" else (G, K, N)), dt=dt, sigma=K ** -0.5)
+    bias, R = rand(gen, G, N, dt=dt), rand(gen, M, N, dt=dt)
+    D = torch.full((M, N), CANARY, dtype=dt, device="cuda")
+    Z = torch.full((M, N), CANARY, dtype=dt, device="cuda")
+    GRP[layout](A, B, e, bias=bias, act="gelu", residual=R, preact=Z, D=D)
+    F = torch.full((M, N), CANARY, dtype=dt, device="cuda")
+    GRP_DACT[layout](A, B, e, R, "silu", D=F)
+    P = torch.full((M, N), CANARY, dtype=dt, device="cuda")
+    GRP[layout](A, B, e, D=P)
+    for g, a, b in L.spans(ends):
+        if a == b:
+            continue
+        what = "%s %s group %d rows %d..%d" % (layout, dtype, g, a, b)
+        L.check_forward(D[a:b], Z[a:b], A[a:b], B[g], layout, bias[g], "gelu", R[a:b], what)
+        L.check_dact(F[a:b], A[a:b], B[g], layout, R[a:b], "silu", what + " dact")
+        L.check_forward(P[a:b], None, A[a:b], B[g], layout, None, "none", None, what + " plain")
+    for t in (D, Z, F, P):
+        assert bool((t[rows:] == CANARY).all())
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("layout", ["nt", "nn"])
+def test_grouped_strides_and_shared_matrix(layout, dtype):
+    dt = L.GEN[dtype]
+    gen = generator(8)
+    sizes, N, K = [30, 0, 200, 5], 90, 104
+    M, G = sum(sizes), len(sizes)
+    ends = ends_of(sizes)
+    e = torch.tensor(ends, dtype=torch.int32, device="cuda")
+    for pa, pb, pd, off in ((0, 0, 0, 0), (8, 8, 8, 8), (3, 1, 5, 1)):
+        A = rand(gen, M, K, dt=dt, pad=pa)
+        B = rand(gen, *((G, N, K) if layout == "nt" else (G, K, N)), dt=dt, sigma=K ** -0.5, pad=pb,
+                 off=off)
+        bias = rand(gen, G, N, dt=dt, pad=pd)
+        dbuf, D = canary(M, N, dt=dt, pad=pd)
+        GRP[layout](A, B, e, bias=bias, act="relu", D=D)
+        for g, a, b in L.spans(ends):
+            if b > a:
+                L.check_forward(D[a:b], None, A[a:b], B[g], layout, bias[g], "relu", None, str(g))
+        padding_untouched(dbuf, N)
+    # one matrix and one bias for all groups, as views of stride 0
+    W, b1 = B[0].contiguous(), bias[0].contiguous()
+    D = GRP[layout](A, W.expand(G, *W.shape), e, bias=b1.expand(G, N))
+    L.check_forward(D, None, A, W, layout, b1, "none", None, "shared")
+
+
+TN_GROUPS = [
+    ([1], 0, 8, 8), ([0, 3, 0], 2, 100, 72), ([64, 0, 65, 63, 1], 3, 264, 300),
+    ([0, 0], 5, 40, 40), ([3000, 10, 0, 700], 8, 256, 256), (spread(40, 3001, 6), 64, 520, 77),
+    (spread(300, 900, 7), 1, 48, 300), ([20000], 0, 300, 100), (spread(6, 6000, 8), 0, 1030, 1800),
+]
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("case", TN_GROUPS, ids=["G%d_rows%d_%dx%d" % (len(s), sum(s), m, n)
+                                                for s, _, m, n in TN_GROUPS])
+def test_tn_grouped_full_check(case, dtype):
+    sizes, behind, M, N = case
+    dt = L.GEN[dtype]
+    rows = sum(sizes)
+    gen = generator(rows + M)
+    ends = ends_of(sizes)
+    e = torch.tensor(ends, dtype=torch.int32, device="cuda")
+    A, B = rand(gen, rows + behind, M, dt=dt), rand(gen, rows + behind, N, dt=dt)
+    A[rows:] = float("nan")
+    B[rows:] = float("inf")
+    D, c = dg.gemm_tn_grouped(A, B, e, colsum=True)
+    for g, a, b in L.spans(ends):
+        L.check_tn(D[g], c[g], A[a:b], B[a:b], "group %d rows %d..%d" % (g, a, b))
+    assert torch.equal(dg.gemm_tn_grouped(A, B, e), D)
+
+
+def test_tn_grouped_strides_and_untouched_padding():
+    dt = torch.float16
+    gen = generator(9)
+    sizes, M, N = [40, 0, 300], 70, 90
+    ends = ends_of(sizes)
+    e = torch.tensor(ends, dtype=torch.int32, device="cuda")
+    A, B = rand(gen, 340, M, dt=dt, pad=2), rand(gen, 340, N, dt=dt, pad=6, off=1)
+    buf = torch.full((3, M + 1, N + 3), CANARY, dtype=dt, device="cuda")
+    dg.gemm_tn_grouped(A, B, e, D=buf[:, :M, :N])
+    for g, a, b in L.spans(ends):
+        L.check_tn(buf[g, :M, :N], None, A[a:b], B[a:b], str(g))
+    assert bool((buf[:, M:] == CANARY).all()) and bool((buf[:, :, N:] == CANARY).all())
+
+
+def test_ends_outside_the_rows_are_clamped():
+    # too large, negative and decreasing ends stay inside the operands: the
+    # guard rows around A, B and D are checked for writes, and the rows that
+    # exactly one group holds for their values
+    dt = torch.bfloat16
+    gen = generator(10)
+    M, N, K = 300, 64, 64
+    abuf = rand(gen, M + 200, K, dt=dt)
+    A = abuf[100:100 + M]
+    B = rand(gen, 4, N, K, dt=dt, sigma=K ** -0.5)
+    for ends, keep in (([-5, 100, 100000, 2 ** 31 - 1], (0, M)), ([200, 50, 50, 300], (0, 50)),
+                       ([400, 400, 10, -7], (0, 10))):
+        e = torch.tensor(ends, dtype=torch.int32, device="cuda")
+        buf = torch.full((M + 200, N), CANARY, dtype=dt, device="cuda")
+        dg.gemm_nt_grouped(A, B, e, D=buf[100:100 + M])
+        torch.cuda.synchronize()
+        assert bool((buf[:100] == CANARY).all()) and bool((buf[100 + M:] == CANARY).all()), ends
+        G = rand(gen, M, N, dt=dt)
+        dg.gemm_tn_grouped(A, G, e, colsum=True)
+        torch.cuda.synchronize()
+        lo, hi = keep
+        got = buf[100 + lo:100 + hi]
+        g_of = {(-5): None}.get(ends[0], 0)
+        if g_of is not None:
+            L.check_forward(got, None, A[lo:hi], B[0], "nt", None, "none", None, str(ends))
+        else:
+            L.check_forward(got[:100], None, A[:100], B[1], "nt", None, "none", None, str(ends))
+            L.check_forward(got[100:], None, A[100:], B[2], "nt", None, "none", None, str(ends))
+
+
+# ---- how the calls are made ----------------------------------------------------
+
+def test_another_stream_workspace_and_repeatability():
+    dt = torch.bfloat16
+    gen = generator(20)
+    M, N, K = 256, 256, 8192  # split K
+    A, B = rand(gen, M, K, dt=dt), rand(gen, N, K, dt=dt, sigma=K ** -0.5)
+    R = rand(gen, M, N, dt=dt)
+    first = dg.gemm_nt_fused(A, B, act="silu", residual=R)
+    tn, c = dg.gemm_tn(A, A, colsum=True)
+    torch.cuda.synchronize()
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    outs = []
+    for _ in range(3):
+        outs.append(dg.gemm_nt_fused(A, B, act="silu", residual=R, stream=s1))
+        outs.append(dg.gemm_nt_fused(A, B, act="silu", residual=R, stream=s2))
+        outs.append(dg.gemm_tn(A, A, colsum=True, stream=s2.cuda_stream))
+    torch.cuda.synchronize()
+    for o in outs:
+        if isinstance(o, tuple):
+            assert torch.equal(o[0], tn) and torch.equal(o[1], c)
+        else:
+            assert torch.equal(o, first)
+    # the caller's workspace: the size that the query reports, no less
+    lib = binding.load_library()
+    import ctypes
+    need = ctypes.c_size_t()
+    assert lib.dense_gemm_layer_workspace_size(2, M, N, K, A.data_ptr(), K, B.data_ptr(), K, None, 0,
+                                               ctypes.byref(need)) == 0
+    assert need.value > 0
+    ws = torch.empty(need.value, dtype=torch.uint8, device="cuda")
+    assert torch.equal(dg.gemm_nt_fused(A, B, act="silu", residual=R, workspace=ws), first)
+    with pytest.raises(binding.DenseGemmError) as err:
+        dg.gemm_nt_fused(A, B, workspace=ws[:-256])
+    assert err.value.status == binding.Status.WORKSPACE_TOO_SMALL
+
+
+def test_layer_captured_in_a_graph_and_replayed():
+    """An expert layer, forward and backward, captured once; each replay has
+    new inputs and another routing, and gives the eager calls' bits."""
+    dt = torch.bfloat16
+    gen = generator(21)
+    G, M, H, F = 6, 500, 192, 320
+    x, dy = torch.empty((M, H), dtype=dt, device="cuda"), torch.empty((M, H), dtype=dt, device="cuda")
+    w1, b1 = rand(gen, G, F, H, dt=dt, sigma=0.1), rand(gen, G, F, dt=dt)
+    w2, b2 = rand(gen, G, H, F, dt=dt, sigma=0.1), rand(gen, G, H, dt=dt)
+    ends = torch.empty(G, dtype=torch.int32, device="cuda")
+
+    def step():
+        z = torch.zeros((M, F), dtype=dt, device="cuda")
+        h = dg.gemm_nt_grouped(x, w1, ends, bias=b1, act="silu", preact=z,
+                               D=torch.zeros((M, F), dtype=dt, device="cuda"))
+        y = dg.gemm_nt_grouped(h, w2, ends, bias=b2, residual=x,
+                               D=torch.zeros((M, H), dtype=dt, device="cuda"))
+        dz = dg.gemm_nn_grouped_dact(dy, w2, ends, z, "silu",
+                                     D=torch.zeros((M, F), dtype=dt, device="cuda"))
+        dw2, db2 = dg.gemm_tn_grouped(dy, h, ends, colsum=True)
+        dw1, db1 = dg.gemm_tn_grouped(dz, x, ends, colsum=True)
+        dx = dg.gemm_nn_grouped(dz, w1, ends, residual=dy,
+                                D=torch.zeros((M, H), dtype=dt, device="cuda"))
+        # few tiles, long sums: the split kernels, which take a workspace
+        t = dg.gemm_nt_fused(x.t().contiguous(), dy.t().contiguous(), act="gelu")
+        return h, y, dz, dw2, db2, dw1, db1, dx, t
+
+    def load(seed):
+        g2 = generator(seed)
+        x.copy_(rand(g2, M, H, dt=dt))
+        dy.copy_(rand(g2, M, H, dt=dt))
+        ends.copy_(torch.tensor(ends_of(spread(G, M - seed % 7, seed)), dtype=torch.int32))
+
+    load(30)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        step()
+    torch.cuda.current_stream().wait_stream(s)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        outs = step()
+    for rep in range(4):
+        load(40 + rep)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [o.clone() for o in outs]
+        want = step()
+        torch.cuda.synchronize()
+        for i, (a, b) in enumerate(zip(got, want)):
+            assert torch.equal(a, b), (rep, i)
+
+
+def test_expert_layer_gradients_against_autograd_and_differences():
+    """y = x + W2 silu(W1 x + b1) + b2 per expert, its gradients by the
+    library's calls, against automatic differentiation of the plain form in
+    64 bits and against central differences."""
+    dt = torch.float16
+    gen = generator(50)
+    sizes, H, F = [50, 0, 131, 7, 84], 72, 136
+    G, M = len(sizes), sum(sizes)
+    ends = ends_of(sizes)
+    e = torch.tensor(ends, dtype=torch.int32, device="cuda")
+    x, dy = rand(gen, M, H, dt=dt), rand(gen, M, H, dt=dt)
+    w1, b1 = rand(gen, G, F, H, dt=dt, sigma=H ** -0.5), rand(gen, G, F, dt=dt, sigma=0.5)
+    w2, b2 = rand(gen, G, H, F, dt=dt, sigma=F ** -0.5), rand(gen, G, H, dt=dt, sigma=0.5)
+    z = torch.empty((M, F), dtype=dt, device="cuda")
+    h = dg.gemm_nt_grouped(x, w1, e, bias=b1, act="silu", preact=z)
+    y = dg.gemm_nt_grouped(h, w2, e, bias=b2, residual=x)
+    dz = dg.gemm_nn_grouped_dact(dy, w2, e, z, "silu")
+    dw2, db2 = dg.gemm_tn_grouped(dy, h, e, colsum=True)
+    dw1, db1 = dg.gemm_tn_grouped(dz, x, e, colsum=True)
+    dx = dg.gemm_nn_grouped(dz, w1, e, residual=dy)
+
+    def plain(p):
+        out = []
+        for g, a, b in L.spans(ends):
+            hh = p["x"][a:b] @ p["w1"][g].t() + p["b1"][g]
+            out.append(p["x"][a:b] + (hh * torch.sigmoid(hh)) @ p["w2"][g].t() + p["b2"][g])
+        return torch.cat(out)
+
+    p = {k: v.double().requires_grad_() for k, v in
+         dict(x=x, w1=w1, b1=b1, w2=w2, b2=b2).items()}
+    yy = plain(p)
+    yy.backward(dy.double())
+    # each stored tensor (h, z, dz) is rounded once by at most 2^-11 of its
+    # values; carried through sums of at most F = 136 or 131 terms of that
+    # relative error, and rounded once more, the root of the mean square stays
+    # within 4 of those half steps of the gradient's own root mean square
+    for name, got, want in (("y", y, yy.detach()), ("dx", dx, p["x"].grad), ("dw1", dw1, p["w1"].grad),
+                            ("db1", db1, p["b1"].grad), ("dw2", dw2, p["w2"].grad),
+                            ("db2", db2, p["b2"].grad)):
+        err = (got.double() - want).square().mean().sqrt()
+        assert float(err) <= 4 * 2.0 ** -11 * float(want.square().mean().sqrt()), name
+    # differences of the plain form along each parameter's gradient direction
+    with torch.no_grad():
+        for name, got in (("x", dx), ("w1", dw1), ("b1", db1), ("w2", dw2), ("b2", db2)):
+            d = torch.randn(p[name].shape, generator=gen, device="cuda").double()
+            step = 1e-5
+            q = {k: v.detach().clone() for k, v in p.items()}
+            q[name] = p[name] + step * d
+            up = (plain(q) * dy.double()).sum()
+            q[name] = p[name] - step * d
+            down = (plain(q) * dy.double()).sum()
+            slope = float((up - down) / (2 * step))
+            mine = float((got.double() * d).sum())
+            size = float(p[name].grad.norm())
+            assert abs(slope - mine) <= 4 * 2.0 ** -11 * size + 1e-6 * abs(slope), name
+
+
+def test_other_device_arguments_and_refusals():
+    dt = torch.bfloat16
+    A = torch.zeros((4, 64), dtype=dt, device="cuda")
+    B = torch.zeros((8, 64), dtype=dt, device="cuda")
+    with pytest.raises(ValueError):
+        dg.gemm_nt_fused(A, B, act="swish")
+    with pytest.raises(ValueError):
+        dg.gemm_nt_fused(A, torch.zeros((8, 72), dtype=dt, device="cuda"))
+    with pytest.raises(TypeError):
+        dg.gemm_nt_fused(A, B.half())
+    with pytest.raises(ValueError):
+        dg.gemm_nt_fused(A, B, bias=torch.zeros(9, dtype=dt, device="cuda"))
+    with pytest.raises(ValueError):
+        dg.gemm_nt_fused(A, B, residual=torch.zeros((4, 9), dtype=dt, device="cuda"))
+    with pytest.raises(ValueError):
+        dg.gemm_nt_fused(A, B.cpu())
+    with pytest.raises(binding.DenseGemmError):  # rows of stride 0
+        dg.gemm_nt_fused(A, B, residual=torch.zeros(8, dtype=dt, device="cuda").expand(4, 8))
+    with pytest.raises(binding.DenseGemmError):
+        dg.gemm_nt_dact(A, B, torch.zeros((4, 8), dtype=dt, device="cuda"), "none")
+    e = torch.tensor([4, 4], dtype=torch.int32, device="cuda")
+    B3 = torch.zeros((2, 8, 64), dtype=dt, device="cuda")
+    with pytest.raises(TypeError):
+        dg.gemm_nt_grouped(A, B3, e.long())
+    with pytest.raises(ValueError):
+        dg.gemm_nt_grouped(A, B3, e[:1])
+    with pytest.raises(ValueError):
+        dg.gemm_nt_grouped(A, B3, e.cpu())
+    with pytest.raises(ValueError):
+        dg.gemm_tn(A, torch.zeros((5, 8), dtype=dt, device="cuda"))
+    with pytest.raises(binding.DenseGemmError):  # groups' outputs on top of each other
+        dg.gemm_tn_grouped(A, A, e, D=torch.zeros((64, 64), dtype=dt, device="cuda").expand(2, 64, 64))
