@@ -368,10 +368,25 @@ def gemm_nt_e4m3_mx(A, SA, B, SB, D=None, stream=None, workspace=None):
 
 
 # ---- the products of a layer ------------------------------------------------
+#
+# A call for one token takes about 6 us on the GPU, so what these functions do
+# before the launch counts: they look each property up once, and enter a
+# device context only where the operands are not on the current device.
 
-def _formats():
+_FMTS = {}   # torch dtype -> (name, dense_gemm_fmt); filled by _torch()
+_raw_stream = None
+
+
+def _torch():
+    global _raw_stream
     import torch
-    return {torch.float16: ("f16", 0), torch.bfloat16: ("bf16", 1)}
+    if not _FMTS:
+        # (the current stream's handle without building a Stream object,
+        # where this torch has it: 0.1 against 2 us)
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        _FMTS[torch.bfloat16] = ("bf16", 1)
+        _FMTS[torch.float16] = ("f16", 0)
+    return torch
 
 
 def _check_like(t, A, dims: int, what: str, shape=None):
@@ -383,13 +398,13 @@ def _check_like(t, A, dims: int, what: str, shape=None):
         raise ValueError("operands on different devices: %s and %s" % (A.device, t.device))
     if t.dim() != dims or (t.stride(-1) != 1 and t.shape[-1] > 1):
         raise ValueError("%s must be %d-D with unit stride in its last dimension" % (what, dims))
-    if shape is not None and tuple(t.shape) != shape:
+    if shape is not None and t.shape != shape:
         raise ValueError("%s has shape %s, expected %s" % (what, tuple(t.shape), shape))
 
 
 def _check_first(A):
     """A's format, as (name, dense_gemm_fmt)."""
-    fmt = _formats().get(A.dtype)
+    fmt = _FMTS.get(A.dtype)
     if fmt is None:
         raise TypeError("A must be float16 or bfloat16, got %s" % A.dtype)
     if not A.is_cuda:
@@ -399,8 +414,7 @@ def _check_first(A):
     return fmt
 
 
-def _check_ends(ends, A):
-    import torch
+def _check_ends(ends, A, torch):
     if ends.dtype != torch.int32:
         raise TypeError("ends must be int32, got %s" % ends.dtype)
     if ends.device != A.device:
@@ -416,81 +430,86 @@ def _stack(t):
     return (t.stride(0) if t.shape[0] > 1 else 0), ld
 
 
-def _run_with_workspace(name, call, size_of, workspace, stream, dev):
-    """Runs ``call(pointer, bytes, stream handle)``.  Without a workspace of
-    the caller's, one is taken from torch's allocator if the call turns out
-    to need it."""
-    import contextlib
-    import torch
-    here = torch.cuda.current_device() == dev.index
-    with contextlib.nullcontext() if here else torch.cuda.device(dev):
+def _launch(name, args, size_of, workspace, stream, dev, torch):
+    """Calls ``name(*args, workspace, bytes, stream)`` on the device.  Without
+    a workspace of the caller's, one is taken from torch's allocator if the
+    call turns out to need it (``size_of``: its size query)."""
+    if torch.cuda.current_device() != dev.index:
+        with torch.cuda.device(dev):
+            return _launch(name, args, size_of, workspace, stream, dev, torch)
+    fn = getattr(_lib, name)
+    if stream is None and _raw_stream is not None:
+        sh = _raw_stream(dev.index)
+    else:
         sh = _stream_handle(stream, dev)
-        if workspace is None or workspace is True:
-            st = call(None, 0, sh)
-            if st == Status.WORKSPACE_TOO_SMALL:
-                need = ctypes.c_size_t()
-                st = size_of(ctypes.byref(need))
-                if st == Status.OK:
-                    ws = _used_by(torch.empty(need.value, dtype=torch.uint8, device=dev), stream,
-                                  dev)
-                    st = call(ws.data_ptr(), need.value, sh)
-        else:
-            if not workspace.is_cuda or workspace.device != dev:
-                raise ValueError("workspace must be a device tensor on %s" % dev)
-            st = call(workspace.data_ptr(), workspace.numel() * workspace.element_size(), sh)
-    if st != Status.OK:
+    if workspace is None or workspace is True:
+        st = fn(*args, None, 0, sh)
+        if st == 10:  # WORKSPACE_TOO_SMALL
+            need = ctypes.c_size_t()
+            st = size_of(need)
+            if st == 0:
+                ws = _used_by(torch.empty(need.value, dtype=torch.uint8, device=dev), stream, dev)
+                st = fn(*args, ws.data_ptr(), need.value, sh)
+    else:
+        if not workspace.is_cuda or workspace.device != dev:
+            raise ValueError("workspace must be a device tensor on %s" % dev)
+        st = fn(*args, workspace.data_ptr(), workspace.numel() * workspace.element_size(), sh)
+    if st != 0:
         raise DenseGemmError(st, name)
 
 
 def _layer(layout, A, B, ends, bias, act, residual, preact, grad, D, stream, workspace):
-    import torch
-    lib = load_library()
-    fmt, _ = _check_first(A)
-    if act not in ACTS:
+    lib = _lib or load_library()
+    torch = _torch()
+    fmt = _check_first(A)
+    code = ACTS.get(act)
+    if code is None:
         raise ValueError("act must be one of %s, got %r" % (", ".join(ACTS), act))
     M, K = A.shape
     _check_like(B, A, 2 if ends is None else 3, "B")
-    Kb, N = B.shape[-2:] if layout == "nn" else (B.shape[-1], B.shape[-2])
+    if layout == "nt":
+        N, Kb = B.shape[-2:]
+    else:
+        Kb, N = B.shape[-2:]
     if Kb != K:
         raise ValueError("inner dimensions differ: A is %s, B is %s"
                          % (tuple(A.shape), tuple(B.shape)))
-    groups = None
+    groups, G = None, ()
     if ends is None:
-        ldb, G = _ld(B), ()
+        ldb = _ld(B)
     else:
-        _check_ends(ends, A)
-        if ends.shape[0] != B.shape[0]:
-            raise ValueError("%d group ends for %d matrices B" % (ends.shape[0], B.shape[0]))
-        stride, ldb = _stack(B)
+        _check_ends(ends, A, torch)
         G = (B.shape[0],)
-        groups = Groups(ends.data_ptr(), B.shape[0], stride)
-    epi = Epilogue(act=ACTS[act], grad=grad)
-    if bias is not None:
-        _check_like(bias, A, 1 + len(G), "bias", G + (N,))
-        epi.bias = bias.data_ptr()
-        epi.bias_stride = bias.stride(0) if G and G[0] > 1 else 0
-    if residual is not None:
-        _check_like(residual, A, 2, "residual", (M, N))
-        epi.residual, epi.ldr = residual.data_ptr(), _ld(residual)
-    if preact is not None:
-        _check_like(preact, A, 2, "preact", (M, N))
-        epi.preact, epi.ldz = preact.data_ptr(), _ld(preact)
+        if ends.shape[0] != G[0]:
+            raise ValueError("%d group ends for %d matrices B" % (ends.shape[0], G[0]))
+        stride, ldb = _stack(B)
+        groups = Groups(ends.data_ptr(), G[0], stride)
+    epi = None
+    if code or bias is not None or residual is not None or preact is not None:
+        epi = Epilogue(act=code, grad=grad)
+        if bias is not None:
+            _check_like(bias, A, 1 + len(G), "bias", G + (N,))
+            epi.bias = bias.data_ptr()
+            if G and G[0] > 1:
+                epi.bias_stride = bias.stride(0)
+        if residual is not None:
+            _check_like(residual, A, 2, "residual", (M, N))
+            epi.residual, epi.ldr = residual.data_ptr(), _ld(residual)
+        if preact is not None:
+            _check_like(preact, A, 2, "preact", (M, N))
+            epi.preact, epi.ldz = preact.data_ptr(), _ld(preact)
     dev = A.device
     if D is None:
         D = _used_by(torch.empty((M, N), dtype=A.dtype, device=dev), stream, dev)
     else:
         _check_like(D, A, 2, "D", (M, N))
-    op = OPS[(layout, fmt)]
-    a, b, lda = A.data_ptr(), B.data_ptr(), _ld(A)
+    args = (OPS[(layout, fmt[0])], M, N, K, A.data_ptr(), _ld(A), B.data_ptr(), ldb)
 
-    def call(ws, nbytes, sh):
-        return lib.dense_gemm_layer(op, M, N, K, a, lda, b, ldb, D.data_ptr(), _ld(D), epi, groups,
-                                    ws, nbytes, sh)
+    def size_of(need):
+        return lib.dense_gemm_layer_workspace_size(*args, groups, 0, ctypes.byref(need))
 
-    def size_of(out):
-        return lib.dense_gemm_layer_workspace_size(op, M, N, K, a, lda, b, ldb, groups, 0, out)
-
-    _run_with_workspace("dense_gemm_layer", call, size_of, workspace, stream, dev)
+    _launch("dense_gemm_layer", args + (D.data_ptr(), _ld(D), epi, groups), size_of, workspace,
+            stream, dev, torch)
     return D
 
 
@@ -554,9 +573,9 @@ def gemm_nn_grouped_dact(A, B, ends, preact, act, D=None, stream=None, workspace
 
 
 def _tn(A, B, ends, D, colsum, stream, workspace):
-    import torch
-    lib = load_library()
-    _, fmt = _check_first(A)
+    lib = _lib or load_library()
+    torch = _torch()
+    fmt = _check_first(A)
     K, M = A.shape
     _check_like(B, A, 2, "B")
     N = B.shape[1]
@@ -565,7 +584,7 @@ def _tn(A, B, ends, D, colsum, stream, workspace):
     dev = A.device
     G = ()
     if ends is not None:
-        _check_ends(ends, A)
+        _check_ends(ends, A, torch)
         G = (ends.shape[0],)
     if D is None:
         D = _used_by(torch.empty(G + (M, N), dtype=A.dtype, device=dev), stream, dev)
@@ -585,17 +604,14 @@ def _tn(A, B, ends, D, colsum, stream, workspace):
     else:
         stride, ldd = _stack(D)
         groups = Groups(ends.data_ptr(), G[0], stride)
-    a, b, lda, ldb = A.data_ptr(), B.data_ptr(), _ld(A), _ld(B)
-    sums_ptr = None if sums is None else sums.data_ptr()
+    args = (M, N, K, A.data_ptr(), _ld(A), B.data_ptr(), _ld(B))
 
-    def call(ws, nbytes, sh):
-        return lib.dense_gemm_tn(fmt, M, N, K, a, lda, b, ldb, D.data_ptr(), ldd, sums_ptr, groups,
-                                 ws, nbytes, sh)
+    def size_of(need):
+        return lib.dense_gemm_tn_workspace_size(*args, groups, 0, ctypes.byref(need))
 
-    def size_of(out):
-        return lib.dense_gemm_tn_workspace_size(M, N, K, a, lda, b, ldb, groups, 0, out)
-
-    _run_with_workspace("dense_gemm_tn", call, size_of, workspace, stream, dev)
+    _launch("dense_gemm_tn",
+            (fmt[1],) + args + (D.data_ptr(), ldd, None if sums is None else sums.data_ptr(), groups),
+            size_of, workspace, stream, dev, torch)
     return D if sums is None else (D, sums)
 
 

@@ -33,6 +33,21 @@ __device__ __forceinline__ int swz_k(int r) { return ((r >> 1) ^ (r << 2)) & 7; 
 // in a different 32-byte group of the 512-byte row, i.e. in distinct banks.
 __device__ __forceinline__ int swz_n(int k) { return ((k & 3) | (((k >> 3) & 3) << 2)) << 1; }
 
+// The same for a tile W columns wide.  W = 128: rows of 256 bytes (16
+// chunks), so two rows span the banks and the row's low bit already tells
+// their halves apart; the XOR of chunk bits 1-3 with r >> 1 and q separates
+// the eight rows of each half.
+template <int W>
+__device__ __forceinline__ int swz_rows(int k) {
+  static_assert(W == 256 || W == 128, "tile widths");
+  return W == 256 ? swz_n(k) : (((k >> 1) & 1) | (((k >> 3) & 3) << 1)) << 1;
+}
+
+// 16 and 8 bytes at any 2-byte alignment: the hardware's unaligned access
+// mode (the ROCm default) takes them in one instruction.
+typedef u32x4 u32x4_any __attribute__((aligned(2)));
+typedef u32x2 u32x2_any __attribute__((aligned(2)));
+
 __device__ __forceinline__ uint32_t lds_addr(const void* p) {
   return (uint32_t)(uintptr_t)(const lds_void*)p;
 }
@@ -139,28 +154,17 @@ __device__ __forceinline__ uint32_t pack2<__bf16>(float lo, float hi) {
   return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2){lo, hi}, bf16x2));
 }
 
-// s plus the eight 16-bit values of an MFMA fragment's lane, in FP32 (two
-// values per v_dot2c, with ones).
+// s plus the two 16-bit values of w, in FP32 (one v_dot2c, with ones).
 template <typename T>
-__device__ __forceinline__ float sum8(float s, u32x4 f);
+__device__ __forceinline__ float sum2(float s, uint32_t w);
 template <>
-__device__ __forceinline__ float sum8<_Float16>(float s, u32x4 f) {
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const uint32_t w = f[k];  // (the bit cast of the element itself takes element 0)
-    s = __builtin_amdgcn_fdot2(__builtin_bit_cast(f16x2, w), (f16x2){1.0f, 1.0f}, s, false);
-  }
-  return s;
+__device__ __forceinline__ float sum2<_Float16>(float s, uint32_t w) {
+  return __builtin_amdgcn_fdot2(__builtin_bit_cast(f16x2, w), (f16x2){1.0f, 1.0f}, s, false);
 }
 template <>
-__device__ __forceinline__ float sum8<__bf16>(float s, u32x4 f) {
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const uint32_t w = f[k];
-    s = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, w),
-                                        (bf16x2){(__bf16)1.0f, (__bf16)1.0f}, s, false);
-  }
-  return s;
+__device__ __forceinline__ float sum2<__bf16>(float s, uint32_t w) {
+  return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, w),
+                                         (bf16x2){(__bf16)1.0f, (__bf16)1.0f}, s, false);
 }
 
 // Transposing LDS read: within each 16-lane block, lane i receives element

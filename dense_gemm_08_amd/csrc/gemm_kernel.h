@@ -98,6 +98,14 @@ struct LayerParams : Params {
   float* colsum_ws;
 };
 
+// Workgroups per CU: two for the 128 x 128 tiles of the layer products (80
+// KiB of LDS and half the registers each), so that one computes while the
+// other waits for its first tiles or writes its last ones.
+template <int LAYOUT, int TN, int TM, bool EPI, bool GROUP>
+constexpr int two_per_cu() {
+  return TM == BM / 2 && TN == BN / 2 && (EPI || GROUP || LAYOUT == TA) ? 2 : 1;
+}
+
 template <int MA, int NB>
 struct Frags {
   u32x4 a[MA];
@@ -121,10 +129,11 @@ struct Frags {
 //   SUMS       (TA) also the sums of A's columns over k.
 template <typename T, int LAYOUT, bool SPLIT, int TN, int TM, bool EPI = false, bool GROUP = false,
           bool SUMS = false>
-__global__ __launch_bounds__(THREADS) void gemm_kernel(
+__global__ __launch_bounds__(THREADS, (two_per_cu<LAYOUT, TN, TM, EPI, GROUP>())) void gemm_kernel(
     std::conditional_t<EPI || GROUP || LAYOUT == TA, LayerParams, Params> p) {
-  static_assert(TN == BN || (TN == BN / 2 && LAYOUT == NT), "tile widths 256, and 128 for A @ B.T");
-  static_assert(TM == BM || (TM == BM / 2 && LAYOUT != TA), "tile rows 256 or 128");
+  static_assert(TN == BN || TN == BN / 2, "tile widths 256 and 128");
+  static_assert(TM == BM || TM == BM / 2, "tile rows 256 or 128");
+  static_assert(LAYOUT != TA || TM == TN, "A.T @ B takes square tiles");
   static_assert(!(EPI && LAYOUT == TA), "no epilogue on A.T @ B");
   static_assert(!SUMS || LAYOUT == TA, "column sums of A where its rows are k");
   static_assert(!(GROUP && SPLIT && LAYOUT != TA), "row groups are not split in K");
@@ -157,11 +166,23 @@ __global__ __launch_bounds__(THREADS) void gemm_kernel(
   const int wm = wave >> 1;  // wave tile row (0..1)
   const int wn = wave & 1;   // wave tile column (0..1)
 
-  const int slot0 = xcd_slot(blockIdx.x, gridDim.x, p.num_xcds);
-  [[maybe_unused]] GroupWalk walk;
-  if constexpr (ROWS) walk.start(p.g);
+  int slot0, num_tasks;
+  // (four registers each for the counts and ends of up to 256 groups)
+  [[maybe_unused]] GroupMap<4> map;
+  if constexpr (ROWS) {
+    // the XCDs share the tiles there are, also where those are fewer than
+    // the launch's workgroups
+    map.count(p.g, TM, p.tiles_n);
+    num_tasks = map.total;
+    const int busy = min((int)gridDim.x, num_tasks);
+    if ((int)blockIdx.x >= busy) return;
+    slot0 = xcd_slot(blockIdx.x, busy, p.num_xcds);
+  } else {
+    slot0 = xcd_slot(blockIdx.x, gridDim.x, p.num_xcds);
+    num_tasks = p.num_tasks;
+  }
 
-  for (int task = slot0; ROWS || task < p.num_tasks; task += gridDim.x) {
+  for (int task = slot0; task < num_tasks; task += gridDim.x) {
     int tm, tn;
     const bool part = SPLIT && task >= p.full_tasks;
     const int u = task - p.full_tasks;
@@ -174,13 +195,14 @@ __global__ __launch_bounds__(THREADS) void gemm_kernel(
     int row0 = 0, M = p.M, K = p.K, steps = p.split_steps;
     [[maybe_unused]] int group = 0;
     if constexpr (ROWS) {
-      if (!walk.find(p.g, task, TM, p.tiles_n)) break;
-      group = walk.g;
-      row0 = walk.beg;
-      M = walk.end;
+      GroupTile t;
+      map.find(p.g, task, TM, p.tiles_n, &t);
+      group = t.group;
+      row0 = t.beg;
+      M = t.end;
       gB += group * p.g.stride;
       const int tiles_m = (M - row0 + TM - 1) / TM;
-      tile_of_task(task - walk.first, tiles_m, p.tiles_n, min(tiles_m, p.group_m), &tm, &tn);
+      tile_of_task(t.tile, tiles_m, p.tiles_n, min(tiles_m, p.group_m), &tm, &tn);
     } else if constexpr (GROUP) {
       const int per = p.tiles_m * p.tiles_n;
       group = tile / per;
@@ -227,8 +249,10 @@ __global__ __launch_bounds__(THREADS) void gemm_kernel(
     // thread covers rows (L w + i) * 8 ... +7, lane -> row lane/8 of the
     // group and a logical chunk by the swizzle (which depends on the row's
     // low four bits, i.e. on i's parity, L being even).
-    // NN and TA B tile, TA A tile: each wave instruction fills 2 k rows of 512 B.
-    const int nn_row_lo = lane >> 5;
+    // NN and TA B tile, TA A tile: each wave instruction fills 2 k rows of
+    // 512 B, or 4 of 256 B where the tile is 128 wide.
+    constexpr int A_RPL = 512 / TM, B_RPL = 512 / TN;  // k rows per wave instruction (512 or 256 B)
+    const int nn_row_lo = lane / (64 / B_RPL);
 
     // Fragment read offsets (bytes within a stage).  Fragment f of a
     // K-contiguous tile (16 rows) sits 16 * 128 bytes after fragment 0: the
@@ -248,14 +272,16 @@ __global__ __launch_bounds__(THREADS) void gemm_kernel(
       const int klane = 8 * lq + (l16 >> 2);
       // swz_n of every row this lane reads (the +4 and +32 row offsets of the
       // reads leave bits 0-1 and 3-4 of k unchanged)
-      const int fl = swz_n(klane);
+      const int fl = swz_rows<TN>(klane);
 #pragma unroll
       for (int j = 0; j < NI; ++j)
-        fbn[j] = klane * 512 + (((wn * 16 + 2 * j + ((lane & 3) >> 1)) ^ fl) << 4) + (lane & 1) * 8;
+        fbn[j] = klane * (2 * TN) + (((wn * (WTN / 8) + 2 * j + ((lane & 3) >> 1)) ^ fl) << 4) +
+                 (lane & 1) * 8;
       if constexpr (LAYOUT == TA) {
 #pragma unroll
         for (int i = 0; i < MI; ++i)
-          fan[i] = klane * 512 + (((wm * 16 + 2 * i + ((lane & 3) >> 1)) ^ fl) << 4) + (lane & 1) * 8;
+          fan[i] = klane * (2 * TM) + (((wm * (WTM / 8) + 2 * i + ((lane & 3) >> 1)) ^ fl) << 4) +
+                   (lane & 1) * 8;
       }
     }
 
@@ -279,8 +305,8 @@ __global__ __launch_bounds__(THREADS) void gemm_kernel(
 #pragma unroll
     for (int i = 0; i < DMA_PER_OPERAND; ++i) {
       if constexpr (LAYOUT == TA) {
-        const int k = 2 * (8 * wave + i) + nn_row_lo;
-        a_off[i] = (uint32_t)(k * p.lda * 2 + ((lane & 31) ^ swz_n(k)) * 16);
+        const int k = A_RPL * (DMA_PER_OPERAND * wave + i) + nn_row_lo;
+        a_off[i] = (uint32_t)(k * p.lda * 2 + ((lane & (64 / A_RPL - 1)) ^ swz_rows<TM>(k)) * 16);
       } else {
         const int r = (DMA_PER_OPERAND * wave + i) * 8 + (lane >> 3);
         a_off[i] = r < vm ? (uint32_t)(r * p.lda * 2 + kc[i & 1] * 16) : OOB;
@@ -295,8 +321,8 @@ __global__ __launch_bounds__(THREADS) void gemm_kernel(
     } else {
 #pragma unroll
       for (int i = 0; i < DMA_B; ++i) {
-        const int k = 2 * (8 * wave + i) + nn_row_lo;
-        const int c = (lane & 31) ^ swz_n(k);
+        const int k = B_RPL * (DMA_B * wave + i) + nn_row_lo;
+        const int c = (lane & (64 / B_RPL - 1)) ^ swz_rows<TN>(k);
         b_off[i] = (uint32_t)(k * p.ldb * 2 + c * 16);
       }
     }
@@ -349,7 +375,7 @@ __global__ __launch_bounds__(THREADS) void gemm_kernel(
       if ((half == 0 && LAYOUT != TA) || LAYOUT == NT) {
         dma16_at(h.r, !masked || h.k0 + (kc[i & 1] << 3) >= 0 ? off : OOB, h.base, i * 1024);
       } else {
-        const int k = 2 * (8 * wave + i) + nn_row_lo;
+        const int k = B_RPL * ((half == 0 ? DMA_PER_OPERAND : DMA_B) * wave + i) + nn_row_lo;
         dma16_at(h.r, !masked || h.k0 + k >= 0 ? off : OOB, h.base, i * 1024);
       }
       fence();
@@ -375,7 +401,7 @@ __global__ __launch_bounds__(THREADS) void gemm_kernel(
       if (f < A_READS) {
         if constexpr (LAYOUT == TA) {
           const int i = f >> 1, h = f & 1;
-          const u32x2 v = read_tr(abase + fan[i] + (s * 32 + 4 * h) * 512);
+          const u32x2 v = read_tr(abase + fan[i] + (s * 32 + 4 * h) * (2 * TM));
           F.a[i][2 * h] = v[0];
           F.a[i][2 * h + 1] = v[1];
         } else {
@@ -386,7 +412,7 @@ __global__ __launch_bounds__(THREADS) void gemm_kernel(
         F.b[j] = *(const u32x4*)(bbase + fb[s] + j * 2048);
       } else {
         const int j = (f - A_READS) >> 1, h = (f - A_READS) & 1;
-        const u32x2 v = read_tr(bbase + fbn[j] + (s * 32 + 4 * h) * 512);
+        const u32x2 v = read_tr(bbase + fbn[j] + (s * 32 + 4 * h) * (2 * TN));
         F.b[j][2 * h] = v[0];
         F.b[j][2 * h + 1] = v[1];
       }
@@ -464,7 +490,8 @@ __global__ __launch_bounds__(THREADS) void gemm_kernel(
       for (int q = 0; q < PAIRS; ++q) {
         share(q, PAIRS, READS, [&](int f) { read_item(es, ls, 1, F1, f); });
         mfma_pair(F0, q);
-        if constexpr (SUMS) share(q, PAIRS, MI, [&](int i) { cs[i] = sum8<T>(cs[i], F0.a[i]); });
+        if constexpr (SUMS)
+          share(q, PAIRS, 4 * MI, [&](int i) { cs[i >> 2] = sum2<T>(cs[i >> 2], F0.a[i >> 2][i & 3]); });
         fence();
         // (the descriptor's scalar work goes behind the first MFMAs)
         if (q == 0) he = half_setup(ks + 2, es2, EARLY);
@@ -481,7 +508,8 @@ __global__ __launch_bounds__(THREADS) void gemm_kernel(
         if (q >= BAR_PAIR)
           share(q - BAR_PAIR, PAIRS - BAR_PAIR, READS, [&](int f) { read_item(es1, ls ^ 1, 0, F0, f); });
         mfma_pair(F1, q);
-        if constexpr (SUMS) share(q, PAIRS, MI, [&](int i) { cs[i] = sum8<T>(cs[i], F1.a[i]); });
+        if constexpr (SUMS)
+          share(q, PAIRS, 4 * MI, [&](int i) { cs[i >> 2] = sum2<T>(cs[i >> 2], F1.a[i >> 2][i & 3]); });
         fence();
         if (q >= BAR_PAIR)
           share(q - BAR_PAIR, PAIRS - BAR_PAIR, DMA_L,
@@ -559,11 +587,10 @@ __global__ __launch_bounds__(THREADS) void gemm_kernel(
       const int rowb = m0 + wm * WTM + rl;  // this lane's first row of the wave's
       uint32_t bias[4] = {0u, 0u, 0u, 0u};
       if (!ep.grad && ep.bias != nullptr && col < p.N)
-        load_row<4>(ep.bias + group * ep.bias_stride, col, p.N, ep.bias_vec, bias);
+        load_row<4>(ep.bias + group * ep.bias_stride, col, p.N, bias);
       // the operand each output needs: the residual, or the gradient's Z
       const uint16_t* side = ep.grad ? ep.z : ep.res;
       const int64_t lds_ = ep.grad ? ep.ldz : ep.ldr;
-      const int side_vec = ep.grad ? ep.z_vec : ep.res_vec;
       auto fetch = [&](int pass, uint32_t(&w)[R][4]) {
 #pragma unroll
         for (int t = 0; t < R; ++t) {
@@ -571,7 +598,7 @@ __global__ __launch_bounds__(THREADS) void gemm_kernel(
 #pragma unroll
           for (int k = 0; k < 4; ++k) w[t][k] = 0u;
           if (side != nullptr && !part && row < M && col < p.N)
-            load_row<4>(side + row * lds_, col, p.N, side_vec, w[t]);
+            load_row<4>(side + row * lds_, col, p.N, w[t]);
         }
       };
       auto stage = [&](int band) {
@@ -586,13 +613,21 @@ __global__ __launch_bounds__(THREADS) void gemm_kernel(
           }
         }
       };
-      uint32_t w[R][4], w_next[R][4];
+      uint32_t w[R][4], w_next[R][4] = {};
       fetch(0, w);
+      stage(0);
+      // Loads are waited for on every path (the empty asm uses their
+      // results): one that the compiler believes pending when the next tile's
+      // K loop begins makes it wait for all loads inside that loop.
+      asm volatile("" : "+v"(bias[0]), "+v"(bias[1]), "+v"(bias[2]), "+v"(bias[3]));
+#pragma unroll
+      for (int t = 0; t < R; ++t)
+        asm volatile("" : "+v"(w[t][0]), "+v"(w[t][1]), "+v"(w[t][2]), "+v"(w[t][3]));
 #pragma unroll 1
       for (int pass = 0; pass < (MI / 2) * PASSES; ++pass) {
         if (pass % PASSES == 0) {
           switch (pass / PASSES) {
-            case 0: stage(0); break;
+            case 0: break;
             case 1: stage(1); break;
             case 2: if constexpr (MI > 4) stage(2); break;
             default: if constexpr (MI > 4) stage(3); break;
@@ -639,7 +674,7 @@ __global__ __launch_bounds__(THREADS) void gemm_kernel(
 #pragma unroll
               for (int k = 0; k < 4; ++k) o[k] = pack2<T>(v[t][2 * k], v[t][2 * k + 1]);
               if (row < M && col < p.N)
-                store_row<4>(ep.z + (int64_t)row * ep.ldz, col, p.N, ep.z_vec, o);
+                store_row<4>(ep.z + (int64_t)row * ep.ldz, col, p.N, o);
             }
           }
           apply_act(ep.act, v);
@@ -651,13 +686,17 @@ __global__ __launch_bounds__(THREADS) void gemm_kernel(
           }
         }
 #pragma unroll
+        for (int t = 0; t < R; ++t)
+          asm volatile("" : "+v"(w_next[t][0]), "+v"(w_next[t][1]), "+v"(w_next[t][2]),
+                       "+v"(w_next[t][3]));
+#pragma unroll
         for (int t = 0; t < R; ++t) {
           const int row = rowb + (pass * R + t) * RPI;
           uint32_t o[4];
 #pragma unroll
           for (int k = 0; k < 4; ++k) o[k] = pack2<T>(v[t][2 * k], v[t][2 * k + 1]);
           if (!part && row < M && col < p.N)
-            store_row<4>(gD + (int64_t)row * p.ldd, col, p.N, p.d_vec, o);
+            store_row<4>(gD + (int64_t)row * p.ldd, col, p.N, o);
 #pragma unroll
           for (int k = 0; k < 4; ++k) w[t][k] = w_next[t][k];
         }
@@ -676,6 +715,7 @@ __global__ __launch_bounds__(THREADS) void gemm_kernel(
     constexpr int RPI = 64 / CH;      // rows per wave instruction of the read-back
     constexpr int NR = 32 / RPI;      // read-back instructions per band
     char* stg = smem + wave * (32 * CH * 16);
+    // (the layer products' 16-byte stores take D rows of any alignment)
     const bool interior = p.d_vec && vm == TM && vn == TN;
 #pragma unroll
     for (int band = 0; band < MI / 2; ++band) {
@@ -718,7 +758,8 @@ __global__ __launch_bounds__(THREADS) void gemm_kernel(
 #pragma unroll
         for (int t = 0; t < NR; ++t) {
           const int rr = t * RPI + lane / CH;
-          __builtin_nontemporal_store(r[t], (u32x4*)(gD + (int64_t)(rowb + rr) * p.ldd + col0 + cc * 8));
+          __builtin_nontemporal_store(r[t],
+                                      (u32x4_any*)(gD + (int64_t)(rowb + rr) * p.ldd + col0 + cc * 8));
         }
       } else {
 #pragma unroll
@@ -729,7 +770,7 @@ __global__ __launch_bounds__(THREADS) void gemm_kernel(
           if (row < M && col < p.N) {
             uint16_t* dst = gD + (int64_t)row * p.ldd + col;
             if (p.d_vec && col + 8 <= p.N) {
-              __builtin_nontemporal_store(r[t], (u32x4*)dst);
+              __builtin_nontemporal_store(r[t], (u32x4_any*)dst);
             } else {
 #pragma unroll
               for (int e = 0; e < 8; ++e)

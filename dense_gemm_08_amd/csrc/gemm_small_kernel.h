@@ -137,8 +137,11 @@ __global__ __launch_bounds__(SMALL_THREADS) void gemm_small(
   const uint16_t* gB = p.B;
   [[maybe_unused]] int group = 0;
   if constexpr (GROUP) {
+    GroupMap<1> map;
+    map.count(p.g, TR, p.tiles_n);
+    if ((int)blockIdx.x >= map.total) return;
     GroupTile t;
-    if (!find_tile(p.g, (int)blockIdx.x, p.num_xcds, TR, p.tiles_n, &t)) return;
+    map.find(p.g, xcd_slot((int)blockIdx.x, map.total, p.num_xcds), TR, p.tiles_n, &t);
     tile = t.tile;
     group = t.group;
     row0 = t.beg;
@@ -308,21 +311,21 @@ __global__ __launch_bounds__(SMALL_THREADS) void gemm_small(
     float x[1][4] = {{s[0], s[1], s[2], s[3]}};
     uint32_t w[1][2] = {{0u, 0u}};
     if (ep.grad) {
-      load_row<2>(ep.z + (int64_t)row * ep.ldz, col, p.N, ep.z_vec, w[0]);
+      load_row<2>(ep.z + (int64_t)row * ep.ldz, col, p.N, w[0]);
       apply_slope<T>(ep.act, x, w);
     } else {
       if (ep.bias != nullptr) {
-        load_row<2>(ep.bias + group * ep.bias_stride, col, p.N, ep.bias_vec, w[0]);
+        load_row<2>(ep.bias + group * ep.bias_stride, col, p.N, w[0]);
 #pragma unroll
         for (int k = 0; k < 4; ++k) x[0][k] += unpack<T>(w[0][k >> 1], k & 1);
       }
       if (ep.z != nullptr) {
         const uint32_t o[2] = {pack2<T>(x[0][0], x[0][1]), pack2<T>(x[0][2], x[0][3])};
-        store_row<2>(ep.z + (int64_t)row * ep.ldz, col, p.N, ep.z_vec, o);
+        store_row<2>(ep.z + (int64_t)row * ep.ldz, col, p.N, o);
       }
       apply_act(ep.act, x);
       if (ep.res != nullptr) {
-        load_row<2>(ep.res + (int64_t)row * ep.ldr, col, p.N, ep.res_vec, w[0]);
+        load_row<2>(ep.res + (int64_t)row * ep.ldr, col, p.N, w[0]);
 #pragma unroll
         for (int k = 0; k < 4; ++k) x[0][k] += unpack<T>(w[0][k >> 1], k & 1);
       }
@@ -335,7 +338,7 @@ __global__ __launch_bounds__(SMALL_THREADS) void gemm_small(
   v[1] = pack2<T>(s[2], s[3]);
   uint16_t* dst = p.D + (int64_t)row * p.ldd + col;
   if (p.d_vec && col + 4 <= p.N) {
-    *(u32x2*)dst = v;
+    *(u32x2_any*)dst = v;
   } else {
 #pragma unroll
     for (int e = 0; e < 4; ++e)

@@ -44,9 +44,12 @@ dense_gemm_status run_grouped(LayerCall c, const dense_gemm_groups& groups, void
   set_operands(p, c);
   p.tiles_n = (int)gp.tiles_n;
   p.group_m = choose_group_m(kMaxDim);
-  p.e = device_epilogue(c.e, 16);
+  p.e = device_epilogue(c.e);
   p.g = g;
-  if (gp.tile_m == BM / 2)
+  if (gp.tile_n == BN / 2)
+    hipLaunchKernelGGL((gemm_kernel<T, LAYOUT, false, BN / 2, BM / 2, true, true>), grid,
+                       dim3(THREADS), 0, c.stream, p);
+  else if (gp.tile_m == BM / 2)
     hipLaunchKernelGGL((gemm_kernel<T, LAYOUT, false, BN, BM / 2, true, true>), grid, dim3(THREADS), 0,
                        c.stream, p);
   else

@@ -5,17 +5,16 @@
 // Group g holds the rows ends[g - 1] .. ends[g] - 1 (ends[-1] = 0).  The ends
 // live on the device: they come from the routing of the tokens, and the host
 // need not wait for them.  So neither the number of output tiles nor their
-// place is known at launch; a workgroup finds the group of its next tile by
-// walking the groups (its tiles come in rising order, so it only ever walks
-// forwards).  Every end is clamped to [0, rows], and a group whose end lies
-// before its beginning is empty: whatever the array holds, no row outside
-// [0, rows) is addressed.
+// place is known at launch: each wave counts the groups' tiles once, one
+// group per lane, and keeps the running counts in registers; finding a
+// tile's group is then a compare and a ballot.  Every end is clamped to [0,
+// rows] and raised to the ends before it, so whatever the array holds, no row
+// outside [0, rows) is addressed, no row belongs to two groups, and the tiles
+// number no more than the host allowed for.
 #pragma once
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
-
-#include "tile_sched.h"
 
 namespace dg {
 
@@ -26,56 +25,16 @@ struct Groups {
   int64_t stride;  // elements between the groups' matrices (B, or D for A.T @ B)
 };
 
-// ends[i], clamped.  Read through the constant address space: i is the same
-// in every lane, so this is a scalar load, which waits for no vector-memory
+__device__ __forceinline__ int clamp_end(const Groups& g, int end) {
+  return min(max(end, 0), g.rows);
+}
+
+// ends[i], clamped, for an i that is the same in every lane: read through the
+// constant address space, a scalar load, which waits for no vector-memory
 // operation of the wave (the previous tile's stores keep draining).
 __device__ __forceinline__ int group_end(const Groups& g, int i) {
   typedef const __attribute__((address_space(4))) int32_t* const_ptr;
-  const int v = ((const_ptr)(uintptr_t)g.ends)[i];
-  return min(max(v, 0), g.rows);
-}
-
-// The group that holds an output tile, tiles numbered group by group.
-struct GroupWalk {
-  int g;         // current group
-  int first;     // number of its first tile
-  int beg, end;  // its rows
-  __device__ __forceinline__ void start(const Groups& gr) {
-    g = 0;
-    first = 0;
-    beg = 0;
-    end = group_end(gr, 0);
-  }
-  // Walks to the group of tile `task` (not before the current group); false
-  // if there is no such tile.
-  __device__ __forceinline__ bool find(const Groups& gr, int task, int tile_rows, int tiles_n) {
-    for (;;) {
-      const int here = end > beg ? (end - beg + tile_rows - 1) / tile_rows * tiles_n : 0;
-      if (task < first + here) return true;
-      first += here;
-      if (++g >= gr.count) return false;
-      beg = end;
-      end = group_end(gr, g);
-    }
-  }
-};
-
-// The tile of a workgroup when the launch holds one workgroup per possible
-// tile: workgroup b of the `total` that have a tile takes tile
-// xcd_slot(b, total) (tile_sched.h), so that neighbouring tiles run on one
-// XCD however many there are.  All lanes of a wave search together, 64
-// groups at a time.
-struct GroupTile {
-  int group, tile;  // the group, and the tile's number within it
-  int beg, end;     // the group's rows
-};
-
-__device__ __forceinline__ int lane_tiles(const Groups& gr, int i, int tile_rows, int tiles_n,
-                                          int* beg, int* end) {
-  const bool live = i < gr.count;
-  *end = live ? min(max(gr.ends[i], 0), gr.rows) : 0;
-  *beg = live && i > 0 ? min(max(gr.ends[i - 1], 0), gr.rows) : 0;
-  return *end > *beg ? (*end - *beg + tile_rows - 1) / tile_rows * tiles_n : 0;
+  return clamp_end(g, ((const_ptr)(uintptr_t)g.ends)[i]);
 }
 
 // The sum of x over this lane and those before it.
@@ -89,35 +48,96 @@ __device__ __forceinline__ int wave_scan(int x) {
   return x;
 }
 
-__device__ __forceinline__ bool find_tile(const Groups& gr, int b, int num_xcds, int tile_rows,
-                                          int tiles_n, GroupTile* out) {
+// The largest x of this lane and those before it.
+__device__ __forceinline__ int wave_max_scan(int x) {
   const int lane = (int)threadIdx.x & 63;
-  int total = 0, beg, end, mine, incl;
-  for (int c = 0; c < gr.count; c += 64) {
-    mine = lane_tiles(gr, c + lane, tile_rows, tiles_n, &beg, &end);
-    incl = wave_scan(mine);
-    total += __builtin_amdgcn_readlane(incl, 63);
+#pragma unroll
+  for (int d = 1; d < 64; d *= 2) {
+    const int y = __shfl_up(x, d);
+    if (lane >= d) x = max(x, y);
   }
-  if (b >= total) return false;
-  const int slot = xcd_slot(b, total, num_xcds);
-  int first = 0;
-  for (int c = 0; c < gr.count; c += 64) {
-    if (gr.count > 64) {  // (else the values of the only pass above still stand)
-      mine = lane_tiles(gr, c + lane, tile_rows, tiles_n, &beg, &end);
-      incl = wave_scan(mine);
-    }
-    const uint64_t past = __ballot(first + incl > slot);
-    if (past != 0) {
-      const int l = __builtin_ctzll(past);
-      out->group = c + l;
-      out->tile = slot - first - __builtin_amdgcn_readlane(incl - mine, l);
-      out->beg = __builtin_amdgcn_readlane(beg, l);
-      out->end = __builtin_amdgcn_readlane(end, l);
-      return true;
-    }
-    first += __builtin_amdgcn_readlane(incl, 63);
-  }
-  return false;
+  return x;
 }
+
+// A tile's place: its group, its number within the group, the group's rows.
+struct GroupTile {
+  int group, tile;
+  int beg, end;
+};
+
+// The running tile counts of the groups, tiles numbered group by group.  The
+// first 64 HELD groups stay in registers (lane l of register c holds group 64
+// c + l); those beyond are counted again from memory where a tile is looked
+// up among them.
+template <int HELD>
+struct GroupMap {
+  int incl[HELD];  // tiles of this lane's group and all before it
+  int end[HELD];   // the group's end
+  int total;       // tiles there are
+
+  // The tiles of this lane's group 64 c + lane, and its end; before: the end
+  // of group 64 c - 1.
+  __device__ __forceinline__ static int lane_tiles(const Groups& gr, int c, int before,
+                                                   int tile_rows, int tiles_n, int* e) {
+    const int lane = (int)threadIdx.x & 63, i = 64 * c + lane;
+    *e = wave_max_scan(max(before, i < gr.count ? clamp_end(gr, gr.ends[i]) : 0));
+    const int prev = __shfl_up(*e, 1);
+    const int rows = *e - (lane > 0 ? prev : before);
+    return (rows + tile_rows - 1) / tile_rows * tiles_n;
+  }
+
+  __device__ __forceinline__ void count(const Groups& gr, int tile_rows, int tiles_n) {
+    total = 0;
+    int before = 0;
+#pragma unroll
+    for (int c = 0; c < HELD; ++c) {
+      incl[c] = total;
+      end[c] = before;
+      if (64 * c < gr.count) {
+        incl[c] += wave_scan(lane_tiles(gr, c, before, tile_rows, tiles_n, &end[c]));
+        total = __builtin_amdgcn_readlane(incl[c], 63);
+        before = __builtin_amdgcn_readlane(end[c], 63);
+      }
+    }
+    for (int c = HELD; 64 * c < gr.count; ++c) {
+      int e;
+      total += __builtin_amdgcn_readlane(
+          wave_scan(lane_tiles(gr, c, before, tile_rows, tiles_n, &e)), 63);
+      before = __builtin_amdgcn_readlane(e, 63);
+    }
+  }
+
+  // Among 64 groups' counts and ends, with the count and end before them.
+  __device__ __forceinline__ static bool find_in(int incl, int end, int before, int beg, int c,
+                                                 int tile, GroupTile* out) {
+    const uint64_t past = __ballot(incl > tile);
+    if (past == 0) return false;
+    const int l = __builtin_ctzll(past);
+    out->group = 64 * c + l;
+    out->end = __builtin_amdgcn_readlane(end, l);
+    out->beg = l > 0 ? __builtin_amdgcn_readlane(end, l - 1) : beg;
+    out->tile = tile - (l > 0 ? __builtin_amdgcn_readlane(incl, l - 1) : before);
+    return true;
+  }
+
+  // The place of tile `tile` (below total).
+  __device__ __forceinline__ void find(const Groups& gr, int tile, int tile_rows, int tiles_n,
+                                       GroupTile* out) const {
+    int before = 0, beg = 0;
+#pragma unroll
+    for (int c = 0; c < HELD; ++c) {
+      if (find_in(incl[c], end[c], before, beg, c, tile, out)) return;
+      before = __builtin_amdgcn_readlane(incl[c], 63);
+      beg = __builtin_amdgcn_readlane(end[c], 63);
+    }
+    for (int c = HELD; 64 * c < gr.count; ++c) {
+      int e;
+      const int n = before + wave_scan(lane_tiles(gr, c, beg, tile_rows, tiles_n, &e));
+      if (find_in(n, e, before, beg, c, tile, out)) return;
+      before = __builtin_amdgcn_readlane(n, 63);
+      beg = __builtin_amdgcn_readlane(e, 63);
+    }
+  }
+};
 
 }  // namespace dg

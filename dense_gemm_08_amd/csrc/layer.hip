@@ -35,7 +35,7 @@ static dense_gemm_status enqueue_tiled(const LayerCall& c, const CallPlan& cp, f
   p.split_steps = (int)cp.plan[9];
   p.num_tasks = (int)(cp.full_tasks + cp.split_tiles * cp.plan[8]);
   p.ws = parts;
-  p.e = device_epilogue(c.e, 16);
+  p.e = device_epilogue(c.e);
   const dim3 grid((unsigned)(p.num_tasks < c.cus ? p.num_tasks : c.cus)), block(THREADS);
   if (p.splits > 1) {
     hipLaunchKernelGGL((gemm_kernel<T, LAYOUT, true, TN, TM, true>), grid, block, 0, c.stream, p);

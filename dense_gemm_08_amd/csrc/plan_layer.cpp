@@ -95,19 +95,38 @@ dense_gemm_status grouped_plan(int layout, int64_t M, int64_t N, int64_t K, cons
                                int64_t cus, GroupedPlan* out) {
   const int64_t K8 = round8(K), N8 = round8(N);
   // The ends are not known here: the tile follows the rows of an average
-  // group (of those that can have any).
+  // group (of those that can have any) and the number of tiles.  Measured
+  // with BF16, us per call:
+  //   * 256 x 256 against 128 x 128 tiles: 16 groups of 1024 rows, N = K =
+  //     4096, 413 against 571; of 256 rows 191 against 201; 32 of 512, N =
+  //     2048, 287 against 341; but 64 of 128 rows, N = K = 2048, 182 against
+  //     161, and 16 of 128, N = K = 4096, 187 against 153.
+  //   * A @ B also has 128 x 256 tiles (B's rows in longer pieces): 16 groups
+  //     of 128 rows, N = K = 4096, 133 against 150 in 128 x 128 tiles, where
+  //     they are enough for the CUs; 4 of 250, N = K = 512, 13.7 against 12.8.
+  //   * The small-output kernel splits K among its waves, which pays where
+  //     128 x 128 tiles would leave CUs idle or with one workgroup: A @ B.T
+  //     with 8 groups of 1 to 16 rows, N = K = 4096 (256 such tiles), 42 to
+  //     44 against 46 to 51; 32 groups, N = K = 2048 (512 tiles), 46 to 55
+  //     against 46 to 47.  Its A @ B tiles read B in 32-byte pieces: 8 groups
+  //     of one row, N = K = 4096, 51 against 44.
   const int64_t active = g.count < M ? g.count : M;
   const int64_t avg = (M + active - 1) / active;
-  out->small = avg <= SMALL_TILE;
+  const int64_t tiles128 = most_row_tiles(M, g.count, BM / 2) * ((N + BN / 2 - 1) / (BN / 2));
+  out->small = avg <= SMALL_TILE && tiles128 <= (layout == NT ? cus : cus / 2);
   if (out->small) {
     out->tile_m = out->tile_n = SMALL_TILE;
-  } else {
-    out->tile_m = avg <= 192 ? BM / 2 : BM;
+  } else if (avg > 192) {
+    out->tile_m = BM;
     out->tile_n = BN;
+  } else {
+    out->tile_m = BM / 2;
+    out->tile_n = layout == NN && (M + BM / 2 - 1) / (BM / 2) * ((N + BN - 1) / BN) >= cus ? BN : BN / 2;
   }
   out->tiles_n = (N + out->tile_n - 1) / out->tile_n;
   const int64_t most = most_row_tiles(M, g.count, out->tile_m) * out->tiles_n;
-  out->grid = out->small || most < cus ? most : cus;
+  const int64_t slots = cus * resident(out->tile_m, out->tile_n);
+  out->grid = out->small || most < slots ? most : slots;
   out->a_direct = K == 0 || (aligned16(A) && (lda & 7) == 0 && (K & 7) == 0);
   out->b_direct = K == 0 || (aligned16(B) && (ldb & 7) == 0 && (g.stride & 7) == 0 &&
                              ((layout == NT ? K : N) & 7) == 0);
@@ -138,7 +157,8 @@ dense_gemm_status tn_validate(int fmt, int64_t M, int64_t N, int64_t K, const vo
   if (M >= kMaxDim || N >= kMaxDim || K >= kMaxDim) return DENSE_GEMM_TOO_LARGE;
   // task numbers are 32-bit
   int64_t tasks;
-  if (__builtin_mul_overflow(((M + BM - 1) / BM) * ((N + BN - 1) / BN), groups, &tasks) ||
+  const int64_t tile = BM / 2;  // the smaller
+  if (__builtin_mul_overflow(((M + tile - 1) / tile) * ((N + tile - 1) / tile), groups, &tasks) ||
       tasks >= kMaxDim)
     return DENSE_GEMM_TOO_LARGE;
   if (D == nullptr || (K > 0 && (A == nullptr || B == nullptr))) return DENSE_GEMM_NULL_PTR;
@@ -163,29 +183,74 @@ dense_gemm_status tn_validate(int fmt, int64_t M, int64_t N, int64_t K, const vo
   return DENSE_GEMM_OK;
 }
 
+// One way to run D = A.T @ B, and its estimated time in 0.01 us, by a model
+// fitted to times on the MI355X (BF16):
+//   * 256 x 256 tiles, one workgroup per CU: waves x (133 per K step + 850);
+//     split-K as for the other products (choose_split: 105, 1200, 12; a split
+//     last wave costs 2500 on top of its steps);
+//   * 128 x 128 tiles, two per CU: waves x (90 per K step + 360), or 50 per
+//     step where each has a CU to itself; split-K only then (1000 for the
+//     second kernel, 1 per partial tile).
+// Measured 256 against 128, us: 4096 x 4096 x 2048 64 against 69; 4096 x 2304
+// x 4096 93 against 111, 4096 x 2048 x 4096 93 against 64 (512 of the smaller
+// tiles: just one wave); 2048 x 2048 x 8192 in 4 parts 77 against 73; 512 x
+// 640 x 20011 in 32 parts 38, in 12 parts of the smaller 26; 40 groups of 75
+// rows, 520 x 1000, 25 against 20; 16 of 1024, 4096 x 4096, 483 against 593.
+struct TnChoice {
+  int64_t tile, splits, steps;
+  double cost;
+};
+
+static TnChoice tn_choice(int64_t M, int64_t N, int64_t nk, int64_t groups, bool grouped,
+                          int64_t cus, int64_t tile) {
+  TnChoice c = {tile, 1, nk, 0.0};
+  const int64_t tasks = ((M + tile - 1) / tile) * ((N + tile - 1) / tile) * groups;
+  const int64_t slots = cus * resident(tile, tile);
+  const int64_t waves = (tasks + slots - 1) / slots;
+  // Parts against few tiles.  With groups they also even out the groups'
+  // lengths, so they are chosen as for a group of twice the average; a last
+  // wave is not split (which tiles it holds is not known here).
+  const int64_t reach = grouped ? 2 * nk : nk;
+  if (tile == BM) {
+    const int64_t last = tasks % cus;
+    if (!grouped || tasks < cus)
+      choose_split(tasks, reach, cus, 105, 1200, 12, BM / 16, &c.splits, &c.steps);
+    c.cost = (double)waves * (133 * nk + 850);
+    if (c.splits > 1)
+      c.cost = (double)(waves - 1) * (133 * nk + 850) + 133 * ((nk + c.splits - 1) / c.splits) + 850 + 2500 +
+               (tasks < cus ? 12 * c.splits * last - 1300 : 0);
+  } else if (tasks < cus) {
+    choose_split(tasks, reach, cus, 50, 1000, 1, BM / 16, &c.splits, &c.steps);
+    c.cost = 50 * ((nk + c.splits - 1) / c.splits) + 360 +
+             (c.splits > 1 ? 1000 + c.splits * tasks : 0);
+  } else {
+    c.cost = (double)waves * (90 * nk + 360);
+  }
+  return c;
+}
+
 dense_gemm_status tn_plan(int64_t M, int64_t N, int64_t K, const void* A, int64_t lda,
                           const void* B, int64_t ldb, const dense_gemm_groups* g, int64_t cus,
                           TnPlan* out) {
-  out->tiles_m = (M + BM - 1) / BM;
-  out->tiles_n = (N + BN - 1) / BN;
   out->groups = g != nullptr ? g->count : 1;
-  const int64_t tasks = out->tiles_m * out->tiles_n * out->groups;
-  // Split-K by the tiled kernel's model (choose_split).  With groups, the
-  // parts are chosen for a group of average length, and only where there are
-  // fewer tiles than CUs: how the tiles' work falls on a last wave is not
-  // known here.
+  // With groups, the plan is made for groups of average length (of those
+  // that can have rows).
   int64_t rows = K;
   if (g != nullptr) {
     const int64_t active = g->count < K ? g->count : K;
     rows = active > 0 ? (K + active - 1) / active : 0;
   }
   const int64_t nk = (rows + BK - 1) / BK;
-  out->splits = 1;
-  out->steps = nk;
-  if (g == nullptr || tasks < cus)
-    choose_split(tasks, nk, cus, 105, 1200, 12, BM / 16, &out->splits, &out->steps);
-  out->full_tasks = tasks;
-  if (out->splits > 1) out->full_tasks = tasks < cus ? 0 : tasks - tasks % cus;
+  const TnChoice wide = tn_choice(M, N, nk, out->groups, g != nullptr, cus, BM);
+  const TnChoice narrow = tn_choice(M, N, nk, out->groups, g != nullptr, cus, BM / 2);
+  const TnChoice& best = narrow.cost < wide.cost ? narrow : wide;
+  out->tile = best.tile;
+  out->tiles_m = (M + best.tile - 1) / best.tile;
+  out->tiles_n = (N + best.tile - 1) / best.tile;
+  out->splits = best.splits;
+  out->steps = best.steps;
+  const int64_t tasks = out->tiles_m * out->tiles_n * out->groups;
+  out->full_tasks = best.splits == 1 ? tasks : tasks < cus ? 0 : tasks - tasks % cus;
   out->split_tiles = tasks - out->full_tasks;
   out->a_direct = K == 0 || (aligned16(A) && (lda & 7) == 0 && (M & 7) == 0);
   out->b_direct = K == 0 || (aligned16(B) && (ldb & 7) == 0 && (N & 7) == 0);
@@ -193,9 +258,10 @@ dense_gemm_status tn_plan(int64_t M, int64_t N, int64_t K, const void* A, int64_
   if (!out->a_direct && !matrix_bytes(K, round8(M), &out->a_bytes)) return DENSE_GEMM_TOO_LARGE;
   if (!out->b_direct && !matrix_bytes(K, round8(N), &out->b_bytes)) return DENSE_GEMM_TOO_LARGE;
   if (out->splits > 1) {
-    // (at most one part per CU: no overflow)
-    out->split_bytes = (size_t)(out->splits * out->split_tiles) * BM * BN * sizeof(float);
-    out->sums_bytes = (size_t)(out->splits * out->split_tiles) * BM * sizeof(float);
+    // (at most one part per resident workgroup: no overflow)
+    out->split_bytes =
+        (size_t)(out->splits * out->split_tiles) * out->tile * out->tile * sizeof(float);
+    out->sums_bytes = (size_t)(out->splits * out->split_tiles) * out->tile * sizeof(float);
   }
   return DENSE_GEMM_OK;
 }

@@ -11,6 +11,12 @@
 
 namespace dg {
 
+// Workgroups that a CU holds at a time: the kernels with 128 x 128 tiles are
+// built for two.
+constexpr int64_t resident(int64_t tile_m, int64_t tile_n) {
+  return tile_m == BM / 2 && tile_n == BN / 2 ? 2 : 1;
+}
+
 // A call of dense_gemm_layer with row groups.
 struct GroupedPlan {
   bool small;                // the small-output kernel
@@ -25,6 +31,7 @@ struct GroupedPlan {
 // A call of dense_gemm_tn.  The tiles of the groups' outputs (of the one
 // output, without groups) form one sequence, `tiles_m * tiles_n` a group.
 struct TnPlan {
+  int64_t tile;              // tiles of tile x tile: 256 or 128
   int64_t tiles_m, tiles_n, groups;
   int64_t full_tasks;        // tiles computed whole
   int64_t split_tiles;       // tiles computed in K parts

@@ -68,13 +68,19 @@ __global__ __launch_bounds__(RT) void split_reduce(
     const int group = (p.full_tasks + st) / per;
     tile_of_task(p.full_tasks + st - group * per, p.tiles_m, p.tiles_n, p.group_m, &tm, &tn);
     D += group * p.stride;
-    if (p.colsum != nullptr && tn == 0 && blockIdx.x % WPT == 0) {
-      for (int c = (int)threadIdx.x; c < TM && tm * TM + c < p.M; c += RT) {
-        float s = 0.0f;
-        for (int k = 0; k < p.splits; ++k)
-          s += p.colsum_ws[((size_t)k * p.tiles + st) * TM + c];
+    if (p.colsum != nullptr && tn == 0) {
+      // the tile's workgroups share its TM columns, LPC lanes each: a lane
+      // adds every LPC-th part, then the lanes add up in a fixed tree
+      constexpr int LPC = RT * WPT / TM;
+      static_assert(LPC == 16 || LPC == 32, "lanes per column");
+      const int c = (blockIdx.x % WPT) * (RT / LPC) + (int)threadIdx.x / LPC;
+      float s = 0.0f;
+      for (int k = (int)threadIdx.x % LPC; k < p.splits; k += LPC)
+        s += p.colsum_ws[((size_t)k * p.tiles + st) * TM + c];
+#pragma unroll
+      for (int d = LPC / 2; d > 0; d /= 2) s += __shfl_xor(s, d);
+      if (threadIdx.x % LPC == 0 && tm * TM + c < p.M)
         p.colsum[(int64_t)group * p.M + tm * TM + c] = (uint16_t)pack2<T>(s, 0.0f);
-      }
     }
   } else {
     tile_of_task(p.full_tasks + st, p.tiles_m, p.tiles_n, p.group_m, &tm, &tn);
@@ -119,11 +125,11 @@ __global__ __launch_bounds__(RT) void split_reduce(
 #pragma unroll
     for (int e = 0; e < 8; ++e) x[0][e] = s[e];
     if (ep.grad) {
-      load_row<4>(ep.z + (int64_t)row * ep.ldz, col, p.N, ep.z_vec, w[0]);
+      load_row<4>(ep.z + (int64_t)row * ep.ldz, col, p.N, w[0]);
       apply_slope<T>(ep.act, x, w);
     } else {
       if (ep.bias != nullptr) {
-        load_row<4>(ep.bias, col, p.N, ep.bias_vec, w[0]);
+        load_row<4>(ep.bias, col, p.N, w[0]);
 #pragma unroll
         for (int e = 0; e < 8; ++e) x[0][e] += unpack<T>(w[0][e >> 1], e & 1);
       }
@@ -131,11 +137,11 @@ __global__ __launch_bounds__(RT) void split_reduce(
         uint32_t o[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[e] = pack2<T>(x[0][2 * e], x[0][2 * e + 1]);
-        store_row<4>(ep.z + (int64_t)row * ep.ldz, col, p.N, ep.z_vec, o);
+        store_row<4>(ep.z + (int64_t)row * ep.ldz, col, p.N, o);
       }
       apply_act(ep.act, x);
       if (ep.res != nullptr) {
-        load_row<4>(ep.res + (int64_t)row * ep.ldr, col, p.N, ep.res_vec, w[0]);
+        load_row<4>(ep.res + (int64_t)row * ep.ldr, col, p.N, w[0]);
 #pragma unroll
         for (int e = 0; e < 8; ++e) x[0][e] += unpack<T>(w[0][e >> 1], e & 1);
       }
@@ -148,7 +154,7 @@ __global__ __launch_bounds__(RT) void split_reduce(
   for (int e = 0; e < 4; ++e) v[e] = pack2<T>(s[2 * e], s[2 * e + 1]);
   uint16_t* dst = D + (int64_t)row * p.ldd + col;
   if (p.d_vec && col + 8 <= p.N) {
-    __builtin_nontemporal_store(v, (u32x4*)dst);
+    __builtin_nontemporal_store(v, (u32x4_any*)dst);
   } else {
 #pragma unroll
     for (int e = 0; e < 8; ++e)

@@ -10,19 +10,27 @@
 
 namespace dg {
 
-template <typename T, bool GROUP, bool SUMS>
-static dense_gemm_status enqueue_tn(const LayerParams& p, const LayerReduceParams& r, int cus,
-                                    hipStream_t stream) {
-  const dim3 grid((unsigned)(p.num_tasks < cus ? p.num_tasks : cus)), block(THREADS);
+template <typename T, int TILE, bool GROUP, bool SUMS>
+static dense_gemm_status enqueue_tile(const LayerParams& p, const LayerReduceParams& r, int cus,
+                                      hipStream_t stream) {
+  const int slots = cus * (int)resident(TILE, TILE);
+  const dim3 grid((unsigned)(p.num_tasks < slots ? p.num_tasks : slots)), block(THREADS);
   if (p.splits > 1) {
-    hipLaunchKernelGGL((gemm_kernel<T, TA, true, BN, BM, false, GROUP, SUMS>), grid, block, 0, stream,
-                       p);
-    enqueue_split_reduce<T, BN, BM>(r, cus, stream);
+    hipLaunchKernelGGL((gemm_kernel<T, TA, true, TILE, TILE, false, GROUP, SUMS>), grid, block, 0,
+                       stream, p);
+    enqueue_split_reduce<T, TILE, TILE>(r, cus, stream);
   } else {
-    hipLaunchKernelGGL((gemm_kernel<T, TA, false, BN, BM, false, GROUP, SUMS>), grid, block, 0, stream,
-                       p);
+    hipLaunchKernelGGL((gemm_kernel<T, TA, false, TILE, TILE, false, GROUP, SUMS>), grid, block, 0,
+                       stream, p);
   }
   return launched();
+}
+
+template <typename T, bool GROUP, bool SUMS>
+static dense_gemm_status enqueue_tn(int64_t tile, const LayerParams& p, const LayerReduceParams& r,
+                                    int cus, hipStream_t stream) {
+  return tile == BM ? enqueue_tile<T, BM, GROUP, SUMS>(p, r, cus, stream)
+                    : enqueue_tile<T, BM / 2, GROUP, SUMS>(p, r, cus, stream);
 }
 
 template <typename T>
@@ -63,7 +71,6 @@ static dense_gemm_status run_tn(LayerCall c, void* colsum, const dense_gemm_grou
   }
   if (groups != nullptr) {
     p.g = {(const int32_t*)groups->ends, (int)groups->count, (int)c.K, groups->stride};
-    p.d_vec = p.d_vec && wide(c.D, groups->stride, 16);
   }
   LayerReduceParams r = {};
   (ReduceParams&)r = {p.D, p.ws, p.M, p.N, p.ldd, p.tiles_m, p.tiles_n, p.group_m,
@@ -72,10 +79,10 @@ static dense_gemm_status run_tn(LayerCall c, void* colsum, const dense_gemm_grou
   r.colsum = p.colsum;
   r.colsum_ws = p.colsum_ws;
   if (groups != nullptr)
-    return colsum != nullptr ? enqueue_tn<T, true, true>(p, r, c.cus, c.stream)
-                             : enqueue_tn<T, true, false>(p, r, c.cus, c.stream);
-  return colsum != nullptr ? enqueue_tn<T, false, true>(p, r, c.cus, c.stream)
-                           : enqueue_tn<T, false, false>(p, r, c.cus, c.stream);
+    return colsum != nullptr ? enqueue_tn<T, true, true>(tp.tile, p, r, c.cus, c.stream)
+                             : enqueue_tn<T, true, false>(tp.tile, p, r, c.cus, c.stream);
+  return colsum != nullptr ? enqueue_tn<T, false, true>(tp.tile, p, r, c.cus, c.stream)
+                           : enqueue_tn<T, false, false>(tp.tile, p, r, c.cus, c.stream);
 }
 
 }  // namespace dg

@@ -370,9 +370,9 @@ typedef struct dense_gemm_epilogue {
  * matrices of neighbouring groups: of B for dense_gemm_layer (0: one matrix
  * for all), of D for dense_gemm_tn.  The ends are read by the kernels, after
  * the work before the call on `stream`; the host never sees them.  Each is
- * clamped to the number of rows, so no array of ends leads outside the
- * operands; where the ends decrease, the rows that several groups name hold
- * one of those groups' results or another, and rows may be left out. */
+ * clamped to [0, the number of rows], so no array of ends leads outside the
+ * operands (dense_gemm_layer also raises each to the ends before it; what
+ * dense_gemm_tn sums where the ends decrease is unspecified). */
 typedef struct dense_gemm_groups {
   const void* ends;
   int64_t count;

@@ -176,14 +176,22 @@ def test_tn_workspace():
     assert tn_bytes(4096, 4096, 4096) == 0
     assert tn_bytes(4096, 4096, 4096, A=258) == 4096 * 4096 * 2
     assert tn_bytes(4097, 4096, 64) == up256(64 * 4104 * 2)
-    # two tiles, long K: partial tiles and their column sums, at most one per CU
+    # few tiles, long K: 128 x 128 partial tiles and their column sums, at
+    # most one per CU
     n = tn_bytes(256, 512, 65536)
-    per = 256 * 256 * 4 + 256 * 4
-    assert n % per == 0 and 2 < n // per <= 256
-    # groups: as many tiles as groups, split for an average group's rows
+    per = 128 * 128 * 4 + 128 * 4
+    assert n % per == 0 and 8 < n // per <= 256
+    # groups, split for their average length
     n = tn_bytes(256, 256, 65536, groups=Gr(count=4))
-    assert n % per == 0 and 4 < n // per <= 256
+    assert n % per == 0 and 16 < n // per <= 256
     assert tn_bytes(256, 256, 512, groups=Gr(count=300)) == 0
+    # a last wave of 256 x 256 tiles (16 of 272) in parts
+    n = tn_bytes(4096, 4352, 4096)
+    per = 256 * 256 * 4 + 256 * 4
+    assert n % per == 0 and 16 < n // per <= 256
+    # sizes near the limits plan without overflow on any device
+    for cus in (1, 256, 1 << 30):
+        tn_bytes((1 << 22) - 8, (1 << 22) - 8, (1 << 31) - 8, cus=cus)
 
 
 def test_size_queries_refuse_bad_arguments():
