@@ -103,7 +103,7 @@ SIGNATURES = {
                                          ctypes.POINTER(ctypes.c_size_t)], _i32),
     "dense_gemm_tn": ([_i32] + _GEMM_ARGS[:-1] + [_vp, ctypes.POINTER(Groups), _vp,
                                                  ctypes.c_size_t, _vp], _i32),
-    "dense_gemm_tn_workspace_size": ([_i64, _i64, _i64, _vp, _i64, _vp, _i64,
+    "dense_gemm_tn_workspace_size": ([_i64, _i64, _i64, _vp, _i64, _vp, _i64, _i32,
                                       ctypes.POINTER(Groups), _i64,
                                       ctypes.POINTER(ctypes.c_size_t)], _i32),
     "gemm_nt_e4m3_mx_ex": ([_i64, _i64, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp,
@@ -607,7 +607,8 @@ def _tn(A, B, ends, D, colsum, stream, workspace):
     args = (M, N, K, A.data_ptr(), _ld(A), B.data_ptr(), _ld(B))
 
     def size_of(need):
-        return lib.dense_gemm_tn_workspace_size(*args, groups, 0, ctypes.byref(need))
+        return lib.dense_gemm_tn_workspace_size(*args, sums is not None, groups, 0,
+                                                ctypes.byref(need))
 
     _launch("dense_gemm_tn",
             (fmt[1],) + args + (D.data_ptr(), ldd, None if sums is None else sums.data_ptr(), groups),

@@ -1,0 +1,62 @@
+// column_sums.h -- the last step of the column sums of A that accompany D =
+// A.T @ B on the MI355X (gfx950): gemm_kernel<..., SUMS> leaves FP32 sums over
+// shares of K, here they are added in a fixed order and rounded once.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "cdna_ops.h"
+
+namespace dg {
+
+struct ColumnSumsParams {
+  const float* ws;  // two rows of TM sums per task
+  uint16_t* out;    // groups x M
+  int M, groups;
+  int tiles_m, tiles_n, group_m;
+  // tasks below full_tasks are whole tiles, then come `splits` parts of each
+  // of the last `tiles` tiles (gemm_kernel.h: Params)
+  int full_tasks, splits, tiles;
+};
+
+// A workgroup adds 16 columns of one group (M / 16 x groups workgroups): 16
+// lanes hold the columns of a row of sums, and the 16 rows of lanes take
+// every 16th of the rows of sums that the column's tiles left; their sums
+// are then added through LDS in order.  Bound by the latency of a few loads.
+constexpr int CS_COLS = 16, CS_LANES = 16;
+template <typename T, int TM>
+__global__ __launch_bounds__(CS_COLS* CS_LANES) void column_sums(ColumnSumsParams p) {
+  __shared__ float part[CS_LANES][CS_COLS];
+  const int per_group = (p.M + CS_COLS - 1) / CS_COLS;
+  const int g = blockIdx.x / per_group;
+  const int c = (int)threadIdx.x % CS_COLS, r = (int)threadIdx.x / CS_COLS;
+  const int m = (blockIdx.x - g * per_group) * CS_COLS + c;
+  const int tm = m / TM;
+  // tile (tm, tn) of the group in the grouped order (tile_sched.h)
+  const int first_m = tm / p.group_m * p.group_m;
+  const int gsize = min(p.group_m, p.tiles_m - first_m);
+  const int tile0 = g * p.tiles_m * p.tiles_n + first_m * p.tiles_n + tm - first_m;
+  float s = 0.0f;
+  if (m < p.M) {
+    const int rows = p.tiles_n * 2 * p.splits;
+    for (int i = r; i < rows; i += CS_LANES) {
+      const int tn = i / (2 * p.splits), k = i % (2 * p.splits) / 2;
+      const int tile = tile0 + tn * gsize;
+      const bool whole = tile < p.full_tasks;
+      if (whole && k > 0) continue;
+      const int64_t task = whole ? tile : (int64_t)k * p.tiles + tile;
+      s += p.ws[(task * 2 + i % 2) * TM + m % TM];
+    }
+  }
+  part[r][c] = s;
+  __syncthreads();
+  if (r == 0 && m < p.M) {
+    s = part[0][c];
+#pragma unroll
+    for (int i = 1; i < CS_LANES; ++i) s += part[i][c];
+    p.out[(int64_t)g * p.M + m] = (uint16_t)pack2<T>(s, 0.0f);
+  }
+}
+
+}  // namespace dg

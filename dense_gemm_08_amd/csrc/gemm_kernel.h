@@ -87,14 +87,12 @@ struct Params {
 };
 
 // What the products of a layer (layer.hip) add: the epilogue's operands
-// (epilogue.h), the row groups (groups.h) and the column sums of A (SUMS;
-// groups x M in the output type): stored by the tiles of the first tile
-// column; a part of a split tile writes its TM sums in FP32 at colsum_ws +
-// (its partial tile's index) * TM.
+// (epilogue.h), the row groups (groups.h) and the column sums of A (SUMS):
+// each task leaves its two wave columns' FP32 sums of its TM columns at
+// colsum_ws + task * 2 TM (added up by column_sums, column_sums.h).
 struct LayerParams : Params {
   Epilogue e;
   Groups g;
-  uint16_t* colsum;
   float* colsum_ws;
 };
 
@@ -471,14 +469,20 @@ __global__ __launch_bounds__(THREADS, (two_per_cu<LAYOUT, TN, TM, EPI, GROUP>())
     wait_vm_barrier<DMA_PER_OPERAND + DMA_B>();
     read_frags(0, 0, 0, F0);
 
-    // Column sums of A: lane (l16, lq) adds the eight k of its part of each A
-    // fragment, in the shadow of the MFMAs that use it.  Every tile does so
-    // though only the first tile column keeps the sums: a branch in the loop
-    // would end the basic block that the fences order.
+    // Column sums of A: a lane adds the eight k that it holds of each A
+    // fragment.  All tiles of a tile row read the same A, so they share the
+    // K steps: step ks is added by wave column ks mod (2 tiles_n) of the
+    // row's 2 tiles_n (two to a tile), between the substeps, where both
+    // substeps' fragments are at hand.  (One v_dot2c per fragment word in
+    // every tile and step took 8 to 12% of 5120 x 8192 x 8192; a branch per
+    // step costs nothing measurable.)
     [[maybe_unused]] float cs[MI];
+    [[maybe_unused]] int sum_at = 0;
     if constexpr (SUMS) {
 #pragma unroll
       for (int i = 0; i < MI; ++i) cs[i] = 0.0f;
+      const int period = 2 * p.tiles_n;
+      sum_at = kbeg + (2 * tn + wn + period - kbeg % period) % period;
     }
     int es = 0;  // early-ring slot of stage ks
     for (int ks = kbeg; ks < kend; ++ks) {
@@ -490,13 +494,25 @@ __global__ __launch_bounds__(THREADS, (two_per_cu<LAYOUT, TN, TM, EPI, GROUP>())
       for (int q = 0; q < PAIRS; ++q) {
         share(q, PAIRS, READS, [&](int f) { read_item(es, ls, 1, F1, f); });
         mfma_pair(F0, q);
-        if constexpr (SUMS)
-          share(q, PAIRS, 4 * MI, [&](int i) { cs[i >> 2] = sum2<T>(cs[i >> 2], F0.a[i >> 2][i & 3]); });
         fence();
         // (the descriptor's scalar work goes behind the first MFMAs)
         if (q == 0) he = half_setup(ks + 2, es2, EARLY);
         // stages from the third on start at k >= 0: no masks
         share(q, PAIRS, DMA_E, [&](int i) { refill_one(he, EARLY, i, false); });
+      }
+      if constexpr (SUMS) {
+        if (ks == sum_at) {
+          sum_at += 2 * p.tiles_n;
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+#pragma unroll
+            for (int i = 0; i < MI; ++i) cs[i] = sum2<T>(cs[i], F0.a[i][k]);
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+#pragma unroll
+            for (int i = 0; i < MI; ++i) cs[i] = sum2<T>(cs[i], F1.a[i][k]);
+        }
+        fence();
       }
       const Half hl = half_setup(ks + 2, ls, 1 - EARLY);
 #pragma unroll
@@ -508,8 +524,6 @@ __global__ __launch_bounds__(THREADS, (two_per_cu<LAYOUT, TN, TM, EPI, GROUP>())
         if (q >= BAR_PAIR)
           share(q - BAR_PAIR, PAIRS - BAR_PAIR, READS, [&](int f) { read_item(es1, ls ^ 1, 0, F0, f); });
         mfma_pair(F1, q);
-        if constexpr (SUMS)
-          share(q, PAIRS, 4 * MI, [&](int i) { cs[i >> 2] = sum2<T>(cs[i >> 2], F1.a[i >> 2][i & 3]); });
         fence();
         if (q >= BAR_PAIR)
           share(q - BAR_PAIR, PAIRS - BAR_PAIR, DMA_L,
@@ -524,21 +538,15 @@ __global__ __launch_bounds__(THREADS, (two_per_cu<LAYOUT, TN, TM, EPI, GROUP>())
     fence();
 
     if constexpr (SUMS) {
-      if (tn == 0 && wn == 0) {
-        // the four lane groups' parts of each column, added in a fixed order
+      // the four lane groups' sums of each column, added in a fixed order;
+      // column_sums adds those of the tile row's wave columns
+      float* w = p.colsum_ws + ((size_t)task * 2 + wn) * TM + wm * WTM;
 #pragma unroll
-        for (int i = 0; i < MI; ++i) {
-          float s = cs[i];
-          s += __shfl_xor(s, 16);
-          s += __shfl_xor(s, 32);
-          const int c = wm * WTM + 16 * i + l16;  // column of the tile
-          if (lq == 0 && c < vm) {
-            if (part)
-              p.colsum_ws[(size_t)(split * p.tiles + u % p.tiles) * TM + c] = s;
-            else
-              p.colsum[(int64_t)group * p.M + m0 + c] = (uint16_t)pack2<T>(s, 0.0f);
-          }
-        }
+      for (int i = 0; i < MI; ++i) {
+        float s = cs[i];
+        s += __shfl_xor(s, 16);
+        s += __shfl_xor(s, 32);
+        if (lq == 0) w[16 * i + l16] = s;
       }
     }
 

@@ -161,6 +161,9 @@ dense_gemm_status tn_validate(int fmt, int64_t M, int64_t N, int64_t K, const vo
   if (__builtin_mul_overflow(((M + tile - 1) / tile) * ((N + tile - 1) / tile), groups, &tasks) ||
       tasks >= kMaxDim)
     return DENSE_GEMM_TOO_LARGE;
+  // and so are the workgroups of 16 column sums each
+  if (colsum != nullptr && (__builtin_mul_overflow((M + 15) / 16, groups, &tasks) || tasks >= kMaxDim))
+    return DENSE_GEMM_TOO_LARGE;
   if (D == nullptr || (K > 0 && (A == nullptr || B == nullptr))) return DENSE_GEMM_NULL_PTR;
   if (ldd < N || (K > 0 && (lda < M || ldb < N))) return DENSE_GEMM_BAD_LD;
   if (((uintptr_t)D & 1) != 0 || ((uintptr_t)colsum & 1) != 0) return DENSE_GEMM_MISALIGNED;
@@ -230,8 +233,8 @@ static TnChoice tn_choice(int64_t M, int64_t N, int64_t nk, int64_t groups, bool
 }
 
 dense_gemm_status tn_plan(int64_t M, int64_t N, int64_t K, const void* A, int64_t lda,
-                          const void* B, int64_t ldb, const dense_gemm_groups* g, int64_t cus,
-                          TnPlan* out) {
+                          const void* B, int64_t ldb, bool colsum, const dense_gemm_groups* g,
+                          int64_t cus, TnPlan* out) {
   out->groups = g != nullptr ? g->count : 1;
   // With groups, the plan is made for groups of average length (of those
   // that can have rows).
@@ -261,8 +264,10 @@ dense_gemm_status tn_plan(int64_t M, int64_t N, int64_t K, const void* A, int64_
     // (at most one part per resident workgroup: no overflow)
     out->split_bytes =
         (size_t)(out->splits * out->split_tiles) * out->tile * out->tile * sizeof(float);
-    out->sums_bytes = (size_t)(out->splits * out->split_tiles) * out->tile * sizeof(float);
   }
+  if (colsum)
+    out->sums_bytes = (size_t)(out->full_tasks + out->splits * out->split_tiles) * 2 * out->tile *
+                      sizeof(float);
   return DENSE_GEMM_OK;
 }
 

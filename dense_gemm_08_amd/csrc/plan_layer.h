@@ -39,7 +39,7 @@ struct TnPlan {
   bool a_direct, b_direct;
   size_t a_bytes, b_bytes;
   size_t split_bytes;        // FP32 partial tiles
-  size_t sums_bytes;         // their column sums
+  size_t sums_bytes;         // the tasks' column sums of A
   size_t total() const { return a_bytes + b_bytes + split_bytes + sums_bytes; }
 };
 
@@ -60,7 +60,7 @@ dense_gemm_status tn_validate(int fmt, int64_t M, int64_t N, int64_t K, const vo
                               const void* colsum, const dense_gemm_groups* g, bool* done);
 
 dense_gemm_status tn_plan(int64_t M, int64_t N, int64_t K, const void* A, int64_t lda,
-                          const void* B, int64_t ldb, const dense_gemm_groups* g, int64_t cus,
-                          TnPlan* out);
+                          const void* B, int64_t ldb, bool colsum, const dense_gemm_groups* g,
+                          int64_t cus, TnPlan* out);
 
 }  // namespace dg

@@ -32,16 +32,12 @@ struct ReduceParams {
   int d_vec;  // D rows are 16-byte aligned (16-byte stores allowed)
 };
 
-// For a layer's products (layer.hip): the epilogue applied to the sums, and
-// for A.T @ B over row groups (`groups` of them; tile t of the order is tile
-// t % (tiles_m * tiles_n) of group t / that, in a D of its own) the column
-// sums of A: each part of a split tile in the first tile column left TM
-// FP32 sums at colsum_ws + (part * tiles + st) * TM.
+// For a layer's products (layer.hip, tn.hip): the epilogue applied to the
+// sums, and for A.T @ B over row groups one D per group (tile t of the order
+// is tile t % (tiles_m * tiles_n) of group t / that).
 struct LayerReduceParams : ReduceParams {
   Epilogue e;
-  int64_t stride;        // elements between the groups' D
-  const float* colsum_ws;
-  uint16_t* colsum;      // groups x M, or null
+  int64_t stride;  // elements between the groups' D
 };
 
 // One thread per 8 consecutive columns of a row, RT threads per workgroup:
@@ -68,20 +64,6 @@ __global__ __launch_bounds__(RT) void split_reduce(
     const int group = (p.full_tasks + st) / per;
     tile_of_task(p.full_tasks + st - group * per, p.tiles_m, p.tiles_n, p.group_m, &tm, &tn);
     D += group * p.stride;
-    if (p.colsum != nullptr && tn == 0) {
-      // the tile's workgroups share its TM columns, LPC lanes each: a lane
-      // adds every LPC-th part, then the lanes add up in a fixed tree
-      constexpr int LPC = RT * WPT / TM;
-      static_assert(LPC == 16 || LPC == 32, "lanes per column");
-      const int c = (blockIdx.x % WPT) * (RT / LPC) + (int)threadIdx.x / LPC;
-      float s = 0.0f;
-      for (int k = (int)threadIdx.x % LPC; k < p.splits; k += LPC)
-        s += p.colsum_ws[((size_t)k * p.tiles + st) * TM + c];
-#pragma unroll
-      for (int d = LPC / 2; d > 0; d /= 2) s += __shfl_xor(s, d);
-      if (threadIdx.x % LPC == 0 && tm * TM + c < p.M)
-        p.colsum[(int64_t)group * p.M + tm * TM + c] = (uint16_t)pack2<T>(s, 0.0f);
-    }
   } else {
     tile_of_task(p.full_tasks + st, p.tiles_m, p.tiles_n, p.group_m, &tm, &tn);
   }

@@ -5,39 +5,54 @@
 // the tiled one with layout TA (gemm_kernel.h): A and B both have k as their
 // row, so their tiles are 64 k rows of 512 bytes and both operands' MFMA
 // fragments come from transposing LDS reads.
+#include "column_sums.h"
 #include "layer_host.h"
 #include "split_reduce.h"
 
 namespace dg {
 
 template <typename T, int TILE, bool GROUP, bool SUMS>
-static dense_gemm_status enqueue_tile(const LayerParams& p, const LayerReduceParams& r, int cus,
-                                      hipStream_t stream) {
+static void enqueue_tile(const LayerParams& p, int cus, hipStream_t stream) {
   const int slots = cus * (int)resident(TILE, TILE);
   const dim3 grid((unsigned)(p.num_tasks < slots ? p.num_tasks : slots)), block(THREADS);
   if (p.splits > 1) {
     hipLaunchKernelGGL((gemm_kernel<T, TA, true, TILE, TILE, false, GROUP, SUMS>), grid, block, 0,
                        stream, p);
+    LayerReduceParams r = {};
+    (ReduceParams&)r = {p.D, p.ws, p.M, p.N, p.ldd, p.tiles_m, p.tiles_n, p.group_m,
+                        p.full_tasks, p.splits, p.tiles, p.d_vec};
+    r.stride = p.g.stride;
     enqueue_split_reduce<T, TILE, TILE>(r, cus, stream);
   } else {
     hipLaunchKernelGGL((gemm_kernel<T, TA, false, TILE, TILE, false, GROUP, SUMS>), grid, block, 0,
                        stream, p);
   }
-  return launched();
 }
 
-template <typename T, bool GROUP, bool SUMS>
-static dense_gemm_status enqueue_tn(int64_t tile, const LayerParams& p, const LayerReduceParams& r,
+template <typename T, int TILE>
+static dense_gemm_status enqueue_tn(const LayerParams& p, uint16_t* colsum, int groups, bool grouped,
                                     int cus, hipStream_t stream) {
-  return tile == BM ? enqueue_tile<T, BM, GROUP, SUMS>(p, r, cus, stream)
-                    : enqueue_tile<T, BM / 2, GROUP, SUMS>(p, r, cus, stream);
+  if (colsum == nullptr) {
+    grouped ? enqueue_tile<T, TILE, true, false>(p, cus, stream)
+            : enqueue_tile<T, TILE, false, false>(p, cus, stream);
+    return launched();
+  }
+  grouped ? enqueue_tile<T, TILE, true, true>(p, cus, stream)
+          : enqueue_tile<T, TILE, false, true>(p, cus, stream);
+  const ColumnSumsParams s = {p.colsum_ws, colsum, p.M, groups, p.tiles_m, p.tiles_n, p.group_m,
+                              p.full_tasks, p.splits, p.tiles};
+  hipLaunchKernelGGL((column_sums<T, TILE>),
+                     dim3((unsigned)((int64_t)groups * ((p.M + CS_COLS - 1) / CS_COLS))),
+                     dim3(CS_COLS * CS_LANES), 0, stream, s);
+  return launched();
 }
 
 template <typename T>
 static dense_gemm_status run_tn(LayerCall c, void* colsum, const dense_gemm_groups* groups,
                                 void* ws, size_t ws_bytes) {
   TnPlan tp;
-  const dense_gemm_status st = tn_plan(c.M, c.N, c.K, c.A, c.lda, c.B, c.ldb, groups, c.cus, &tp);
+  const dense_gemm_status st = tn_plan(c.M, c.N, c.K, c.A, c.lda, c.B, c.ldb, colsum != nullptr, groups,
+                                       c.cus, &tp);
   if (st != DENSE_GEMM_OK) return st;
   if (tp.total() > 0) {
     if (ws == nullptr || ws_bytes < tp.total()) return DENSE_GEMM_WORKSPACE_TOO_SMALL;
@@ -64,25 +79,14 @@ static dense_gemm_status run_tn(LayerCall c, void* colsum, const dense_gemm_grou
   p.splits = (int)tp.splits;
   p.split_steps = (int)tp.steps;
   p.num_tasks = (int)(tp.full_tasks + tp.split_tiles * tp.splits);
-  p.colsum = (uint16_t*)colsum;
-  if (tp.splits > 1) {
-    p.ws = (float*)at;
-    p.colsum_ws = (float*)(at + tp.split_bytes);
-  }
-  if (groups != nullptr) {
-    p.g = {(const int32_t*)groups->ends, (int)groups->count, (int)c.K, groups->stride};
-  }
-  LayerReduceParams r = {};
-  (ReduceParams&)r = {p.D, p.ws, p.M, p.N, p.ldd, p.tiles_m, p.tiles_n, p.group_m,
-                      p.full_tasks, p.splits, p.tiles, p.d_vec};
-  r.stride = p.g.stride;
-  r.colsum = p.colsum;
-  r.colsum_ws = p.colsum_ws;
+  if (tp.splits > 1) p.ws = (float*)at;
+  if (colsum != nullptr) p.colsum_ws = (float*)(at + tp.split_bytes);
   if (groups != nullptr)
-    return colsum != nullptr ? enqueue_tn<T, true, true>(tp.tile, p, r, c.cus, c.stream)
-                             : enqueue_tn<T, true, false>(tp.tile, p, r, c.cus, c.stream);
-  return colsum != nullptr ? enqueue_tn<T, false, true>(tp.tile, p, r, c.cus, c.stream)
-                           : enqueue_tn<T, false, false>(tp.tile, p, r, c.cus, c.stream);
+    p.g = {(const int32_t*)groups->ends, (int)groups->count, (int)c.K, groups->stride};
+  return tp.tile == BM ? enqueue_tn<T, BM>(p, (uint16_t*)colsum, (int)tp.groups, groups != nullptr,
+                                           c.cus, c.stream)
+                       : enqueue_tn<T, BM / 2>(p, (uint16_t*)colsum, (int)tp.groups,
+                                               groups != nullptr, c.cus, c.stream);
 }
 
 }  // namespace dg
@@ -107,7 +111,7 @@ dense_gemm_status dense_gemm_tn(int fmt, int64_t M, int64_t N, int64_t K, const 
 }
 
 dense_gemm_status dense_gemm_tn_workspace_size(int64_t M, int64_t N, int64_t K, const void* A,
-                                               int64_t lda, const void* B, int64_t ldb,
+                                               int64_t lda, const void* B, int64_t ldb, int colsum,
                                                const dense_gemm_groups* groups, int64_t num_cus,
                                                size_t* bytes) {
   if (bytes == nullptr || num_cus < 0) return DENSE_GEMM_BAD_ARG;
@@ -119,8 +123,9 @@ dense_gemm_status dense_gemm_tn_workspace_size(int64_t M, int64_t N, int64_t K, 
     if (M > 0 && N > 0 && M < kMaxDim && N < kMaxDim) g.stride = M * N;
   }
   bool done;
-  dense_gemm_status st = tn_validate(DENSE_GEMM_F16, M, N, K, A, lda, B, ldb, any, N, nullptr,
-                                     groups != nullptr ? &g : nullptr, &done);
+  dense_gemm_status st = tn_validate(DENSE_GEMM_F16, M, N, K, A, lda, B, ldb, any, N,
+                                     colsum != 0 ? any : nullptr, groups != nullptr ? &g : nullptr,
+                                     &done);
   if (st != DENSE_GEMM_OK) return st;
   *bytes = 0;
   if (done) return DENSE_GEMM_OK;
@@ -130,7 +135,7 @@ dense_gemm_status dense_gemm_tn_workspace_size(int64_t M, int64_t N, int64_t K, 
     if (st != DENSE_GEMM_OK) return st;
   }
   TnPlan tp;
-  st = tn_plan(M, N, K, A, lda, B, ldb, groups != nullptr ? &g : nullptr, cus, &tp);
+  st = tn_plan(M, N, K, A, lda, B, ldb, colsum != 0, groups != nullptr ? &g : nullptr, cus, &tp);
   if (st == DENSE_GEMM_OK) *bytes = tp.total();
   return st;
 }

@@ -418,10 +418,11 @@ dense_gemm_status dense_gemm_tn(int fmt, int64_t M, int64_t N, int64_t K, const 
                                 void* colsum, const dense_gemm_groups* groups, void* workspace,
                                 size_t workspace_bytes, hipStream_t stream);
 
-/* Bytes of workspace dense_gemm_tn needs: repacked operands, and FP32 partial
- * tiles (with their column sums) where K is split.  `ends` is not read. */
+/* Bytes of workspace dense_gemm_tn needs: repacked operands, FP32 partial
+ * tiles where K is split, and with colsum (not 0) 2 KiB of partial column sums
+ * per output tile and part.  `ends` is not read. */
 dense_gemm_status dense_gemm_tn_workspace_size(int64_t M, int64_t N, int64_t K, const void* A,
-                                               int64_t lda, const void* B, int64_t ldb,
+                                               int64_t lda, const void* B, int64_t ldb, int colsum,
                                                const dense_gemm_groups* groups, int64_t num_cus,
                                                size_t* bytes);
 
