@@ -164,23 +164,46 @@ __global__ __launch_bounds__(THREADS, (two_per_cu<LAYOUT, TN, TM, EPI, GROUP>())
   const int wm = wave >> 1;  // wave tile row (0..1)
   const int wn = wave & 1;   // wave tile column (0..1)
 
-  int slot0, num_tasks;
+  // Where all tasks are alike, the layer products deal each XCD one run of
+  // them, an even share, which its workgroups take in turn: the tasks of a
+  // last, partial round then fall on all XCDs, a few CUs each (48 groups,
+  // 5003 rows, 63 -> 53 us; A.T @ B 5120 x 8192 x 8192, 2.5 rounds, 551 ->
+  // 533).  Else the tasks are dealt round by round, so that a round's tiles
+  // are neighbours over all XCDs: groups of different K would leave the XCDs
+  // with different work (16 groups' A.T @ B 508 us, 1254 in runs), and 16
+  // groups of 1024 rows take 509 us, 523 in runs.
+  constexpr bool SHARES = !SPLIT && (GROUP ? ROWS && TM == BM / 2 : EPI || LAYOUT == TA);
+  int slot0, num_tasks, stride = gridDim.x;
   // (four registers each for the counts and ends of up to 256 groups)
   [[maybe_unused]] GroupMap<4> map;
   if constexpr (ROWS) {
-    // the XCDs share the tiles there are, also where those are fewer than
-    // the launch's workgroups
     map.count(p.g, TM, p.tiles_n);
     num_tasks = map.total;
+  } else {
+    num_tasks = p.num_tasks;
+  }
+  if constexpr (SHARES) {
+    // (the first num_tasks % xcds shares hold one task more, as the first
+    // gridDim.x % xcds XCDs hold one workgroup more: no share is without a
+    // workgroup, and a grid of one workgroup per task does one each)
+    const int xcds = min(p.num_xcds, (int)gridDim.x);
+    const int xcd = blockIdx.x % xcds;
+    const int share = num_tasks / xcds, more = num_tasks % xcds;
+    const int first = xcd * share + min(xcd, more);
+    slot0 = first + blockIdx.x / xcds;
+    num_tasks = first + share + (xcd < more ? 1 : 0);
+    stride = ((int)gridDim.x - xcd + xcds - 1) / xcds;
+  } else if constexpr (ROWS) {
+    // (the XCDs share the tiles there are, also where they are fewer than
+    // the workgroups)
     const int busy = min((int)gridDim.x, num_tasks);
     if ((int)blockIdx.x >= busy) return;
     slot0 = xcd_slot(blockIdx.x, busy, p.num_xcds);
   } else {
     slot0 = xcd_slot(blockIdx.x, gridDim.x, p.num_xcds);
-    num_tasks = p.num_tasks;
   }
 
-  for (int task = slot0; task < num_tasks; task += gridDim.x) {
+  for (int task = slot0; task < num_tasks; task += stride) {
     int tm, tn;
     const bool part = SPLIT && task >= p.full_tasks;
     const int u = task - p.full_tasks;
@@ -296,6 +319,17 @@ __global__ __launch_bounds__(THREADS, (two_per_cu<LAYOUT, TN, TM, EPI, GROUP>())
     // per-lane masks.  (TA: k is a row of both operands, so no rounding.)
     const int K8 = LAYOUT == TA ? K : (K + 7) & ~7;
     const int koff = (BK - (K8 & (BK - 1))) & (BK - 1);
+    // Groups of rows, A @ B.T: a tile starts its K steps at one of its own
+    // and wraps around.  In step, all tiles would read the same 128 bytes of
+    // rows a power of two apart, i.e. the same few memory channels: 64 groups
+    // of 2 rows, N = 1024, K = 2048, weights from HBM, 67 -> 51 us (5.2
+    // TB/s).  256-row tiles turn by group only, as the tiles of a row share
+    // A's steps in L2 (16 groups of 1024, N = K = 4096: 507 us, 527 with a
+    // turn per tile).
+    [[maybe_unused]] int turn = 0;
+    if constexpr (ROWS && LAYOUT == NT) {
+      if (koff == 0 && nk > 0) turn = ((TM == BM ? 0 : tn * 5) + group * 3) % nk;
+    }
     uint32_t a_off[DMA_PER_OPERAND], b_off[DMA_B];
     int kc[2];  // logical chunk of this lane for even / odd instruction index
 #pragma unroll
@@ -341,7 +375,12 @@ __global__ __launch_bounds__(THREADS, (two_per_cu<LAYOUT, TN, TM, EPI, GROUP>())
     // suffice; 64-bit forms made the compiler branch inside the loop.)
     auto half_setup = [&](int ks, int slot, int half) {
       Half h;
-      const int k0 = ks * BK - koff;
+      int kt = ks;
+      if constexpr (ROWS && LAYOUT == NT) {
+        kt += turn;
+        kt -= kt >= nk ? nk : 0;
+      }
+      const int k0 = kt * BK - koff;
       const bool live = ks < kend;
       h.k0 = k0;
       h.base = lds0 + (half == EARLY ? 0 : RING2) + slot * (half == 0 ? A_BYTES : B_TILE) +

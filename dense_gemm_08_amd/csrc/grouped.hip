@@ -19,18 +19,10 @@ dense_gemm_status run_grouped(LayerCall c, const dense_gemm_groups& groups, void
     if (((uintptr_t)ws & 255) != 0) return DENSE_GEMM_MISALIGNED;
   }
   Groups g = {(const int32_t*)groups.ends, (int)groups.count, (int)c.M, groups.stride};
-  if (!gp.a_direct) {
-    c.lda = enqueue_repack(c.A, 1, c.M, c.K, c.lda, 0, ws, c.stream);
-    c.A = (const uint16_t*)ws;
-  }
-  if (!gp.b_direct) {
-    const int64_t rows = LAYOUT == NT ? c.N : c.K;
-    void* at = (char*)ws + gp.a_bytes;
-    c.ldb = enqueue_repack(c.B, g.count, rows, LAYOUT == NT ? c.K : c.N, c.ldb, g.stride, at,
-                           c.stream);
-    c.B = (const uint16_t*)at;
-    g.stride = rows * c.ldb;
-  }
+  const int64_t b_rows = LAYOUT == NT ? c.N : c.K;
+  repack_operands(c, gp.a_direct ? nullptr : ws, groups.count, b_rows, LAYOUT == NT ? c.K : c.N,
+                  g.stride, gp.b_direct ? nullptr : (char*)ws + gp.a_bytes);
+  if (!gp.b_direct) g.stride = b_rows * c.ldb;
   const dim3 grid((unsigned)gp.grid);
   if (gp.small) {
     SmallLayerParams p = small_params(c);

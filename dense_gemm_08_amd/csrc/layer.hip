@@ -12,14 +12,24 @@
 
 namespace dg {
 
-int64_t enqueue_repack(const void* src, int64_t count, int64_t rows, int64_t cols, int64_t ld,
-                       int64_t stride, void* dst, hipStream_t stream) {
-  const int64_t dcols = (cols + 7) & ~(int64_t)7;
-  const int64_t blocks = (count * rows * (dcols / 8) + 255) / 256;
-  hipLaunchKernelGGL(repack_groups, dim3((unsigned)(blocks < REPACK_MAX_BLOCKS ? blocks : REPACK_MAX_BLOCKS)),
-                     dim3(256), 0, stream, (const uint16_t*)src, count, rows, cols, ld, stride,
-                     (uint16_t*)dst, dcols);
-  return dcols;
+void enqueue_repacks(const Repack& a, const Repack& b, hipStream_t stream) {
+  const Repack* in[2] = {&a, &b};
+  RepackJob job[2] = {};
+  int64_t grid = 0;
+  for (int i = 0; i < 2; ++i) {
+    const Repack& r = *in[i];
+    if (r.dst == nullptr) continue;
+    RepackJob& j = job[i];
+    j = {(const uint16_t*)r.src, (uint16_t*)r.dst, r.count, r.rows, r.cols, r.ld, r.stride,
+         repacked_ld(r.cols), 0, 1};
+    while (j.lanes < 256 && j.lanes * 8 < j.dcols) j.lanes *= 2;
+    const int64_t per = 256 / j.lanes;
+    j.blocks = (r.count * r.rows + per - 1) / per;
+    if (j.blocks > REPACK_MAX_BLOCKS) j.blocks = REPACK_MAX_BLOCKS;
+    grid += j.blocks;
+  }
+  if (grid > 0)
+    hipLaunchKernelGGL(repack_groups, dim3((unsigned)grid), dim3(256), 0, stream, job[0], job[1]);
 }
 
 template <typename T, int LAYOUT, int TN, int TM>
@@ -36,7 +46,8 @@ static dense_gemm_status enqueue_tiled(const LayerCall& c, const CallPlan& cp, f
   p.num_tasks = (int)(cp.full_tasks + cp.split_tiles * cp.plan[8]);
   p.ws = parts;
   p.e = device_epilogue(c.e);
-  const dim3 grid((unsigned)(p.num_tasks < c.cus ? p.num_tasks : c.cus)), block(THREADS);
+  const int slots = c.cus * (int)resident(TM, TN);
+  const dim3 grid((unsigned)(p.num_tasks < slots ? p.num_tasks : slots)), block(THREADS);
   if (p.splits > 1) {
     hipLaunchKernelGGL((gemm_kernel<T, LAYOUT, true, TN, TM, true>), grid, block, 0, c.stream, p);
     LayerReduceParams r = {};
@@ -72,31 +83,22 @@ static dense_gemm_status enqueue_small_output(const LayerCall& c, const CallPlan
 template <typename T, int LAYOUT>
 static dense_gemm_status run_layer(LayerCall c, void* ws, size_t ws_bytes) {
   CallPlan cp;
-  const dense_gemm_status st = plan_call(LAYOUT, c.M, c.N, c.K, c.A, c.lda, c.B, c.ldb, c.cus,
-                                         nullptr, &cp);
+  const dense_gemm_status st = layer_plan(LAYOUT, c.M, c.N, c.K, c.A, c.lda, c.B, c.ldb, c.cus, &cp);
   if (st != DENSE_GEMM_OK) return st;
   if (cp.total() > 0) {
     if (ws == nullptr || ws_bytes < cp.total()) return DENSE_GEMM_WORKSPACE_TOO_SMALL;
     if (((uintptr_t)ws & 255) != 0) return DENSE_GEMM_MISALIGNED;
   }
   char* at = (char*)ws;
-  if (!cp.a_direct) {
-    c.lda = enqueue_repack(c.A, 1, c.M, c.K, c.lda, 0, at, c.stream);
-    c.A = (const uint16_t*)at;
-  }
-  at += cp.a_bytes;
-  if (!cp.b_direct) {
-    c.ldb = enqueue_repack(c.B, 1, LAYOUT == NT ? c.N : c.K, LAYOUT == NT ? c.K : c.N, c.ldb, 0, at,
-                           c.stream);
-    c.B = (const uint16_t*)at;
-  }
-  at += cp.b_bytes;
+  repack_operands(c, cp.a_direct ? nullptr : at, 1, LAYOUT == NT ? c.N : c.K,
+                  LAYOUT == NT ? c.K : c.N, 0, cp.b_direct ? nullptr : at + cp.a_bytes);
+  at += cp.a_bytes + cp.b_bytes;
   if (cp.small()) return enqueue_small_output<T, LAYOUT>(c, cp);
   const bool short_tiles = cp.plan[0] == BM / 2;
+  if (short_tiles && cp.plan[1] == BN / 2)
+    return enqueue_tiled<T, LAYOUT, BN / 2, BM / 2>(c, cp, (float*)at);
   if constexpr (LAYOUT == NT) {
-    if (cp.plan[1] == BN / 2)
-      return short_tiles ? enqueue_tiled<T, LAYOUT, BN / 2, BM / 2>(c, cp, (float*)at)
-                         : enqueue_tiled<T, LAYOUT, BN / 2, BM>(c, cp, (float*)at);
+    if (cp.plan[1] == BN / 2) return enqueue_tiled<T, LAYOUT, BN / 2, BM>(c, cp, (float*)at);
   }
   return short_tiles ? enqueue_tiled<T, LAYOUT, BN, BM / 2>(c, cp, (float*)at)
                      : enqueue_tiled<T, LAYOUT, BN, BM>(c, cp, (float*)at);
@@ -166,7 +168,7 @@ dense_gemm_status dense_gemm_layer_workspace_size(int op, int64_t M, int64_t N, 
     return st;
   }
   CallPlan cp;
-  st = plan_call(op_layout(op), M, N, K, A, lda, B, ldb, cus, nullptr, &cp);
+  st = layer_plan(op_layout(op), M, N, K, A, lda, B, ldb, cus, &cp);
   if (st == DENSE_GEMM_OK) *bytes = cp.total();
   return st;
 }

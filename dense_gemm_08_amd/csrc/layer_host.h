@@ -15,11 +15,17 @@ namespace dg {
 
 dense_gemm_status device_topology(int* cus, int* xcds);
 
-// Enqueues a copy of `count` matrices of rows x cols 16-bit elements, ld
-// between their rows and stride between the matrices, into dense zero-padded
-// ones (repack_groups in layer.hip); returns the copies' leading dimension.
-int64_t enqueue_repack(const void* src, int64_t count, int64_t rows, int64_t cols, int64_t ld,
-                       int64_t stride, void* dst, hipStream_t stream);
+// A copy of `count` matrices of rows x cols 16-bit elements, ld between their
+// rows and stride between the matrices, into dense zero-padded ones at dst
+// (null: none), whose leading dimension is repacked_ld(cols).
+struct Repack {
+  const void* src;
+  void* dst;
+  int64_t count, rows, cols, ld, stride;
+};
+inline int64_t repacked_ld(int64_t cols) { return (cols + 7) & ~(int64_t)7; }
+// Enqueues one launch for both (none if neither is asked for): layer.hip.
+void enqueue_repacks(const Repack& a, const Repack& b, hipStream_t stream);
 
 inline dense_gemm_status launched() {
   return hipGetLastError() == hipSuccess ? DENSE_GEMM_OK : DENSE_GEMM_LAUNCH_FAILED;
@@ -52,6 +58,22 @@ struct LayerCall {
   int cus, xcds;
   hipStream_t stream;
 };
+
+// Copies A (M x K) and the `count` matrices B (b_rows x b_cols) where a place
+// for the copy is given, and makes the copies the call's operands.
+inline void repack_operands(LayerCall& c, void* a_dst, int64_t count, int64_t b_rows,
+                            int64_t b_cols, int64_t b_stride, void* b_dst) {
+  enqueue_repacks({c.A, a_dst, 1, c.M, c.K, c.lda, 0},
+                  {c.B, b_dst, count, b_rows, b_cols, c.ldb, b_stride}, c.stream);
+  if (a_dst != nullptr) {
+    c.A = (const uint16_t*)a_dst;
+    c.lda = repacked_ld(c.K);
+  }
+  if (b_dst != nullptr) {
+    c.B = (const uint16_t*)b_dst;
+    c.ldb = repacked_ld(b_cols);
+  }
+}
 
 inline void set_operands(Params& p, const LayerCall& c) {
   p.A = c.A;

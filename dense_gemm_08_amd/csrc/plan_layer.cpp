@@ -17,6 +17,12 @@ bool matrix_bytes(int64_t a, int64_t b, size_t* out) {
   return true;
 }
 
+// Over more than one wave, 128 x 128 tiles are considered up to this many K
+// steps: they move twice the operand bytes per product, and under long load
+// the board's power limit makes that count for more than the estimates below
+// say (8192 x 5120 x 17408, 640 large tiles or 2560: 1078 against 1499 us).
+constexpr int64_t NARROW_STEPS = 16;
+
 int64_t round8(int64_t x) { return (x + 7) & ~(int64_t)7; }
 
 bool aligned16(const void* p) { return ((uintptr_t)p & 15) == 0; }
@@ -90,6 +96,65 @@ dense_gemm_status layer_validate(int op, int64_t M, int64_t N, int64_t K, const 
   return DENSE_GEMM_OK;
 }
 
+// 128 x 128 tiles where they are estimated faster than the plain product's
+// plan.  The estimates, in 0.01 us, are fitted to times on the MI355X (BF16,
+// SILU in the epilogue, operands from HBM), nk K steps of 64:
+//   * 256 x 256 tiles: waves x (133 nk + 1650); a split (choose_split) costs
+//     800 and 4 per partial tile, a split last wave 1500;
+//   * 256 x 128 and 128 x 256: one wave of 75 nk + 960, a split 600 and 1.5 a
+//     partial tile;
+//   * 128 x 128, two workgroups per CU: waves x (79 nk + 650); where each has
+//     a CU to itself 47 nk + 550, and split-K costs 700 and 1 per partial tile.
+// Measured, us, the plain product's plan against 128 x 128: A @ B.T 2048 x
+// 2048 x 2048 30 against 22, 777 x 1000 x 2048 29 against 19 (in 3 parts),
+// 4096 x 2048 x 1024 22 against 20, x 4096 56 against 57, 4096 x 4096 x 512
+// 27 against 25; A @ B 2048 x 2048 x 2048 51 against 23, 4096 x 2048 x 4096
+// 88 against 60, 512 x 512 x 4096 29 against 17, 100 x 8000 x 3000 25 against
+// 21.
+dense_gemm_status layer_plan(int layout, int64_t M, int64_t N, int64_t K, const void* A,
+                             int64_t lda, const void* B, int64_t ldb, int64_t cus, CallPlan* cp) {
+  const dense_gemm_status st = plan_call(layout, M, N, K, A, lda, B, ldb, cus, nullptr, cp);
+  if (st != DENSE_GEMM_OK || cp->small()) return st;
+  const int64_t nk = (K + BK - 1) / BK;
+  int64_t* plan = cp->plan;
+  const int64_t had = plan[3] * plan[4], parts = cp->split_tiles * plan[8];
+  double cost;
+  if (plan[0] == BM && plan[1] == BN) {
+    const int64_t waves = (had + cus - 1) / cus;
+    cost = (double)(plan[8] > 1 ? waves - 1 : waves) * (133 * nk + 1650);
+    if (plan[8] > 1) cost += 133 * plan[9] + 1650 + (had < cus ? 800 + 4.0 * parts : 1500);
+  } else {
+    cost = 75.0 * plan[9] + 960 + (plan[8] > 1 ? 600 + 1.5 * parts : 0);
+  }
+  const int64_t tiles_m = (M + BM / 2 - 1) / (BM / 2), tiles_n = (N + BN / 2 - 1) / (BN / 2);
+  const int64_t tasks = tiles_m * tiles_n, slots = cus * resident(BM / 2, BN / 2);
+  int64_t splits = 1, steps = nk;
+  if (tasks < cus) choose_split(tasks, nk, cus, 50, 700, 1, BM / 16, &splits, &steps);
+  double narrow;
+  if (splits > 1)
+    narrow = 50.0 * steps + 1250 + splits * tasks;
+  else if (tasks <= cus)
+    narrow = 47.0 * nk + 550;
+  else
+    narrow = (double)((tasks + slots - 1) / slots) * (79 * nk + 650);
+  if (narrow >= cost || tasks >= kMaxDim || (tasks > slots && nk > NARROW_STEPS)) return st;
+  plan[0] = BM / 2;
+  plan[1] = BN / 2;
+  plan[3] = tiles_m;
+  plan[4] = tiles_n;
+  plan[5] = tasks * splits < slots ? tasks * splits : slots;
+  plan[6] = choose_group_m(tiles_m);
+  plan[7] = THREADS;
+  plan[8] = splits;
+  plan[9] = steps;
+  cp->full_tasks = splits > 1 ? 0 : tasks;
+  cp->split_tiles = tasks - cp->full_tasks;
+  // (at most one part per CU: no overflow)
+  cp->split_bytes =
+      splits > 1 ? (size_t)(splits * tasks) * (BM / 2) * (BN / 2) * sizeof(float) : 0;
+  return DENSE_GEMM_OK;
+}
+
 dense_gemm_status grouped_plan(int layout, int64_t M, int64_t N, int64_t K, const void* A,
                                int64_t lda, const void* B, int64_t ldb, const dense_gemm_groups& g,
                                int64_t cus, GroupedPlan* out) {
@@ -113,7 +178,7 @@ dense_gemm_status grouped_plan(int layout, int64_t M, int64_t N, int64_t K, cons
   const int64_t active = g.count < M ? g.count : M;
   const int64_t avg = (M + active - 1) / active;
   const int64_t tiles128 = most_row_tiles(M, g.count, BM / 2) * ((N + BN / 2 - 1) / (BN / 2));
-  out->small = avg <= SMALL_TILE && tiles128 <= (layout == NT ? cus : cus / 2);
+  out->small = avg <= SMALL_TILE && tiles128 <= (layout == NT ? cus : cus / 4);
   if (out->small) {
     out->tile_m = out->tile_n = SMALL_TILE;
   } else if (avg > 192) {
@@ -228,6 +293,7 @@ static TnChoice tn_choice(int64_t M, int64_t N, int64_t nk, int64_t groups, bool
              (c.splits > 1 ? 1000 + c.splits * tasks : 0);
   } else {
     c.cost = (double)waves * (90 * nk + 360);
+    if (waves > 1 && nk > NARROW_STEPS) c.cost = 1e30;
   }
   return c;
 }

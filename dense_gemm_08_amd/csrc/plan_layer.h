@@ -50,6 +50,11 @@ dense_gemm_status layer_validate(int op, int64_t M, int64_t N, int64_t K, const 
                                  int64_t ldd, const dense_gemm_epilogue* e,
                                  const dense_gemm_groups* g, bool* done);
 
+// The plan of a call of dense_gemm_layer without groups whose arguments passed
+// layer_validate: plan_call's, or 128 x 128 tiles (plan[0] and plan[1]).
+dense_gemm_status layer_plan(int layout, int64_t M, int64_t N, int64_t K, const void* A,
+                             int64_t lda, const void* B, int64_t ldb, int64_t cus, CallPlan* cp);
+
 // The plan of a grouped call whose arguments passed layer_validate.
 dense_gemm_status grouped_plan(int layout, int64_t M, int64_t N, int64_t K, const void* A,
                                int64_t lda, const void* B, int64_t ldb, const dense_gemm_groups& g,

@@ -59,16 +59,20 @@ static dense_gemm_status run_tn(LayerCall c, void* colsum, const dense_gemm_grou
     if (((uintptr_t)ws & 255) != 0) return DENSE_GEMM_MISALIGNED;
   }
   char* at = (char*)ws;
+  Repack a = {}, b = {};
   if (!tp.a_direct) {
-    c.lda = enqueue_repack(c.A, 1, c.K, c.M, c.lda, 0, at, c.stream);
+    a = {c.A, at, 1, c.K, c.M, c.lda, 0};
     c.A = (const uint16_t*)at;
+    c.lda = repacked_ld(c.M);
   }
   at += tp.a_bytes;
   if (!tp.b_direct) {
-    c.ldb = enqueue_repack(c.B, 1, c.K, c.N, c.ldb, 0, at, c.stream);
+    b = {c.B, at, 1, c.K, c.N, c.ldb, 0};
     c.B = (const uint16_t*)at;
+    c.ldb = repacked_ld(c.N);
   }
   at += tp.b_bytes;
+  enqueue_repacks(a, b, c.stream);
   LayerParams p = {};
   set_operands(p, c);
   p.tiles_m = (int)tp.tiles_m;

@@ -385,9 +385,9 @@ typedef struct dense_gemm_groups {
  * with B_g = B + g * groups->stride, N x K or K x N by op, leading dimension
  * ldb.  M is the number of rows of A, D, residual and preact; rows that no
  * group holds (those from ends[count - 1] on) are neither read nor written.
- * count 0 does nothing.  Without groups the plan is that of dense_gemm_ex
- * without options; with groups it depends on M, N, K, the count and the
- * device alone, not on the ends.  Fewer than 2^31 output tiles are accepted
+ * count 0 does nothing.  The plan, and with it the order of the sums, may
+ * differ from the plain product's; with groups it depends on M, N, K, the
+ * count and the device alone, not on the ends.  Fewer than 2^31 output tiles are accepted
  * (DENSE_GEMM_TOO_LARGE), counting one more row of tiles per group. */
 dense_gemm_status dense_gemm_layer(int op, int64_t M, int64_t N, int64_t K, const void* A,
                                    int64_t lda, const void* B, int64_t ldb, void* D, int64_t ldd,

@@ -142,15 +142,19 @@ def test_residual_and_preact_in_place(M, N, K, layout):
 
 
 @pytest.mark.parametrize("dtype", ["f16", "bf16"])
-def test_no_epilogue_gives_the_plain_product_bits(dtype):
+def test_exact_sums_give_the_plain_product_bits(dtype):
+    # small integers: every order of the sums is exact, so without an epilogue
+    # the result is the plain product's whatever the plans
     dt = L.GEN[dtype]
     gen = generator(12)
     plain = {("nt", "f16"): dg.gemm_nt_f16, ("nn", "f16"): dg.gemm_nn_f16,
              ("nt", "bf16"): dg.gemm_nt_bf16, ("nn", "bf16"): dg.gemm_nn_bf16}
     for layout, (M, N, K) in itertools.product(("nt", "nn"), [(5, 100, 64), (120, 700, 1000),
-                                                              (700, 600, 3001), (256, 128, 4096)]):
-        A = rand(gen, M, K, dt=dt)
-        B = rand(gen, *((N, K) if layout == "nt" else (K, N)), dt=dt)
+                                                              (700, 600, 3001), (256, 128, 4096),
+                                                              (2048, 2048, 100)]):
+        A = torch.randint(-3, 4, (M, K), generator=gen, device="cuda").to(dt)
+        B = torch.randint(-3, 4, (N, K) if layout == "nt" else (K, N), generator=gen,
+                          device="cuda").to(dt)
         assert torch.equal(NT_F[layout](A, B), plain[(layout, dtype)](A, B)), (layout, M, N, K)
 
 

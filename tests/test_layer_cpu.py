@@ -150,13 +150,23 @@ def up256(n):
     return (n + 255) // 256 * 256
 
 
-def test_layer_workspace_is_the_plain_products():
+def test_layer_workspace():
     for op in range(4):
-        for M, N, K in ((1, 4096, 4096), (256, 128, 8192), (300, 301, 77), (4096, 4352, 512)):
-            layout, fmt = {v: k for k, v in binding.OPS.items()}[op]
-            want = binding.workspace_size(layout, fmt, M, N, K, 256, K, 256,
-                                          K if layout == "nt" else N, num_cus=256)
-            assert layer_bytes(op, M, N, K) == want
+        # the small-output kernel, and whole tiles of either size
+        assert layer_bytes(op, 1, 4096, 4096) == 0
+        assert layer_bytes(op, 2048, 2048, 2048) == 0
+        assert layer_bytes(op, 4096, 4096, 4096) == 0
+        # few tiles, long K: 128 x 128 partial tiles, at most one per CU
+        n = layer_bytes(op, 256, 128, 8192)
+        assert n % (128 * 128 * 4) == 0 and 4 <= n // (128 * 128 * 4) <= 256
+        # a last wave of 256 x 256 tiles in parts, as in the plain product
+        layout, fmt = {v: k for k, v in binding.OPS.items()}[op]
+        assert layer_bytes(op, 4096, 4352, 4096) == binding.workspace_size(
+            layout, fmt, 4096, 4352, 4096, 256, 4096, 256, 4096 if layout == "nt" else 4352,
+            num_cus=256) > 0
+        # operands off 16 bytes, copied
+        assert layer_bytes(op, 300, 304, 80, A=258) == up256(300 * 80 * 2)
+        assert layer_bytes(op, 300, 304, 80, B=258) == up256(304 * 80 * 2)
 
 
 def test_grouped_workspace_holds_the_repacked_operands():
