@@ -389,13 +389,14 @@ def _torch():
     return torch
 
 
-def _check_like(t, A, dims: int, what: str, shape=None):
-    """A device tensor of A's type and device with ``dims`` dimensions, a unit
-    last stride and (where given) this shape."""
-    if t.dtype != A.dtype:
-        raise TypeError("%s must be %s like A, got %s" % (what, A.dtype, t.dtype))
-    if t.device != A.device:
-        raise ValueError("operands on different devices: %s and %s" % (A.device, t.device))
+def _check_like(t, dtype, dev: int, dims: int, what: str, shape=None):
+    """A tensor of this type on device number ``dev``, with ``dims``
+    dimensions, a unit last stride and (where given) this shape."""
+    if t.dtype is not dtype:
+        raise TypeError("%s must be %s like A, got %s" % (what, dtype, t.dtype))
+    if t.get_device() != dev:
+        raise ValueError("operands on different devices: A on cuda:%d, %s on %s"
+                         % (dev, what, t.device))
     if t.dim() != dims or (t.stride(-1) != 1 and t.shape[-1] > 1):
         raise ValueError("%s must be %d-D with unit stride in its last dimension" % (what, dims))
     if shape is not None and t.shape != shape:
@@ -403,22 +404,24 @@ def _check_like(t, A, dims: int, what: str, shape=None):
 
 
 def _check_first(A):
-    """A's format, as (name, dense_gemm_fmt)."""
-    fmt = _FMTS.get(A.dtype)
+    """A's format, as (name, dense_gemm_fmt), type and device number."""
+    dtype = A.dtype
+    fmt = _FMTS.get(dtype)
     if fmt is None:
-        raise TypeError("A must be float16 or bfloat16, got %s" % A.dtype)
+        raise TypeError("A must be float16 or bfloat16, got %s" % dtype)
     if not A.is_cuda:
         raise ValueError("A must be a device tensor")
     if A.dim() != 2 or (A.stride(1) != 1 and A.shape[1] > 1):
         raise ValueError("A must be 2-D with unit column stride")
-    return fmt
+    return fmt, dtype, A.get_device()
 
 
-def _check_ends(ends, A, torch):
-    if ends.dtype != torch.int32:
+def _check_ends(ends, dev, torch):
+    if ends.dtype is not torch.int32:
         raise TypeError("ends must be int32, got %s" % ends.dtype)
-    if ends.device != A.device:
-        raise ValueError("operands on different devices: %s and %s" % (A.device, ends.device))
+    if ends.get_device() != dev:
+        raise ValueError("operands on different devices: A on cuda:%d, ends on %s"
+                         % (dev, ends.device))
     if ends.dim() != 1 or (ends.shape[0] > 1 and ends.stride(0) != 1):
         raise ValueError("ends must be 1-D and contiguous")
 
@@ -431,42 +434,46 @@ def _stack(t):
 
 
 def _launch(name, args, size_of, workspace, stream, dev, torch):
-    """Calls ``name(*args, workspace, bytes, stream)`` on the device.  Without
-    a workspace of the caller's, one is taken from torch's allocator if the
-    call turns out to need it (``size_of``: its size query)."""
-    if torch.cuda.current_device() != dev.index:
+    """Calls ``name(*args, workspace, bytes, stream)`` on device number
+    ``dev``.  Without a workspace of the caller's, one is taken from torch's
+    allocator if the call turns out to need it (``size_of``: its size query
+    and that query's arguments)."""
+    if torch.cuda.current_device() != dev:
         with torch.cuda.device(dev):
             return _launch(name, args, size_of, workspace, stream, dev, torch)
     fn = getattr(_lib, name)
     if stream is None and _raw_stream is not None:
-        sh = _raw_stream(dev.index)
+        sh = _raw_stream(dev)
     else:
         sh = _stream_handle(stream, dev)
     if workspace is None or workspace is True:
         st = fn(*args, None, 0, sh)
         if st == 10:  # WORKSPACE_TOO_SMALL
             need = ctypes.c_size_t()
-            st = size_of(need)
+            st = getattr(_lib, size_of[0])(*size_of[1:], ctypes.byref(need))
             if st == 0:
-                ws = _used_by(torch.empty(need.value, dtype=torch.uint8, device=dev), stream, dev)
+                ws = torch.empty(need.value, dtype=torch.uint8, device=dev)
+                if stream is not None:
+                    _used_by(ws, stream, ws.device)
                 st = fn(*args, ws.data_ptr(), need.value, sh)
     else:
-        if not workspace.is_cuda or workspace.device != dev:
-            raise ValueError("workspace must be a device tensor on %s" % dev)
+        if workspace.get_device() != dev:
+            raise ValueError("workspace must be a device tensor on cuda:%d" % dev)
         st = fn(*args, workspace.data_ptr(), workspace.numel() * workspace.element_size(), sh)
     if st != 0:
         raise DenseGemmError(st, name)
 
 
 def _layer(layout, A, B, ends, bias, act, residual, preact, grad, D, stream, workspace):
-    lib = _lib or load_library()
+    if _lib is None:
+        load_library()
     torch = _torch()
-    fmt = _check_first(A)
+    fmt, dtype, dev = _check_first(A)
     code = ACTS.get(act)
     if code is None:
         raise ValueError("act must be one of %s, got %r" % (", ".join(ACTS), act))
     M, K = A.shape
-    _check_like(B, A, 2 if ends is None else 3, "B")
+    _check_like(B, dtype, dev, 2 if ends is None else 3, "B")
     if layout == "nt":
         N, Kb = B.shape[-2:]
     else:
@@ -478,7 +485,7 @@ def _layer(layout, A, B, ends, bias, act, residual, preact, grad, D, stream, wor
     if ends is None:
         ldb = _ld(B)
     else:
-        _check_ends(ends, A, torch)
+        _check_ends(ends, dev, torch)
         G = (B.shape[0],)
         if ends.shape[0] != G[0]:
             raise ValueError("%d group ends for %d matrices B" % (ends.shape[0], G[0]))
@@ -488,28 +495,25 @@ def _layer(layout, A, B, ends, bias, act, residual, preact, grad, D, stream, wor
     if code or bias is not None or residual is not None or preact is not None:
         epi = Epilogue(act=code, grad=grad)
         if bias is not None:
-            _check_like(bias, A, 1 + len(G), "bias", G + (N,))
+            _check_like(bias, dtype, dev, 1 + len(G), "bias", G + (N,))
             epi.bias = bias.data_ptr()
             if G and G[0] > 1:
                 epi.bias_stride = bias.stride(0)
         if residual is not None:
-            _check_like(residual, A, 2, "residual", (M, N))
+            _check_like(residual, dtype, dev, 2, "residual", (M, N))
             epi.residual, epi.ldr = residual.data_ptr(), _ld(residual)
         if preact is not None:
-            _check_like(preact, A, 2, "preact", (M, N))
+            _check_like(preact, dtype, dev, 2, "preact", (M, N))
             epi.preact, epi.ldz = preact.data_ptr(), _ld(preact)
-    dev = A.device
     if D is None:
-        D = _used_by(torch.empty((M, N), dtype=A.dtype, device=dev), stream, dev)
+        D = torch.empty((M, N), dtype=dtype, device=A.device)
+        if stream is not None:
+            _used_by(D, stream, A.device)
     else:
-        _check_like(D, A, 2, "D", (M, N))
+        _check_like(D, dtype, dev, 2, "D", (M, N))
     args = (OPS[(layout, fmt[0])], M, N, K, A.data_ptr(), _ld(A), B.data_ptr(), ldb)
-
-    def size_of(need):
-        return lib.dense_gemm_layer_workspace_size(*args, groups, 0, ctypes.byref(need))
-
-    _launch("dense_gemm_layer", args + (D.data_ptr(), _ld(D), epi, groups), size_of, workspace,
-            stream, dev, torch)
+    _launch("dense_gemm_layer", args + (D.data_ptr(), _ld(D), epi, groups),
+            ("dense_gemm_layer_workspace_size",) + args + (groups, 0), workspace, stream, dev, torch)
     return D
 
 
@@ -573,31 +577,37 @@ def gemm_nn_grouped_dact(A, B, ends, preact, act, D=None, stream=None, workspace
 
 
 def _tn(A, B, ends, D, colsum, stream, workspace):
-    lib = _lib or load_library()
+    if _lib is None:
+        load_library()
     torch = _torch()
-    fmt = _check_first(A)
+    fmt, dtype, dev = _check_first(A)
     K, M = A.shape
-    _check_like(B, A, 2, "B")
+    _check_like(B, dtype, dev, 2, "B")
     N = B.shape[1]
     if B.shape[0] != K:
         raise ValueError("row counts differ: A is %s, B is %s" % (tuple(A.shape), tuple(B.shape)))
-    dev = A.device
     G = ()
     if ends is not None:
-        _check_ends(ends, A, torch)
+        _check_ends(ends, dev, torch)
         G = (ends.shape[0],)
+    own = []
     if D is None:
-        D = _used_by(torch.empty(G + (M, N), dtype=A.dtype, device=dev), stream, dev)
+        D = torch.empty(G + (M, N), dtype=dtype, device=A.device)
+        own.append(D)
     else:
-        _check_like(D, A, 2 + len(G), "D", G + (M, N))
+        _check_like(D, dtype, dev, 2 + len(G), "D", G + (M, N))
     sums = None
     if colsum is True:
-        sums = _used_by(torch.empty(G + (M,), dtype=A.dtype, device=dev), stream, dev)
+        sums = torch.empty(G + (M,), dtype=dtype, device=A.device)
+        own.append(sums)
     elif colsum is not None and colsum is not False:
         sums = colsum
-        _check_like(sums, A, 1 + len(G), "colsum", G + (M,))
+        _check_like(sums, dtype, dev, 1 + len(G), "colsum", G + (M,))
         if not sums.is_contiguous():
             raise ValueError("colsum must be contiguous")
+    if stream is not None:
+        for t in own:
+            _used_by(t, stream, A.device)
     groups = None
     if ends is None:
         ldd = _ld(D)
@@ -605,14 +615,10 @@ def _tn(A, B, ends, D, colsum, stream, workspace):
         stride, ldd = _stack(D)
         groups = Groups(ends.data_ptr(), G[0], stride)
     args = (M, N, K, A.data_ptr(), _ld(A), B.data_ptr(), _ld(B))
-
-    def size_of(need):
-        return lib.dense_gemm_tn_workspace_size(*args, sums is not None, groups, 0,
-                                                ctypes.byref(need))
-
     _launch("dense_gemm_tn",
             (fmt[1],) + args + (D.data_ptr(), ldd, None if sums is None else sums.data_ptr(), groups),
-            size_of, workspace, stream, dev, torch)
+            ("dense_gemm_tn_workspace_size",) + args + (sums is not None, groups, 0), workspace,
+            stream, dev, torch)
     return D if sums is None else (D, sums)
 
 

@@ -47,8 +47,6 @@
 namespace dg {
 
 // ---- tile configuration (Layout, BM, BN, BK, WAVES, THREADS: tile_config.h)
-constexpr int SLOTS3 = 3;            // LDS ring depth of the early operand (below)
-constexpr int SLOTS2 = 2;            // LDS ring depth of the other operand
 constexpr int MK = 32;               // K depth of one MFMA (16 x 16 x 32)
 constexpr int SUB = BK / MK;         // MFMA k-substeps per stage
 // Tile rows TM: 256 (BM), or 128 for products with M <= 128 (half the
@@ -96,12 +94,24 @@ struct LayerParams : Params {
   float* colsum_ws;
 };
 
-// Workgroups per CU: two for the 128 x 128 tiles of the layer products (80
-// KiB of LDS and half the registers each), so that one computes while the
-// other waits for its first tiles or writes its last ones.
-template <int LAYOUT, int TN, int TM, bool EPI, bool GROUP>
-constexpr int two_per_cu() {
-  return TM == BM / 2 && TN == BN / 2 && (EPI || GROUP || LAYOUT == TA) ? 2 : 1;
+// Stages loaded ahead of the one in use.  Two, with rings of three slots for
+// one operand and two for the other, fill the LDS for 256-wide tiles.  The
+// 128 x 128 tiles of the layer products are 80 KiB that way:
+//   * many tiles run two workgroups per CU, so that one computes while the
+//     other waits for its first tiles or writes its last ones;
+//   * at most one tile or part per CU (the SPLIT kernels) runs four stages
+//     ahead instead, in 144 KiB, to cover the load latency alone.
+template <int LAYOUT, bool SPLIT, int TN, int TM, bool EPI, bool GROUP>
+constexpr bool pair_tile() {
+  return TM == BM / 2 && TN == BN / 2 && (EPI || GROUP || LAYOUT == TA);
+}
+template <int LAYOUT, bool SPLIT, int TN, int TM, bool EPI, bool GROUP>
+constexpr int stages_ahead() {
+  return pair_tile<LAYOUT, SPLIT, TN, TM, EPI, GROUP>() && SPLIT ? 4 : 2;
+}
+template <int LAYOUT, bool SPLIT, int TN, int TM, bool EPI, bool GROUP>
+constexpr int per_cu() {
+  return pair_tile<LAYOUT, SPLIT, TN, TM, EPI, GROUP>() && !SPLIT ? 2 : 1;
 }
 
 template <int MA, int NB>
@@ -127,7 +137,7 @@ struct Frags {
 //   SUMS       (TA) also the sums of A's columns over k.
 template <typename T, int LAYOUT, bool SPLIT, int TN, int TM, bool EPI = false, bool GROUP = false,
           bool SUMS = false>
-__global__ __launch_bounds__(THREADS, (two_per_cu<LAYOUT, TN, TM, EPI, GROUP>())) void gemm_kernel(
+__global__ __launch_bounds__(THREADS, (per_cu<LAYOUT, SPLIT, TN, TM, EPI, GROUP>())) void gemm_kernel(
     std::conditional_t<EPI || GROUP || LAYOUT == TA, LayerParams, Params> p) {
   static_assert(TN == BN || TN == BN / 2, "tile widths 256 and 128");
   static_assert(TM == BM || TM == BM / 2, "tile rows 256 or 128");
@@ -154,8 +164,9 @@ __global__ __launch_bounds__(THREADS, (two_per_cu<LAYOUT, TN, TM, EPI, GROUP>())
   constexpr int DMA_L = EARLY == 0 ? DMA_B : DMA_PER_OPERAND;   // and of the other
   constexpr int E_BYTES = EARLY == 0 ? A_BYTES : B_TILE;
   constexpr int L_BYTES = EARLY == 0 ? B_TILE : A_BYTES;
-  constexpr int RING2 = SLOTS3 * E_BYTES;            // the two-slot ring follows the other
-  constexpr int LDS_BYTES = RING2 + SLOTS2 * L_BYTES;  // all 160 KiB for 256-wide tiles
+  constexpr int AHEAD = stages_ahead<LAYOUT, SPLIT, TN, TM, EPI, GROUP>();
+  constexpr int RING2 = (AHEAD + 1) * E_BYTES;       // the other ring follows the early one
+  constexpr int LDS_BYTES = RING2 + AHEAD * L_BYTES;   // all 160 KiB for 256-wide tiles
   using Frags = dg::Frags<MI, NI>;
   __shared__ __attribute__((aligned(1024))) char smem[LDS_BYTES];
   const uint32_t lds0 = lds_addr(smem);
@@ -418,7 +429,7 @@ __global__ __launch_bounds__(THREADS, (two_per_cu<LAYOUT, TN, TM, EPI, GROUP>())
       fence();
     };
     auto refill_stage = [&](int ks, int slot) {
-      const Half ha = half_setup(ks, slot, 0);  // A and B slots agree for stages 0 and 1
+      const Half ha = half_setup(ks, slot, 0);  // A and B slots agree for the first stages
       const Half hb = half_setup(ks, slot, 1);
 #pragma unroll
       for (int i = 0; i < DMA_PER_OPERAND; ++i) refill_one(ha, 0, i, true);
@@ -485,7 +496,9 @@ __global__ __launch_bounds__(THREADS, (two_per_cu<LAYOUT, TN, TM, EPI, GROUP>())
       }
     };
 
-    // The rings: stage ks (counted from the task's first step) keeps its
+    // The rings (AHEAD = 2; with more, the rings have AHEAD + 1 and AHEAD
+    // slots, and "ks+2" below reads "ks+AHEAD", the stages between in
+    // flight): stage ks (counted from the task's first step) keeps its
     // EARLY operand's tile in slot ks % 3 of the three-slot ring and the
     // other's in slot ks % 2 of the two-slot ring.  Entering step ks, stage
     // ks has landed, stage ks+1 is in flight, and F0 holds substep 0 of
@@ -505,7 +518,11 @@ __global__ __launch_bounds__(THREADS, (two_per_cu<LAYOUT, TN, TM, EPI, GROUP>())
     Frags F0, F1;
     refill_stage(kbeg, 0);
     refill_stage(kbeg + 1, 1);
-    wait_vm_barrier<DMA_PER_OPERAND + DMA_B>();
+    if constexpr (AHEAD > 2) {
+      refill_stage(kbeg + 2, 2);
+      refill_stage(kbeg + 3, 3);
+    }
+    wait_vm_barrier<(AHEAD - 1) * (DMA_PER_OPERAND + DMA_B)>();
     read_frags(0, 0, 0, F0);
 
     // Column sums of A: a lane adds the eight k that it holds of each A
@@ -525,9 +542,10 @@ __global__ __launch_bounds__(THREADS, (two_per_cu<LAYOUT, TN, TM, EPI, GROUP>())
     }
     int es = 0;  // early-ring slot of stage ks
     for (int ks = kbeg; ks < kend; ++ks) {
-      const int ls = (ks - kbeg) & 1;           // two-slot-ring slot of stage ks
-      const int es1 = es == 2 ? 0 : es + 1;     // early-ring slot of stage ks+1
-      const int es2 = es1 == 2 ? 0 : es1 + 1;   // early-ring slot of stage ks+2
+      const int ls = (ks - kbeg) & (AHEAD - 1);     // other-ring slot of stage ks
+      const int es1 = es == AHEAD ? 0 : es + 1;     // early-ring slot of stage ks+1
+      // early-ring slot of stage ks+AHEAD (that of stage ks-1)
+      const int es2 = AHEAD == 2 ? (es1 == 2 ? 0 : es1 + 1) : (es == 0 ? AHEAD : es - 1);
       Half he;
 #pragma unroll
       for (int q = 0; q < PAIRS; ++q) {
@@ -535,7 +553,7 @@ __global__ __launch_bounds__(THREADS, (two_per_cu<LAYOUT, TN, TM, EPI, GROUP>())
         mfma_pair(F0, q);
         fence();
         // (the descriptor's scalar work goes behind the first MFMAs)
-        if (q == 0) he = half_setup(ks + 2, es2, EARLY);
+        if (q == 0) he = half_setup(ks + AHEAD, es2, EARLY);
         // stages from the third on start at k >= 0: no masks
         share(q, PAIRS, DMA_E, [&](int i) { refill_one(he, EARLY, i, false); });
       }
@@ -553,15 +571,16 @@ __global__ __launch_bounds__(THREADS, (two_per_cu<LAYOUT, TN, TM, EPI, GROUP>())
         }
         fence();
       }
-      const Half hl = half_setup(ks + 2, ls, 1 - EARLY);
+      const Half hl = half_setup(ks + AHEAD, ls, 1 - EARLY);
 #pragma unroll
       for (int q = 0; q < PAIRS; ++q) {
         if (q == BAR_PAIR) {
-          wait_vm_barrier<DMA_E>();
+          wait_vm_barrier<(AHEAD - 2) * (DMA_E + DMA_L) + DMA_E>();
           fence();
         }
         if (q >= BAR_PAIR)
-          share(q - BAR_PAIR, PAIRS - BAR_PAIR, READS, [&](int f) { read_item(es1, ls ^ 1, 0, F0, f); });
+          share(q - BAR_PAIR, PAIRS - BAR_PAIR, READS,
+                [&](int f) { read_item(es1, AHEAD == 2 ? ls ^ 1 : (ls + 1) & (AHEAD - 1), 0, F0, f); });
         mfma_pair(F1, q);
         fence();
         if (q >= BAR_PAIR)
@@ -618,9 +637,14 @@ __global__ __launch_bounds__(THREADS, (two_per_cu<LAYOUT, TN, TM, EPI, GROUP>())
       // residual could only be added after a first rounding.)  Chunk c of
       // row r is stored at c ^ (c >> 3 & 1) ^ (r & 7): the writes (one chunk
       // of eight rows) and the reads (every other chunk of a row) both touch
-      // distinct banks.  The loop over the bands is not unrolled: the code of
+      // distinct banks.  The loop over the passes is not unrolled: the code of
       // eight activations and slopes stays small enough for the instruction
-      // cache beside the K loop.
+      // cache beside the K loop.  A pass reads the next one's residual or Z
+      // from memory before it computes, and where a wave has its SIMD to
+      // itself (nothing else would cover the latency) the next one's values
+      // from LDS too: 4096^3 without an activation 103 -> 97 us; with two
+      // workgroups per CU the registers that takes cost more (48 ragged
+      // groups, 53 us against 56).
       constexpr int CH = WTN / 8;      // lanes per staged row
       constexpr int CHF = WTN / 4;     // 16-byte chunks per staged row
       constexpr int RPI = 64 / CH;     // rows per wave instruction
@@ -670,18 +694,7 @@ __global__ __launch_bounds__(THREADS, (two_per_cu<LAYOUT, TN, TM, EPI, GROUP>())
 #pragma unroll
       for (int t = 0; t < R; ++t)
         asm volatile("" : "+v"(w[t][0]), "+v"(w[t][1]), "+v"(w[t][2]), "+v"(w[t][3]));
-#pragma unroll 1
-      for (int pass = 0; pass < (MI / 2) * PASSES; ++pass) {
-        if (pass % PASSES == 0) {
-          switch (pass / PASSES) {
-            case 0: break;
-            case 1: stage(1); break;
-            case 2: if constexpr (MI > 4) stage(2); break;
-            default: if constexpr (MI > 4) stage(3); break;
-          }
-        }
-        if (pass + 1 < (MI / 2) * PASSES) fetch(pass + 1, w_next);
-        float v[R][8];
+      auto read_staged = [&](int pass, float(&v)[R][8]) {
 #pragma unroll
         for (int t = 0; t < R; ++t) {
           const int r = (pass % PASSES * R + t) * RPI + rl;
@@ -693,6 +706,29 @@ __global__ __launch_bounds__(THREADS, (two_per_cu<LAYOUT, TN, TM, EPI, GROUP>())
             for (int k = 0; k < 4; ++k) v[t][4 * h + k] = x[k];
           }
         }
+      };
+      constexpr bool PIPE = per_cu<LAYOUT, SPLIT, TN, TM, EPI, GROUP>() == 1;
+      float v[R][8];
+      [[maybe_unused]] float v_next[R][8];
+      if constexpr (PIPE) read_staged(0, v);
+#pragma unroll 1
+      for (int pass = 0; pass < (MI / 2) * PASSES; ++pass) {
+        // (a wave's LDS accesses complete in order: the next band's writes
+        // follow the reads of this one's last values)
+        const int to_stage = PIPE ? pass + 1 : pass;  // the pass whose band to stage now
+        if (to_stage % PASSES == 0) {
+          switch (to_stage / PASSES) {
+            case 1: stage(1); break;
+            case 2: if constexpr (MI > 4) stage(2); break;
+            case 3: if constexpr (MI > 4) stage(3); break;
+            default: break;
+          }
+        }
+        if (pass + 1 < (MI / 2) * PASSES) {
+          fetch(pass + 1, w_next);
+          if constexpr (PIPE) read_staged(pass + 1, v_next);
+        }
+        if constexpr (!PIPE) read_staged(pass, v);
         if (part) {
           // the part's FP32 partial tile, row-major TM x TN (elements outside
           // D are skipped: nothing reads them)
@@ -746,6 +782,9 @@ __global__ __launch_bounds__(THREADS, (two_per_cu<LAYOUT, TN, TM, EPI, GROUP>())
             store_row<4>(gD + (int64_t)row * p.ldd, col, p.N, o);
 #pragma unroll
           for (int k = 0; k < 4; ++k) w[t][k] = w_next[t][k];
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            if constexpr (PIPE) v[t][k] = v_next[t][k];
         }
       }
       wait_lds_barrier();

@@ -48,8 +48,11 @@ static dense_gemm_status enqueue_tiled(const LayerCall& c, const CallPlan& cp, f
   p.e = device_epilogue(c.e);
   const int slots = c.cus * (int)resident(TM, TN);
   const dim3 grid((unsigned)(p.num_tasks < slots ? p.num_tasks : slots)), block(THREADS);
-  if (p.splits > 1) {
+  if (p.splits > 1 || (resident(TM, TN) > 1 && p.num_tasks <= c.cus)) {
+    // (whole 128 x 128 tiles that have a CU each also run this kernel, for
+    // its deeper rings)
     hipLaunchKernelGGL((gemm_kernel<T, LAYOUT, true, TN, TM, true>), grid, block, 0, c.stream, p);
+    if (p.splits == 1) return launched();
     LayerReduceParams r = {};
     (ReduceParams&)r = {p.D, p.ws, p.M, p.N, p.ldd, p.tiles_m, p.tiles_n, p.group_m,
                         p.full_tasks, p.splits, p.tiles, p.d_vec};

@@ -104,13 +104,13 @@ dense_gemm_status layer_validate(int op, int64_t M, int64_t N, int64_t K, const 
 //   * 256 x 128 and 128 x 256: one wave of 75 nk + 960, a split 600 and 1.5 a
 //     partial tile;
 //   * 128 x 128, two workgroups per CU: waves x (79 nk + 650); where each has
-//     a CU to itself 47 nk + 550, and split-K costs 700 and 1 per partial tile.
+//     a CU to itself 35 (A @ B.T) or 41 nk + 550, and split-K costs 600 and 1
+//     per partial tile.
 // Measured, us, the plain product's plan against 128 x 128: A @ B.T 2048 x
-// 2048 x 2048 30 against 22, 777 x 1000 x 2048 29 against 19 (in 3 parts),
-// 4096 x 2048 x 1024 22 against 20, x 4096 56 against 57, 4096 x 4096 x 512
-// 27 against 25; A @ B 2048 x 2048 x 2048 51 against 23, 4096 x 2048 x 4096
-// 88 against 60, 512 x 512 x 4096 29 against 17, 100 x 8000 x 3000 25 against
-// 21.
+// 2048 x 2048 30 against 21, 777 x 1000 x 2048 29 against 19, 4096 x 2048 x
+// 1024 22 against 20, x 4096 56 against 57, 4096 x 4096 x 512 27 against 25;
+// A @ B 2048 x 2048 x 2048 51 against 23, 4096 x 2048 x 4096 88 against 60,
+// 512 x 512 x 4096 29 against 18 (in 8 parts), 100 x 8000 x 3000 25 against 21.
 dense_gemm_status layer_plan(int layout, int64_t M, int64_t N, int64_t K, const void* A,
                              int64_t lda, const void* B, int64_t ldb, int64_t cus, CallPlan* cp) {
   const dense_gemm_status st = plan_call(layout, M, N, K, A, lda, B, ldb, cus, nullptr, cp);
@@ -129,12 +129,13 @@ dense_gemm_status layer_plan(int layout, int64_t M, int64_t N, int64_t K, const 
   const int64_t tiles_m = (M + BM / 2 - 1) / (BM / 2), tiles_n = (N + BN / 2 - 1) / (BN / 2);
   const int64_t tasks = tiles_m * tiles_n, slots = cus * resident(BM / 2, BN / 2);
   int64_t splits = 1, steps = nk;
-  if (tasks < cus) choose_split(tasks, nk, cus, 50, 700, 1, BM / 16, &splits, &steps);
+  const int64_t step = layout == NT ? 35 : 41;
+  if (tasks < cus) choose_split(tasks, nk, cus, step, 600, 1, BM / 16, &splits, &steps);
   double narrow;
   if (splits > 1)
-    narrow = 50.0 * steps + 1250 + splits * tasks;
+    narrow = (double)step * steps + 1150 + splits * tasks;
   else if (tasks <= cus)
-    narrow = 47.0 * nk + 550;
+    narrow = (double)step * nk + 550;
   else
     narrow = (double)((tasks + slots - 1) / slots) * (79 * nk + 650);
   if (narrow >= cost || tasks >= kMaxDim || (tasks > slots && nk > NARROW_STEPS)) return st;
@@ -256,9 +257,9 @@ dense_gemm_status tn_validate(int fmt, int64_t M, int64_t N, int64_t K, const vo
 //   * 256 x 256 tiles, one workgroup per CU: waves x (133 per K step + 850);
 //     split-K as for the other products (choose_split: 105, 1200, 12; a split
 //     last wave costs 2500 on top of its steps);
-//   * 128 x 128 tiles, two per CU: waves x (90 per K step + 360), or 50 per
-//     step where each has a CU to itself; split-K only then (1000 for the
-//     second kernel, 1 per partial tile).
+//   * 128 x 128 tiles, two per CU: waves x (90 per K step + 360), or 47 per
+//     step + 550 where each has a CU to itself; split-K only then (600 for
+//     the second kernel, 1 per partial tile).
 // Measured 256 against 128, us: 4096 x 4096 x 2048 64 against 69; 4096 x 2304
 // x 4096 93 against 111, 4096 x 2048 x 4096 93 against 64 (512 of the smaller
 // tiles: just one wave); 2048 x 2048 x 8192 in 4 parts 77 against 73; 512 x
@@ -288,9 +289,9 @@ static TnChoice tn_choice(int64_t M, int64_t N, int64_t nk, int64_t groups, bool
       c.cost = (double)(waves - 1) * (133 * nk + 850) + 133 * ((nk + c.splits - 1) / c.splits) + 850 + 2500 +
                (tasks < cus ? 12 * c.splits * last - 1300 : 0);
   } else if (tasks < cus) {
-    choose_split(tasks, reach, cus, 50, 1000, 1, BM / 16, &c.splits, &c.steps);
-    c.cost = 50 * ((nk + c.splits - 1) / c.splits) + 360 +
-             (c.splits > 1 ? 1000 + c.splits * tasks : 0);
+    choose_split(tasks, reach, cus, 47, 600, 1, BM / 16, &c.splits, &c.steps);
+    c.cost = 47 * ((nk + c.splits - 1) / c.splits) + 550 +
+             (c.splits > 1 ? 600 + c.splits * tasks : 0);
   } else {
     c.cost = (double)waves * (90 * nk + 360);
     if (waves > 1 && nk > NARROW_STEPS) c.cost = 1e30;

@@ -15,9 +15,12 @@ template <typename T, int TILE, bool GROUP, bool SUMS>
 static void enqueue_tile(const LayerParams& p, int cus, hipStream_t stream) {
   const int slots = cus * (int)resident(TILE, TILE);
   const dim3 grid((unsigned)(p.num_tasks < slots ? p.num_tasks : slots)), block(THREADS);
-  if (p.splits > 1) {
+  if (p.splits > 1 || (resident(TILE, TILE) > 1 && p.num_tasks <= cus)) {
+    // (whole 128 x 128 tiles that have a CU each also run this kernel, for
+    // its deeper rings)
     hipLaunchKernelGGL((gemm_kernel<T, TA, true, TILE, TILE, false, GROUP, SUMS>), grid, block, 0,
                        stream, p);
+    if (p.splits == 1) return;
     LayerReduceParams r = {};
     (ReduceParams&)r = {p.D, p.ws, p.M, p.N, p.ldd, p.tiles_m, p.tiles_n, p.group_m,
                         p.full_tasks, p.splits, p.tiles, p.d_vec};
