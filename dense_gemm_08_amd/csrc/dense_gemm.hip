@@ -17,7 +17,6 @@
 #include "gemm_kernel.h"
 #include "gemm_small_kernel.h"
 #include "plan.h"
-#include "repack.h"
 #include "split_reduce.h"
 
 namespace dg {

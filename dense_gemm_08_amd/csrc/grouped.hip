@@ -39,13 +39,13 @@ dense_gemm_status run_grouped(LayerCall c, const dense_gemm_groups& groups, void
   p.e = device_epilogue(c.e);
   p.g = g;
   if (gp.tile_n == BN / 2)
-    hipLaunchKernelGGL((gemm_kernel<T, LAYOUT, false, BN / 2, BM / 2, true, true>), grid,
+    hipLaunchKernelGGL((layer_gemm_kernel<T, LAYOUT, false, BN / 2, BM / 2, true>), grid,
                        dim3(THREADS), 0, c.stream, p);
   else if (gp.tile_m == BM / 2)
-    hipLaunchKernelGGL((gemm_kernel<T, LAYOUT, false, BN, BM / 2, true, true>), grid, dim3(THREADS), 0,
+    hipLaunchKernelGGL((layer_gemm_kernel<T, LAYOUT, false, BN, BM / 2, true>), grid, dim3(THREADS), 0,
                        c.stream, p);
   else
-    hipLaunchKernelGGL((gemm_kernel<T, LAYOUT, false, BN, BM, true, true>), grid, dim3(THREADS), 0,
+    hipLaunchKernelGGL((layer_gemm_kernel<T, LAYOUT, false, BN, BM, true>), grid, dim3(THREADS), 0,
                        c.stream, p);
   return launched();
 }

@@ -25,7 +25,7 @@ void enqueue_repacks(const Repack& a, const Repack& b, hipStream_t stream) {
     while (j.lanes < 256 && j.lanes * 8 < j.dcols) j.lanes *= 2;
     const int64_t per = 256 / j.lanes;
     j.blocks = (r.count * r.rows + per - 1) / per;
-    if (j.blocks > REPACK_MAX_BLOCKS) j.blocks = REPACK_MAX_BLOCKS;
+    if (j.blocks > REPACK_GROUPS_MAX_BLOCKS) j.blocks = REPACK_GROUPS_MAX_BLOCKS;
     grid += j.blocks;
   }
   if (grid > 0)
@@ -51,15 +51,15 @@ static dense_gemm_status enqueue_tiled(const LayerCall& c, const CallPlan& cp, f
   if (p.splits > 1 || (resident(TM, TN) > 1 && p.num_tasks <= c.cus)) {
     // (whole 128 x 128 tiles that have a CU each also run this kernel, for
     // its deeper rings)
-    hipLaunchKernelGGL((gemm_kernel<T, LAYOUT, true, TN, TM, true>), grid, block, 0, c.stream, p);
+    hipLaunchKernelGGL((layer_gemm_kernel<T, LAYOUT, true, TN, TM, false>), grid, block, 0, c.stream, p);
     if (p.splits == 1) return launched();
     LayerReduceParams r = {};
     (ReduceParams&)r = {p.D, p.ws, p.M, p.N, p.ldd, p.tiles_m, p.tiles_n, p.group_m,
-                        p.full_tasks, p.splits, p.tiles, p.d_vec};
+                        p.full_tasks, p.splits, p.tiles, 1};
     r.e = p.e;
     enqueue_split_reduce<T, TN, TM>(r, c.cus, c.stream);
   } else {
-    hipLaunchKernelGGL((gemm_kernel<T, LAYOUT, false, TN, TM, true>), grid, block, 0, c.stream, p);
+    hipLaunchKernelGGL((layer_gemm_kernel<T, LAYOUT, false, TN, TM, false>), grid, block, 0, c.stream, p);
   }
   return launched();
 }

@@ -7,8 +7,8 @@
 #include <stdint.h>
 
 #include "dense_gemm.h"
-#include "gemm_kernel.h"
 #include "gemm_small_kernel.h"
+#include "layer_kernel.h"
 #include "plan_layer.h"
 
 namespace dg {
@@ -75,7 +75,7 @@ inline void repack_operands(LayerCall& c, void* a_dst, int64_t count, int64_t b_
   }
 }
 
-inline void set_operands(Params& p, const LayerCall& c) {
+inline void set_operands(LayerParams& p, const LayerCall& c) {
   p.A = c.A;
   p.B = c.B;
   p.D = c.D;
@@ -86,7 +86,6 @@ inline void set_operands(Params& p, const LayerCall& c) {
   p.ldb = (int)c.ldb;
   p.ldd = (int)c.ldd;
   p.num_xcds = c.xcds;
-  p.d_vec = 1;  // (D's 16-byte stores take any alignment in these kernels)
 }
 
 inline SmallLayerParams small_params(const LayerCall& c) {

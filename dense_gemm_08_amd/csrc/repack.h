@@ -12,31 +12,7 @@
 
 namespace dg {
 
-// Copy of a rows x cols matrix of 16-bit elements (any leading dimension,
-// 2-byte alignment) into a dense, 16-byte aligned rows x dcols matrix
-// (dcols = cols rounded up to 8), zero-filling columns cols .. dcols-1: the
-// layout the tiled kernel's 16-byte chunk loads need.  Each thread handles
-// 8-element chunks of the destination, striding over the grid.
-constexpr int64_t REPACK_MAX_BLOCKS = 1 << 16;
-[[maybe_unused]] static __global__ __launch_bounds__(256) void repack(
-    const uint16_t* __restrict__ src, int64_t rows, int64_t cols, int64_t ld,
-    uint16_t* __restrict__ dst, int64_t dcols) {
-  const int64_t chunks = dcols / 8, total = rows * chunks;
-  const int64_t stride = (int64_t)gridDim.x * blockDim.x;
-  for (int64_t gid = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; gid < total; gid += stride) {
-    const int64_t r = gid / chunks;
-    const int64_t c0 = (gid % chunks) * 8;
-    const uint16_t* s = src + r * ld + c0;
-    uint32_t w[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const uint32_t lo = c0 + 2 * e < cols ? s[2 * e] : 0u;
-      const uint32_t hi = c0 + 2 * e + 1 < cols ? s[2 * e + 1] : 0u;
-      w[e] = lo | (hi << 16);
-    }
-    *(u32x4*)(dst + r * dcols + c0) = (u32x4){w[0], w[1], w[2], w[3]};
-  }
-}
+constexpr int64_t REPACK_GROUPS_MAX_BLOCKS = 1 << 16;
 
 // A copy of `count` matrices of rows x cols 16-bit elements (any leading
 // dimension and distance, 2-byte alignment) into dense, 16-byte aligned ones

@@ -18,16 +18,16 @@ static void enqueue_tile(const LayerParams& p, int cus, hipStream_t stream) {
   if (p.splits > 1 || (resident(TILE, TILE) > 1 && p.num_tasks <= cus)) {
     // (whole 128 x 128 tiles that have a CU each also run this kernel, for
     // its deeper rings)
-    hipLaunchKernelGGL((gemm_kernel<T, TA, true, TILE, TILE, false, GROUP, SUMS>), grid, block, 0,
+    hipLaunchKernelGGL((layer_gemm_kernel<T, TA, true, TILE, TILE, GROUP, SUMS>), grid, block, 0,
                        stream, p);
     if (p.splits == 1) return;
     LayerReduceParams r = {};
     (ReduceParams&)r = {p.D, p.ws, p.M, p.N, p.ldd, p.tiles_m, p.tiles_n, p.group_m,
-                        p.full_tasks, p.splits, p.tiles, p.d_vec};
+                        p.full_tasks, p.splits, p.tiles, 1};
     r.stride = p.g.stride;
     enqueue_split_reduce<T, TILE, TILE>(r, cus, stream);
   } else {
-    hipLaunchKernelGGL((gemm_kernel<T, TA, false, TILE, TILE, false, GROUP, SUMS>), grid, block, 0,
+    hipLaunchKernelGGL((layer_gemm_kernel<T, TA, false, TILE, TILE, GROUP, SUMS>), grid, block, 0,
                        stream, p);
   }
 }
