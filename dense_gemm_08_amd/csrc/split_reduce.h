@@ -13,6 +13,7 @@
 #include <type_traits>
 
 #include "cdna_ops.h"
+#include "column_sums.h"
 #include "epilogue.h"
 #include "tile_sched.h"
 
@@ -35,9 +36,12 @@ struct ReduceParams {
 // For a layer's products (layer.hip, tn.hip): the epilogue applied to the
 // sums, and for A.T @ B over row groups one D per group (tile t of the order
 // is tile t % (tiles_m * tiles_n) of group t / that).
+// A launch's workgroups beyond those of the tiles add up column sums.
 struct LayerReduceParams : ReduceParams {
   Epilogue e;
   int64_t stride;  // elements between the groups' D
+  ColumnSumsParams sums;
+  int64_t sums_blocks;
 };
 
 // One thread per 8 consecutive columns of a row, RT threads per workgroup:
@@ -56,6 +60,12 @@ __global__ __launch_bounds__(RT) void split_reduce(
   constexpr int RPW = RT / TPR;    // rows per workgroup
   constexpr int WPT = TM / RPW;    // workgroups per split tile
   static_assert(RT % TPR == 0 && WPT == reduce_blocks_per_tile<TN, RT, TM>(), "whole rows per workgroup");
+  if constexpr (LAYER) {
+    if ((int)blockIdx.x >= p.tiles * WPT) {
+      column_sums_block<T, TM, RT>(p.sums, (int)blockIdx.x - p.tiles * WPT);
+      return;
+    }
+  }
   const int st = blockIdx.x / WPT;      // split tile (0 .. tiles-1)
   int tm, tn;
   uint16_t* D = p.D;
@@ -151,13 +161,15 @@ template <typename T, int TN, int TM, typename P>
 static inline void enqueue_split_reduce(const P& r, int cus, hipStream_t stream) {
   constexpr bool LAYER = std::is_same_v<P, LayerReduceParams>;
   const int64_t wide = r.tiles * (int64_t)reduce_blocks_per_tile<TN, 256, TM>();
+  int64_t more = 0;
+  if constexpr (LAYER) more = r.sums_blocks;
   if (wide < cus)
     hipLaunchKernelGGL((split_reduce<T, TN, 64, TM, LAYER>),
-                       dim3((unsigned)(r.tiles * reduce_blocks_per_tile<TN, 64, TM>())), dim3(64), 0,
-                       stream, r);
+                       dim3((unsigned)(r.tiles * reduce_blocks_per_tile<TN, 64, TM>() + more)),
+                       dim3(64), 0, stream, r);
   else
-    hipLaunchKernelGGL((split_reduce<T, TN, 256, TM, LAYER>), dim3((unsigned)wide), dim3(256), 0,
-                       stream, r);
+    hipLaunchKernelGGL((split_reduce<T, TN, 256, TM, LAYER>), dim3((unsigned)(wide + more)),
+                       dim3(256), 0, stream, r);
 }
 
 }  // namespace dg

@@ -12,41 +12,45 @@
 namespace dg {
 
 template <typename T, int TILE, bool GROUP, bool SUMS>
-static void enqueue_tile(const LayerParams& p, int cus, hipStream_t stream) {
+static void enqueue_tile(const LayerParams& p, const ColumnSumsParams& sums, int64_t sums_blocks,
+                         int cus, hipStream_t stream) {
   const int slots = cus * (int)resident(TILE, TILE);
   const dim3 grid((unsigned)(p.num_tasks < slots ? p.num_tasks : slots)), block(THREADS);
-  if (p.splits > 1 || (resident(TILE, TILE) > 1 && p.num_tasks <= cus)) {
+  if (p.splits > 1 || (resident(TILE, TILE) > 1 && p.num_tasks <= cus))
     // (whole 128 x 128 tiles that have a CU each also run this kernel, for
     // its deeper rings)
     hipLaunchKernelGGL((layer_gemm_kernel<T, TA, true, TILE, TILE, GROUP, SUMS>), grid, block, 0,
                        stream, p);
-    if (p.splits == 1) return;
+  else
+    hipLaunchKernelGGL((layer_gemm_kernel<T, TA, false, TILE, TILE, GROUP, SUMS>), grid, block, 0,
+                       stream, p);
+  if (p.splits > 1) {
     LayerReduceParams r = {};
     (ReduceParams&)r = {p.D, p.ws, p.M, p.N, p.ldd, p.tiles_m, p.tiles_n, p.group_m,
                         p.full_tasks, p.splits, p.tiles, 1};
     r.stride = p.g.stride;
+    r.sums = sums;
+    r.sums_blocks = sums_blocks;
     enqueue_split_reduce<T, TILE, TILE>(r, cus, stream);
-  } else {
-    hipLaunchKernelGGL((layer_gemm_kernel<T, TA, false, TILE, TILE, GROUP, SUMS>), grid, block, 0,
-                       stream, p);
+  } else if constexpr (SUMS) {
+    hipLaunchKernelGGL((column_sums<T, TILE>), dim3((unsigned)sums_blocks), dim3(CS_THREADS), 0,
+                       stream, sums);
   }
 }
 
 template <typename T, int TILE>
 static dense_gemm_status enqueue_tn(const LayerParams& p, uint16_t* colsum, int groups, bool grouped,
                                     int cus, hipStream_t stream) {
-  if (colsum == nullptr) {
-    grouped ? enqueue_tile<T, TILE, true, false>(p, cus, stream)
-            : enqueue_tile<T, TILE, false, false>(p, cus, stream);
-    return launched();
-  }
-  grouped ? enqueue_tile<T, TILE, true, true>(p, cus, stream)
-          : enqueue_tile<T, TILE, false, true>(p, cus, stream);
   const ColumnSumsParams s = {p.colsum_ws, colsum, p.M, groups, p.tiles_m, p.tiles_n, p.group_m,
                               p.full_tasks, p.splits, p.tiles};
-  hipLaunchKernelGGL((column_sums<T, TILE>),
-                     dim3((unsigned)((int64_t)groups * ((p.M + CS_COLS - 1) / CS_COLS))),
-                     dim3(CS_COLS * CS_LANES), 0, stream, s);
+  if (colsum == nullptr) {
+    grouped ? enqueue_tile<T, TILE, true, false>(p, s, 0, cus, stream)
+            : enqueue_tile<T, TILE, false, false>(p, s, 0, cus, stream);
+  } else {
+    const int64_t blocks = column_sums_blocks(p.M, groups);
+    grouped ? enqueue_tile<T, TILE, true, true>(p, s, blocks, cus, stream)
+            : enqueue_tile<T, TILE, false, true>(p, s, blocks, cus, stream);
+  }
   return launched();
 }
 
