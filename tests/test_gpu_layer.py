@@ -310,6 +310,9 @@ GROUPS = [  # (sizes, rows behind the last, N, K)
     (spread(100, 1500, 1), 9, 200, 96),
     (spread(200, 260, 2), 0, 56, 128),
     (spread(12, 5000, 3), 33, 1100, 160),
+    # more groups than a wave holds in registers (256): few and many rows each
+    (spread(300, 900, 9), 4, 72, 64), ([1] * 700, 3, 16, 40), (spread(600, 30000, 10), 1, 136, 72),
+    ([0] * 400 + [5] + [0] * 100 + [300], 2, 264, 64),
     (spread(5, 77, 4), 0, 1001, 333),
     (spread(9, 2000, 5), 12, 301, 75),
 ]

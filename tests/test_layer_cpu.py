@@ -6,6 +6,8 @@ waits in the rings, scratch memory."""
 import ctypes
 import os
 import re
+import shutil
+import subprocess
 
 import pytest
 
@@ -232,6 +234,20 @@ def test_python_entry_points_refuse_host_tensors():
             call()
     with pytest.raises(TypeError):
         dg.gemm_tn(A.float(), A.float())
+
+
+@pytest.mark.skipif(shutil.which("g++") is None, reason="g++ not available")
+def test_planning_under_sanitizers(tmp_path):
+    here = os.path.dirname(os.path.abspath(__file__))
+    csrc = os.path.join(os.path.dirname(here), "dense_gemm_08_amd", "csrc")
+    exe = str(tmp_path / "layer_fuzz")
+    subprocess.run(["g++", "-std=c++17", "-Wall", "-fsanitize=address,undefined",
+                    "-fno-sanitize-recover=all", "-g", "-O1",
+                    "-I", os.path.join(os.path.dirname(here), "include"), "-I", csrc,
+                    os.path.join(here, "layer_fuzz.cpp"), os.path.join(csrc, "plan.cpp"),
+                    os.path.join(csrc, "plan_layer.cpp"), "-o", exe], check=True)
+    r = subprocess.run([exe], capture_output=True, text=True, timeout=600)
+    assert r.returncode == 0 and r.stdout.startswith("planned"), r.stdout + r.stderr[-4000:]
 
 
 # ---- generated code -------------------------------------------------------------
