@@ -459,6 +459,8 @@ def _launch(name, args, size_of, workspace, stream, dev, torch):
     else:
         if workspace.get_device() != dev:
             raise ValueError("workspace must be a device tensor on cuda:%d" % dev)
+        if not workspace.is_contiguous():  # (its bytes are not its elements')
+            raise ValueError("workspace must be contiguous")
         st = fn(*args, workspace.data_ptr(), workspace.numel() * workspace.element_size(), sh)
     if st != 0:
         raise DenseGemmError(st, name)

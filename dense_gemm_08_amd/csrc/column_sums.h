@@ -1,5 +1,5 @@
 // column_sums.h -- the last step of the column sums of A that accompany D =
-// A.T @ B on the MI355X (gfx950): gemm_kernel<..., SUMS> leaves FP32 sums over
+// A.T @ B on the MI355X (gfx950): layer_gemm_kernel<..., SUMS> leaves FP32 sums over
 // shares of K, here they are added in a fixed order and rounded once.
 #pragma once
 
@@ -16,7 +16,7 @@ struct ColumnSumsParams {
   int M, groups;
   int tiles_m, tiles_n, group_m;
   // tasks below full_tasks are whole tiles, then come `splits` parts of each
-  // of the last `tiles` tiles (gemm_kernel.h: Params)
+  // of the last `tiles` tiles (layer_kernel.h)
   int full_tasks, splits, tiles;
 };
 
@@ -73,11 +73,16 @@ __device__ __forceinline__ void column_sums_block(const ColumnSumsParams& p, int
   }
 }
 
-// The sums alone.
+// The sums alone, in up to CS_MAX_GRID workgroups (a launch holds fewer than
+// 2^32 threads, many groups can have more blocks than that).
 constexpr int CS_THREADS = 256;
+constexpr int64_t CS_MAX_GRID = 1 << 16;
 template <typename T, int TM>
-__global__ __launch_bounds__(CS_THREADS) void column_sums(ColumnSumsParams p) {
-  column_sums_block<T, TM, CS_THREADS>(p, blockIdx.x);
+__global__ __launch_bounds__(CS_THREADS) void column_sums(ColumnSumsParams p, int blocks) {
+  for (int64_t b = blockIdx.x; b < blocks; b += gridDim.x) {
+    column_sums_block<T, TM, CS_THREADS>(p, (int)b);
+    __syncthreads();
+  }
 }
 
 }  // namespace dg

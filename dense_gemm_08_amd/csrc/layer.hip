@@ -1,11 +1,10 @@
 // layer.hip -- the products of a transformer layer on the MI355X (gfx950):
 // the FP16/BF16 product with bias, activation and residual in its epilogue
 // and its gradient form (dense_gemm_layer, include/dense_gemm.h).  Host side:
-// the plan (that of the plain product, plan.cpp), the launches and the C ABI
-// entry point, which hands calls with row groups to grouped.hip.  The kernels
-// are those of the plain products with the template parameters that
-// gemm_kernel.h and gemm_small_kernel.h describe; epilogue.h holds what is
-// new in them.
+// the plan (layer_plan in plan_layer.cpp), the launches and the C ABI entry
+// point, which hands calls with row groups to grouped.hip.  The kernels are
+// layer_gemm_kernel (layer_kernel.h) and, for small outputs, gemm_small with
+// the epilogue of epilogue.h.
 #include "layer_host.h"
 #include "repack.h"
 #include "split_reduce.h"

@@ -75,8 +75,12 @@ dense_gemm_status layer_validate(int op, int64_t M, int64_t N, int64_t K, const 
   if (g != nullptr) {
     st = check_groups(g);
     if (st != DENSE_GEMM_OK) return st;
+    if (g->count > kLayerMaxGroups) return DENSE_GEMM_TOO_LARGE;
   }
   if (M == 0 || N == 0 || (g != nullptr && g->count == 0)) return DENSE_GEMM_OK;
+  if (M > kLayerMaxDim || N > kLayerMaxDim || K > kLayerMaxDim) return DENSE_GEMM_TOO_LARGE;
+  const int64_t tile = BM / 2;  // the smallest of the tiled kernels
+  if (((M + tile - 1) / tile) * ((N + tile - 1) / tile) > kLayerMaxTiles) return DENSE_GEMM_TOO_LARGE;
   if (e != nullptr) {
     if (e->grad != 0 && e->preact == nullptr) return DENSE_GEMM_NULL_PTR;
     if (((uintptr_t)e->bias & 1) != 0) return DENSE_GEMM_MISALIGNED;
@@ -88,8 +92,8 @@ dense_gemm_status layer_validate(int op, int64_t M, int64_t N, int64_t K, const 
   if (g != nullptr) {
     if (g->ends == nullptr) return DENSE_GEMM_NULL_PTR;
     if (((uintptr_t)g->ends & 3) != 0) return DENSE_GEMM_MISALIGNED;
-    // tile numbers are 32-bit: the smallest tiles there are
-    if (most_row_tiles(M, g->count, SMALL_TILE) * ((N + SMALL_TILE - 1) / SMALL_TILE) >= kMaxDim)
+    // the smallest tiles there are
+    if (most_row_tiles(M, g->count, SMALL_TILE) * ((N + SMALL_TILE - 1) / SMALL_TILE) > kLayerMaxTiles)
       return DENSE_GEMM_TOO_LARGE;
   }
   *done = false;
@@ -138,7 +142,7 @@ dense_gemm_status layer_plan(int layout, int64_t M, int64_t N, int64_t K, const 
     narrow = (double)step * nk + 550;
   else
     narrow = (double)((tasks + slots - 1) / slots) * (79 * nk + 650);
-  if (narrow >= cost || tasks >= kMaxDim || (tasks > slots && nk > NARROW_STEPS)) return st;
+  if (narrow >= cost || (tasks > slots && nk > NARROW_STEPS)) return st;
   plan[0] = BM / 2;
   plan[1] = BN / 2;
   plan[3] = tiles_m;
@@ -220,15 +224,15 @@ dense_gemm_status tn_validate(int fmt, int64_t M, int64_t N, int64_t K, const vo
   const int64_t groups = g != nullptr ? g->count : 1;
   if (M == 0 || groups == 0) return DENSE_GEMM_OK;
   if (N == 0) return colsum != nullptr ? DENSE_GEMM_BAD_ARG : DENSE_GEMM_OK;
-  if (M >= kMaxDim || N >= kMaxDim || K >= kMaxDim) return DENSE_GEMM_TOO_LARGE;
-  // task numbers are 32-bit
+  if (M > kLayerMaxDim || N > kLayerMaxDim || K > kLayerMaxDim) return DENSE_GEMM_TOO_LARGE;
   int64_t tasks;
   const int64_t tile = BM / 2;  // the smaller
   if (__builtin_mul_overflow(((M + tile - 1) / tile) * ((N + tile - 1) / tile), groups, &tasks) ||
-      tasks >= kMaxDim)
+      tasks > kLayerMaxTiles)
     return DENSE_GEMM_TOO_LARGE;
-  // and so are the workgroups of 16 column sums each
-  if (colsum != nullptr && (__builtin_mul_overflow((M + 15) / 16, groups, &tasks) || tasks >= kMaxDim))
+  // and the blocks of 16 column sums each
+  if (colsum != nullptr &&
+      (__builtin_mul_overflow((M + 15) / 16, groups, &tasks) || tasks > kLayerMaxTiles))
     return DENSE_GEMM_TOO_LARGE;
   if (D == nullptr || (K > 0 && (A == nullptr || B == nullptr))) return DENSE_GEMM_NULL_PTR;
   if (ldd < N || (K > 0 && (lda < M || ldb < N))) return DENSE_GEMM_BAD_LD;

@@ -17,6 +17,15 @@ constexpr int64_t resident(int64_t tile_m, int64_t tile_n) {
   return tile_m == BM / 2 && tile_n == BN / 2 ? 2 : 1;
 }
 
+// The kernels count rows, columns, K and tasks in 32 bits and look a tile's
+// height, a few K steps or one round of workgroups past the end.
+constexpr int64_t kLayerMaxDim = kMaxDim - 1024;
+constexpr int64_t kLayerMaxTiles = kMaxDim - (1 << 20);
+// A tile of a group past those held in registers (groups.h) is found by
+// walking all ends, 64 at a time: bounded, so that no array of ends takes
+// longer than milliseconds to search.
+constexpr int64_t kLayerMaxGroups = 1 << 20;
+
 // A call of dense_gemm_layer with row groups.
 struct GroupedPlan {
   bool small;                // the small-output kernel

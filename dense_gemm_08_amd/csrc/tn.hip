@@ -2,8 +2,8 @@
 // A.T @ B and the column sums of A, for one matrix or one per group of rows
 // (dense_gemm_tn, include/dense_gemm.h).  Host side: the plan (tn_plan in
 // plan_layer.cpp), the launches and the C ABI entry points.  The kernel is
-// the tiled one with layout TA (gemm_kernel.h): A and B both have k as their
-// row, so their tiles are 64 k rows of 512 bytes and both operands' MFMA
+// the tiled one with layout TA (layer_kernel.h): A and B both have k as their
+// row, so their tiles are 64 k rows and both operands' MFMA
 // fragments come from transposing LDS reads.
 #include "column_sums.h"
 #include "layer_host.h"
@@ -33,8 +33,9 @@ static void enqueue_tile(const LayerParams& p, const ColumnSumsParams& sums, int
     r.sums_blocks = sums_blocks;
     enqueue_split_reduce<T, TILE, TILE>(r, cus, stream);
   } else if constexpr (SUMS) {
-    hipLaunchKernelGGL((column_sums<T, TILE>), dim3((unsigned)sums_blocks), dim3(CS_THREADS), 0,
-                       stream, sums);
+    const int64_t grid = sums_blocks < CS_MAX_GRID ? sums_blocks : CS_MAX_GRID;
+    hipLaunchKernelGGL((column_sums<T, TILE>), dim3((unsigned)grid), dim3(CS_THREADS), 0, stream, sums,
+                       (int)sums_blocks);
   }
 }
 

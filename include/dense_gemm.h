@@ -387,8 +387,10 @@ typedef struct dense_gemm_groups {
  * group holds (those from ends[count - 1] on) are neither read nor written.
  * count 0 does nothing.  The plan, and with it the order of the sums, may
  * differ from the plain product's; with groups it depends on M, N, K, the
- * count and the device alone, not on the ends.  Fewer than 2^31 output tiles are accepted
- * (DENSE_GEMM_TOO_LARGE), counting one more row of tiles per group. */
+ * count and the device alone, not on the ends.  DENSE_GEMM_TOO_LARGE: M, N or
+ * K above 2^31 - 1024, more than 2^20 groups, or more than 2^31 - 2^20 output
+ * tiles, counting one more row of tiles per group (those limits, the groups'
+ * aside, hold for dense_gemm_tn too). */
 dense_gemm_status dense_gemm_layer(int op, int64_t M, int64_t N, int64_t K, const void* A,
                                    int64_t lda, const void* B, int64_t ldb, void* D, int64_t ldd,
                                    const dense_gemm_epilogue* epilogue,
@@ -419,8 +421,8 @@ dense_gemm_status dense_gemm_tn(int fmt, int64_t M, int64_t N, int64_t K, const 
                                 size_t workspace_bytes, hipStream_t stream);
 
 /* Bytes of workspace dense_gemm_tn needs: repacked operands, FP32 partial
- * tiles where K is split, and with colsum (not 0) 2 KiB of partial column sums
- * per output tile and part.  `ends` is not read. */
+ * tiles where K is split, and with colsum (not 0) up to 2 KiB of partial
+ * column sums per output tile and part.  `ends` is not read. */
 dense_gemm_status dense_gemm_tn_workspace_size(int64_t M, int64_t N, int64_t K, const void* A,
                                                int64_t lda, const void* B, int64_t ldb, int colsum,
                                                const dense_gemm_groups* groups, int64_t num_cus,

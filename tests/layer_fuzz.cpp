@@ -14,7 +14,8 @@ static std::mt19937_64 rng(12345);
 
 static int64_t dim() {
   static const int64_t edge[] = {0, 1, 2, 7, 8, 15, 16, 17, 63, 64, 65, 127, 128, 129, 255, 256, 257,
-                                 4096, (1 << 16) + 1, (1 << 22) - 8, (1LL << 31) - 8, (1LL << 31) - 1,
+                                 4096, (1 << 16) + 1, (1 << 22) - 8, (1LL << 31) - 1024,
+                                 (1LL << 31) - 1023, 1 << 20, (1LL << 31) - 1,
                                  1LL << 31, INT64_MAX, -1};
   const uint64_t r = rng();
   if (r % 3 == 0) return edge[(r >> 8) % (sizeof(edge) / sizeof(edge[0]))];
@@ -98,7 +99,9 @@ int main() {
       const int64_t tasks = p.tiles_m * p.tiles_n * p.groups;
       REQUIRE(p.tile * p.tiles_m >= M && p.tile * p.tiles_n >= N);
       REQUIRE(p.full_tasks + p.split_tiles == tasks && p.splits >= 1);
-      REQUIRE(tasks < (1LL << 31) && p.full_tasks + p.splits * p.split_tiles < (1LL << 31));
+      REQUIRE(tasks <= kLayerMaxTiles);
+      // (a workgroup's next task is looked for one round past the last)
+      REQUIRE(p.full_tasks + p.splits * p.split_tiles + 2 * cus < (1LL << 31));
       REQUIRE(grouped || p.splits == 1 || p.splits * p.steps * BK >= K);
       REQUIRE(!grouped || p.splits == 1 || p.full_tasks == 0);
       const size_t all = (size_t)(p.full_tasks + p.splits * p.split_tiles);

@@ -404,6 +404,22 @@ def test_tn_grouped_full_check(case, dtype):
     assert torch.equal(dg.gemm_tn_grouped(A, B, e), D)
 
 
+def test_tn_grouped_column_sums_of_more_groups_than_a_launch_holds():
+    # 70001 blocks of column sums; row r is group 14 (r + 1) alone
+    rows, G, M, N = 5000, 70001, 8, 16
+    gen = generator(77)
+    A = torch.randint(-8, 9, (rows, M), generator=gen, device="cuda").bfloat16()
+    B = torch.randint(-8, 9, (rows, N), generator=gen, device="cuda").bfloat16()
+    ends = (torch.arange(G, device="cuda") // 14).to(torch.int32)
+    D, c = dg.gemm_tn_grouped(A, B, ends, colsum=True)
+    want = torch.zeros((G, M, N), dtype=torch.bfloat16, device="cuda")
+    want_c = torch.zeros((G, M), dtype=torch.bfloat16, device="cuda")
+    at = 14 * torch.arange(1, rows + 1, device="cuda")
+    want[at] = A[:, :, None] * B[:, None, :]
+    want_c[at] = A
+    assert torch.equal(D, want) and torch.equal(c, want_c)
+
+
 def test_tn_grouped_strides_and_untouched_padding():
     dt = torch.float16
     gen = generator(9)
@@ -617,6 +633,8 @@ def test_other_device_arguments_and_refusals():
         dg.gemm_nt_fused(A, B, residual=torch.zeros(8, dtype=dt, device="cuda").expand(4, 8))
     with pytest.raises(binding.DenseGemmError):
         dg.gemm_nt_dact(A, B, torch.zeros((4, 8), dtype=dt, device="cuda"), "none")
+    with pytest.raises(ValueError):  # fewer bytes than elements
+        dg.gemm_nt_fused(A, B, workspace=torch.zeros(1, dtype=torch.uint8, device="cuda").expand(1 << 20))
     e = torch.tensor([4, 4], dtype=torch.int32, device="cuda")
     B3 = torch.zeros((2, 8, 64), dtype=dt, device="cuda")
     with pytest.raises(TypeError):

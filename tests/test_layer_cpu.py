@@ -108,6 +108,17 @@ def test_group_refusals():
         assert call(groups=Gr(count=1 << 31)) == S.TOO_LARGE
         assert call(groups=Gr(stride=-8)) == S.BAD_ARG
         assert call(groups=Gr(count=1 << 20, stride=1 << 45)) == S.TOO_LARGE
+        # sizes and tile numbers stay this far from 2^31: the kernels look past
+        # the end in 32 bits
+        dims = dict(M=1, N=1, K=1, lda=1 << 20, ldb=1 << 20, ldd=1 << 20)
+        for d in "MNK":
+            big = dict(dims, **{d: (1 << 31) - 1023}, groups=Gr(count=1))
+            for ld in {"M": ["lda"] if call is tn else [], "N": ["ldb", "ldd"] if call is tn else ["ldd"],
+                       "K": [] if call is tn else ["lda", "ldb"]}[d]:
+                big[ld] = (1 << 31) - 1
+            assert call(**big) == S.TOO_LARGE
+    assert layer(groups=Gr(count=(1 << 20) + 1)) == S.TOO_LARGE
+    assert tn(M=1, N=1, groups=Gr(count=(1 << 31) - (1 << 20) + 1, stride=1)) == S.TOO_LARGE
     # output tiles past 32-bit numbers
     big = (1 << 31) - 8
     assert layer(M=big, N=1024, ldd=1024, groups=Gr(count=big)) == S.TOO_LARGE
@@ -205,7 +216,7 @@ def test_tn_workspace():
     assert tn_bytes(4096, 4352, 4096, colsum=1) == n + (256 + parts) * 2 * 256 * 4
     # sizes near the limits plan without overflow on any device
     for cus in (1, 256, 1 << 30):
-        tn_bytes((1 << 22) - 8, (1 << 22) - 8, (1 << 31) - 8, cus=cus)
+        tn_bytes((1 << 22) - 8, (1 << 22) - 8, (1 << 31) - 1024, cus=cus)
 
 
 def test_size_queries_refuse_bad_arguments():
