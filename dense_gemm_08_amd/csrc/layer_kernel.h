@@ -44,8 +44,11 @@ struct LayerParams {
   Epilogue e;
   Groups g;
   // SUMS: each task leaves its two wave columns' FP32 sums of its TM columns
-  // of A at colsum_ws + task * 2 TM (added up by column_sums.h)
+  // of A at colsum_ws + task * 2 TM (added up by column_sums.h); or, where
+  // colsum_ws is null, the first tile of each tile row writes its columns of
+  // colsum (M a group)
   float* colsum_ws;
+  uint16_t* colsum;
 };
 
 // Stages loaded ahead of the one in use.  Two, with rings of three slots for
@@ -394,14 +397,21 @@ __global__ __launch_bounds__(THREADS, (per_cu<SPLIT, TN, TM>())) void layer_gemm
     // row's 2 tiles_n (two to a tile), between the substeps, where both
     // substeps' fragments are at hand.  (One v_dot2c per fragment word in
     // every tile and step took 8 to 12% of 5120 x 8192 x 8192; a branch per
-    // step costs nothing measurable.)
+    // step costs nothing measurable.)  Short K: the first tile of the row
+    // takes all steps, its two wave columns by turns, and needs no second
+    // kernel.
     [[maybe_unused]] float cs[MI];
-    [[maybe_unused]] int sum_at = 0;
+    [[maybe_unused]] int sum_at = 0, sum_step = 2;
+    [[maybe_unused]] const bool direct = SUMS && p.colsum_ws == nullptr;
     if constexpr (SUMS) {
 #pragma unroll
       for (int i = 0; i < MI; ++i) cs[i] = 0.0f;
-      const int period = 2 * p.tiles_n;
-      sum_at = at.kbeg + (2 * at.tn + wn + period - at.kbeg % period) % period;
+      if (direct) {
+        sum_at = at.tn == 0 ? wn : at.kend;
+      } else {
+        sum_step = 2 * p.tiles_n;
+        sum_at = at.kbeg + (2 * at.tn + wn + sum_step - at.kbeg % sum_step) % sum_step;
+      }
     }
 
     // Stage 0 has landed; the loads of the stages after it, and the last
@@ -440,7 +450,7 @@ __global__ __launch_bounds__(THREADS, (per_cu<SPLIT, TN, TM>())) void layer_gemm
       }
       if constexpr (SUMS) {
         if (ks == sum_at) {
-          sum_at += 2 * p.tiles_n;
+          sum_at += sum_step;
 #pragma unroll
           for (int k = 0; k < 4; ++k)
 #pragma unroll
@@ -479,13 +489,31 @@ __global__ __launch_bounds__(THREADS, (per_cu<SPLIT, TN, TM>())) void layer_gemm
     if constexpr (SUMS) {
       // the four lane groups' sums of each column, added in a fixed order;
       // column_sums adds those of the tile row's wave columns
-      float* w = p.colsum_ws + ((size_t)at.task * 2 + wn) * TM + wm * WTM;
 #pragma unroll
       for (int i = 0; i < MI; ++i) {
-        float s = cs[i];
-        s += __shfl_xor(s, 16);
-        s += __shfl_xor(s, 32);
-        if (lq == 0) w[16 * i + l16] = s;
+        cs[i] += __shfl_xor(cs[i], 16);
+        cs[i] += __shfl_xor(cs[i], 32);
+      }
+      if (!direct) {
+        float* w = p.colsum_ws + ((size_t)at.task * 2 + wn) * TM + wm * WTM;
+#pragma unroll
+        for (int i = 0; i < MI; ++i)
+          if (lq == 0) w[16 * i + l16] = cs[i];
+      } else if (at.tn == 0) {
+        // the second wave column's sums to the first, through the place in
+        // LDS where that wave alone will stage its outputs
+        float* x = (float*)(smem + STAGE_AT + 2 * wm * (STAGING / WAVES));
+        if (wn == 1 && lq == 0)
+#pragma unroll
+          for (int i = 0; i < MI; ++i) x[16 * i + l16] = cs[i];
+        __syncthreads();
+        if (wn == 0 && lq == 0)
+#pragma unroll
+          for (int i = 0; i < MI; ++i) {
+            const int m = at.m0 + wm * WTM + 16 * i + l16;
+            if (m < at.M)
+              p.colsum[(int64_t)at.group * p.M + m] = (uint16_t)pack2<T>(cs[i] + x[16 * i + l16], 0.0f);
+          }
       }
     }
 

@@ -23,6 +23,15 @@ bool matrix_bytes(int64_t a, int64_t b, size_t* out) {
 // say (8192 x 5120 x 17408, 640 large tiles or 2560: 1078 against 1499 us).
 constexpr int64_t NARROW_STEPS = 16;
 
+// K steps of a 128 x 128 tile that has a CU to itself, in 0.01 us: past
+// LONG_RUN of them they cost `late`, not `step` (the operands then no longer
+// come from the caches: A @ B.T 1664 x 1984 x 12672 117 us against 97 in
+// parts of 256 x 256 tiles, x 8192 70 against 70).
+constexpr int64_t LONG_RUN = 96;
+int64_t narrow_steps(int64_t steps, int64_t step, int64_t late) {
+  return steps <= LONG_RUN ? step * steps : step * LONG_RUN + late * (steps - LONG_RUN);
+}
+
 int64_t round8(int64_t x) { return (x + 7) & ~(int64_t)7; }
 
 bool aligned16(const void* p) { return ((uintptr_t)p & 15) == 0; }
@@ -108,8 +117,8 @@ dense_gemm_status layer_validate(int op, int64_t M, int64_t N, int64_t K, const 
 //   * 256 x 128 and 128 x 256: one wave of 75 nk + 960, a split 600 and 1.5 a
 //     partial tile;
 //   * 128 x 128, two workgroups per CU: waves x (79 nk + 650); where each has
-//     a CU to itself 35 (A @ B.T) or 41 nk + 550, and split-K costs 600 and 1
-//     per partial tile.
+//     a CU to itself 35 (A @ B.T) or 41 nk (later steps 90) + 550, and split-K
+//     costs 600 and 1 per partial tile.
 // Measured, us, the plain product's plan against 128 x 128: A @ B.T 2048 x
 // 2048 x 2048 30 against 21, 777 x 1000 x 2048 29 against 19, 4096 x 2048 x
 // 1024 22 against 20, x 4096 56 against 57, 4096 x 4096 x 512 27 against 25;
@@ -137,9 +146,9 @@ dense_gemm_status layer_plan(int layout, int64_t M, int64_t N, int64_t K, const 
   if (tasks < cus) choose_split(tasks, nk, cus, step, 600, 1, BM / 16, &splits, &steps);
   double narrow;
   if (splits > 1)
-    narrow = (double)step * steps + 1150 + splits * tasks;
+    narrow = (double)narrow_steps(steps, step, 90) + 1150 + splits * tasks;
   else if (tasks <= cus)
-    narrow = (double)step * nk + 550;
+    narrow = (double)narrow_steps(nk, step, 90) + 550;
   else
     narrow = (double)((tasks + slots - 1) / slots) * (79 * nk + 650);
   if (narrow >= cost || (tasks > slots && nk > NARROW_STEPS)) return st;
@@ -170,7 +179,12 @@ dense_gemm_status grouped_plan(int layout, int64_t M, int64_t N, int64_t K, cons
   //   * 256 x 256 against 128 x 128 tiles: 16 groups of 1024 rows, N = K =
   //     4096, 413 against 571; of 256 rows 191 against 201; 32 of 512, N =
   //     2048, 287 against 341; but 64 of 128 rows, N = K = 2048, 182 against
-  //     161, and 16 of 128, N = K = 4096, 187 against 153.
+  //     161, and 16 of 128, N = K = 4096, 187 against 153.  Groups of more
+  //     than 192 rows take 128 x 128 tiles too where their estimated time
+  //     (that of layer_plan, half a tile of each group empty) is less: 4 of
+  //     512, N = 512, K = 2048, 49 against 22; 16 of 512, N = K = 2048, 106
+  //     against 80; of 2768, 328 against 392 (256 x 256 taken).  Over more
+  //     than one round up to 32 K steps alone, as above.
   //   * A @ B also has 128 x 256 tiles (B's rows in longer pieces): 16 groups
   //     of 128 rows, N = K = 4096, 133 against 150 in 128 x 128 tiles, where
   //     they are enough for the CUs; 4 of 250, N = K = 512, 13.7 against 12.8.
@@ -183,12 +197,18 @@ dense_gemm_status grouped_plan(int layout, int64_t M, int64_t N, int64_t K, cons
   const int64_t active = g.count < M ? g.count : M;
   const int64_t avg = (M + active - 1) / active;
   const int64_t tiles128 = most_row_tiles(M, g.count, BM / 2) * ((N + BN / 2 - 1) / (BN / 2));
+  const int64_t nk = (K + BK - 1) / BK, slots128 = cus * resident(BM / 2, BN / 2);
+  const int64_t est256 = (M + BM / 2 * active) / BM * ((N + BN - 1) / BN);
+  const int64_t est128 = (M + BM / 4 * active) / (BM / 2) * ((N + BN / 2 - 1) / (BN / 2));
+  const bool narrow = (est128 <= slots128 || nk <= 2 * NARROW_STEPS) &&
+                      (double)((est128 + slots128 - 1) / slots128) * (79 * nk + 650) <
+                          (double)((est256 + cus - 1) / cus) * (133 * nk + 1650);
   out->small = avg <= SMALL_TILE && tiles128 <= (layout == NT ? cus : cus / 4);
   if (out->small) {
     out->tile_m = out->tile_n = SMALL_TILE;
   } else if (avg > 192) {
-    out->tile_m = BM;
-    out->tile_n = BN;
+    out->tile_m = narrow ? BM / 2 : BM;
+    out->tile_n = narrow ? BN / 2 : BN;
   } else {
     out->tile_m = BM / 2;
     out->tile_n = layout == NN && (M + BM / 2 - 1) / (BM / 2) * ((N + BN - 1) / BN) >= cus ? BN : BN / 2;
@@ -256,14 +276,25 @@ dense_gemm_status tn_validate(int fmt, int64_t M, int64_t N, int64_t K, const vo
   return DENSE_GEMM_OK;
 }
 
+// Column sums: up to this many K steps the first tile of each tile row adds
+// its columns alone; beyond, the row's tiles share the steps and a second
+// kernel adds up theirs (layer_kernel.h).  Measured, us, alone against shared:
+// 1024 x 1024 x 333 8.5 and 14.9, 5120 x 8192 x 1024 87 and 90, x 8192 532 and
+// 530; 64 groups, 2048 x 2048 each, of 64 rows 136 and 150; 16 of 4096 rows,
+// 512 x 512, 67 and 64.  Groups may be several times as long as their average,
+// which is all that is known here, and the longest decide: they count four
+// times (16 unevenly filled groups of 1024 rows on average, 4096 x
+// 4096, 535 and 519).
+constexpr int64_t DIRECT_SUM_STEPS = 32;
+
 // One way to run D = A.T @ B, and its estimated time in 0.01 us, by a model
 // fitted to times on the MI355X (BF16):
 //   * 256 x 256 tiles, one workgroup per CU: waves x (133 per K step + 850);
 //     split-K as for the other products (choose_split: 105, 1200, 12; a split
 //     last wave costs 2500 on top of its steps);
 //   * 128 x 128 tiles, two per CU: waves x (90 per K step + 360), or 47 per
-//     step + 550 where each has a CU to itself; split-K only then (600 for
-//     the second kernel, 1 per partial tile).
+//     step (later ones 70) + 550 where each has a CU to itself; split-K only
+//     then (600 for the second kernel, 1 per partial tile).
 // Measured 256 against 128, us: 4096 x 4096 x 2048 64 against 69; 4096 x 2304
 // x 4096 93 against 111, 4096 x 2048 x 4096 93 against 64 (512 of the smaller
 // tiles: just one wave); 2048 x 2048 x 8192 in 4 parts 77 against 73; 512 x
@@ -294,7 +325,7 @@ static TnChoice tn_choice(int64_t M, int64_t N, int64_t nk, int64_t groups, bool
                (tasks < cus ? 12 * c.splits * last - 1300 : 0);
   } else if (tasks < cus) {
     choose_split(tasks, reach, cus, 47, 600, 1, BM / 16, &c.splits, &c.steps);
-    c.cost = 47 * ((nk + c.splits - 1) / c.splits) + 550 +
+    c.cost = narrow_steps((nk + c.splits - 1) / c.splits, 47, 70) + 550 +
              (c.splits > 1 ? 600 + c.splits * tasks : 0);
   } else {
     c.cost = (double)waves * (90 * nk + 360);
@@ -336,7 +367,7 @@ dense_gemm_status tn_plan(int64_t M, int64_t N, int64_t K, const void* A, int64_
     out->split_bytes =
         (size_t)(out->splits * out->split_tiles) * out->tile * out->tile * sizeof(float);
   }
-  if (colsum)
+  if (colsum && !(out->splits == 1 && (g != nullptr ? 4 * nk : nk) <= DIRECT_SUM_STEPS))
     out->sums_bytes = (size_t)(out->full_tasks + out->splits * out->split_tiles) * 2 * out->tile *
                       sizeof(float);
   return DENSE_GEMM_OK;

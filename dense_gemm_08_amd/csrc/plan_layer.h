@@ -48,7 +48,7 @@ struct TnPlan {
   bool a_direct, b_direct;
   size_t a_bytes, b_bytes;
   size_t split_bytes;        // FP32 partial tiles
-  size_t sums_bytes;         // the tasks' column sums of A
+  size_t sums_bytes;         // the tasks' column sums of A (0: the tiles write them whole)
   size_t total() const { return a_bytes + b_bytes + split_bytes + sums_bytes; }
 };
 

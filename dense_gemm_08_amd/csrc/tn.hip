@@ -32,7 +32,7 @@ static void enqueue_tile(const LayerParams& p, const ColumnSumsParams& sums, int
     r.sums = sums;
     r.sums_blocks = sums_blocks;
     enqueue_split_reduce<T, TILE, TILE>(r, cus, stream);
-  } else if constexpr (SUMS) {
+  } else if (SUMS && p.colsum_ws != nullptr) {
     const int64_t grid = sums_blocks < CS_MAX_GRID ? sums_blocks : CS_MAX_GRID;
     hipLaunchKernelGGL((column_sums<T, TILE>), dim3((unsigned)grid), dim3(CS_THREADS), 0, stream, sums,
                        (int)sums_blocks);
@@ -92,7 +92,8 @@ static dense_gemm_status run_tn(LayerCall c, void* colsum, const dense_gemm_grou
   p.split_steps = (int)tp.steps;
   p.num_tasks = (int)(tp.full_tasks + tp.split_tiles * tp.splits);
   if (tp.splits > 1) p.ws = (float*)at;
-  if (colsum != nullptr) p.colsum_ws = (float*)(at + tp.split_bytes);
+  if (tp.sums_bytes > 0) p.colsum_ws = (float*)(at + tp.split_bytes);
+  p.colsum = (uint16_t*)colsum;
   if (groups != nullptr)
     p.g = {(const int32_t*)groups->ends, (int)groups->count, (int)c.K, groups->stride};
   return tp.tile == BM ? enqueue_tn<T, BM>(p, (uint16_t*)colsum, (int)tp.groups, groups != nullptr,
