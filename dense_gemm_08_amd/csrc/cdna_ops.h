@@ -33,14 +33,13 @@ __device__ __forceinline__ int swz_k(int r) { return ((r >> 1) ^ (r << 2)) & 7; 
 // in a different 32-byte group of the 512-byte row, i.e. in distinct banks.
 __device__ __forceinline__ int swz_n(int k) { return ((k & 3) | (((k >> 3) & 3) << 2)) << 1; }
 
-// The same for a tile W columns wide.  W = 128: rows of 256 bytes (16
-// chunks), so two rows span the banks and the row's low bit already tells
-// their halves apart; the XOR of chunk bits 1-3 with r >> 1 and q separates
-// the eight rows of each half.
+// The same for a tile W columns wide: within the 16 chunks of a 256-byte row
+// too, a half-wave's eight rows (k & 3 and one bit of k >> 3) fall in distinct
+// 32-byte groups.
 template <int W>
 __device__ __forceinline__ int swz_rows(int k) {
   static_assert(W == 256 || W == 128, "tile widths");
-  return W == 256 ? swz_n(k) : (((k >> 1) & 1) | (((k >> 3) & 3) << 1)) << 1;
+  return swz_n(k) & (W / 8 - 1);
 }
 
 // 16 and 8 bytes at any 2-byte alignment: the hardware's unaligned access
