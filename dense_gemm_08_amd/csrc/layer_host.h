@@ -97,7 +97,7 @@ inline SmallLayerParams small_params(const LayerCall& c) {
   p.N = (int)c.N;
   p.K = (int)c.K;
   p.K8 = (int)((c.K + 7) & ~(int64_t)7);
-  p.N8 = (int)((c.N + 7) & ~(int64_t)7);
+  p.N8 = (int)((c.N + 1) & ~(int64_t)1);  // (columns of B that may be read: whole words)
   p.lda = (int)c.lda;
   p.ldb = (int)c.ldb;
   p.ldd = (int)c.ldd;

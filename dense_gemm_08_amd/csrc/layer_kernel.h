@@ -276,11 +276,12 @@ __global__ __launch_bounds__(THREADS, (per_cu<SPLIT, TN, TM>())) void layer_gemm
       const uint32_t bytes = (uint32_t)(span + at.K8 - k0) * 2u;
       h.r = make_rsrc(src + 2 * (int64_t)k0, live ? bytes : 0u);
     } else {
-      // rows k0 .. min(k0 + BK, K) - 1, columns m0 .. M or n0 .. N (rounded up to 8)
+      // rows k0 .. min(k0 + BK, K) - 1, columns m0 .. M or n0 .. N (rounded up
+      // to whole words: the range check is by word; an odd row is a padded copy)
       const int ld = half == 0 ? p.lda : p.ldb;
       const int cols = half == 0 ? at.M - at.m0 : p.N - at.n0;
       const int rows = min(BK, at.K - k0);
-      const uint32_t bytes = (uint32_t)((rows - 1) * ld + ((cols + 7) & ~7)) * 2u;
+      const uint32_t bytes = (uint32_t)((rows - 1) * ld + ((cols + 1) & ~1)) * 2u;
       const uint64_t src = half == 0 ? (uint64_t)(uintptr_t)(at.A + at.m0)
                                      : (uint64_t)(uintptr_t)(at.B + at.n0);
       h.r = make_rsrc(src + 2 * (int64_t)k0 * ld, live ? bytes : 0u);

@@ -34,7 +34,14 @@ int64_t narrow_steps(int64_t steps, int64_t step, int64_t late) {
 
 int64_t round8(int64_t x) { return (x + 7) & ~(int64_t)7; }
 
-bool aligned16(const void* p) { return ((uintptr_t)p & 15) == 0; }
+// Whether the 16-byte LDS-DMA loads read a matrix in place: they need 4-byte
+// addresses, and a range that ends between words (their range check is by
+// word).  So rows of an even number of elements, at even distances; and
+// `cols` that are K values, of both operands in the same 16-byte piece, a
+// multiple of 8.
+bool direct(const void* p, int64_t ld, int64_t stride, int64_t cols, bool k) {
+  return ((uintptr_t)p & 3) == 0 && ((ld | stride) & 1) == 0 && (cols & (k ? 7 : 1)) == 0;
+}
 
 // A matrix of the epilogue: its leading dimension and alignment.
 dense_gemm_status check_matrix(const void* p, int64_t ld, int64_t N) {
@@ -127,7 +134,17 @@ dense_gemm_status layer_validate(int op, int64_t M, int64_t N, int64_t K, const 
 dense_gemm_status layer_plan(int layout, int64_t M, int64_t N, int64_t K, const void* A,
                              int64_t lda, const void* B, int64_t ldb, int64_t cus, CallPlan* cp) {
   const dense_gemm_status st = plan_call(layout, M, N, K, A, lda, B, ldb, cus, nullptr, cp);
-  if (st != DENSE_GEMM_OK || cp->small()) return st;
+  if (st != DENSE_GEMM_OK) return st;
+  // (the plain product reads fewer operands in place)
+  if (direct(A, lda, 0, K, true)) {
+    cp->a_direct = true;
+    cp->a_bytes = 0;
+  }
+  if (direct(B, ldb, 0, layout == NT ? K : N, layout == NT)) {
+    cp->b_direct = true;
+    cp->b_bytes = 0;
+  }
+  if (cp->small()) return st;
   const int64_t nk = (K + BK - 1) / BK;
   int64_t* plan = cp->plan;
   const int64_t had = plan[3] * plan[4], parts = cp->split_tiles * plan[8];
@@ -217,9 +234,8 @@ dense_gemm_status grouped_plan(int layout, int64_t M, int64_t N, int64_t K, cons
   const int64_t most = most_row_tiles(M, g.count, out->tile_m) * out->tiles_n;
   const int64_t slots = cus * resident(out->tile_m, out->tile_n);
   out->grid = out->small || most < slots ? most : slots;
-  out->a_direct = K == 0 || (aligned16(A) && (lda & 7) == 0 && (K & 7) == 0);
-  out->b_direct = K == 0 || (aligned16(B) && (ldb & 7) == 0 && (g.stride & 7) == 0 &&
-                             ((layout == NT ? K : N) & 7) == 0);
+  out->a_direct = K == 0 || direct(A, lda, 0, K, true);
+  out->b_direct = K == 0 || direct(B, ldb, g.stride, layout == NT ? K : N, layout == NT);
   out->a_bytes = out->b_bytes = 0;
   if (!out->a_direct && !matrix_bytes(M, K8, &out->a_bytes)) return DENSE_GEMM_TOO_LARGE;
   if (!out->b_direct) {
@@ -357,8 +373,8 @@ dense_gemm_status tn_plan(int64_t M, int64_t N, int64_t K, const void* A, int64_
   const int64_t tasks = out->tiles_m * out->tiles_n * out->groups;
   out->full_tasks = best.splits == 1 ? tasks : tasks < cus ? 0 : tasks - tasks % cus;
   out->split_tiles = tasks - out->full_tasks;
-  out->a_direct = K == 0 || (aligned16(A) && (lda & 7) == 0 && (M & 7) == 0);
-  out->b_direct = K == 0 || (aligned16(B) && (ldb & 7) == 0 && (N & 7) == 0);
+  out->a_direct = K == 0 || direct(A, lda, 0, M, false);
+  out->b_direct = K == 0 || direct(B, ldb, 0, N, false);
   out->a_bytes = out->b_bytes = out->split_bytes = out->sums_bytes = 0;
   if (!out->a_direct && !matrix_bytes(K, round8(M), &out->a_bytes)) return DENSE_GEMM_TOO_LARGE;
   if (!out->b_direct && !matrix_bytes(K, round8(N), &out->b_bytes)) return DENSE_GEMM_TOO_LARGE;

@@ -97,6 +97,10 @@ STRIDED = [  # (M, N, K, pads of A, B, D, residual, Z; offsets of A, B)
     (70, 90, 100, 3, 5, 1, 7, 2, 0, 0), (300, 520, 264, 8, 16, 8, 24, 8, 0, 0),
     (300, 520, 264, 0, 0, 3, 0, 1, 1, 3), (16, 1000, 333, 0, 0, 0, 5, 0, 0, 1),
     (129, 300, 4097, 0, 1, 0, 0, 8, 5, 0),
+    # read in place at 4-byte alignment: leading dimensions, offsets, N (A @ B)
+    (70, 90, 104, 2, 4, 1, 7, 2, 0, 0), (300, 522, 264, 6, 2, 8, 24, 8, 2, 6),
+    (16, 1002, 336, 0, 0, 0, 5, 0, 2, 0), (129, 300, 4104, 2, 2, 0, 0, 8, 0, 4),
+    (600, 1030, 200, 10, 0, 0, 0, 0, 6, 2), (128, 122, 8192, 2, 0, 0, 0, 0, 0, 0),
 ]
 
 
@@ -238,7 +242,10 @@ def test_tn_full_check(M, N, K, dtype):
 @pytest.mark.parametrize("dtype", ["f16", "bf16"])
 @pytest.mark.parametrize("M,N,K,pa,pb,pd,oa,ob", [
     (100, 90, 300, 3, 0, 1, 0, 0), (264, 520, 500, 8, 16, 8, 0, 0), (264, 520, 500, 0, 0, 0, 1, 7),
-    (513, 40, 9000, 7, 24, 2, 0, 0)])
+    (513, 40, 9000, 7, 24, 2, 0, 0),
+    # read in place at 4-byte alignment
+    (100, 90, 300, 2, 0, 1, 0, 2), (266, 522, 500, 0, 4, 0, 6, 0), (130, 1030, 9000, 0, 0, 0, 0, 0),
+    (2050, 2058, 130, 2, 10, 0, 2, 4)])
 def test_tn_strides_offsets_and_untouched_padding(M, N, K, pa, pb, pd, oa, ob, dtype):
     dt = L.GEN[dtype]
     gen = generator(M + pa)
@@ -315,6 +322,7 @@ GROUPS = [  # (sizes, rows behind the last, N, K)
     ([0] * 400 + [5] + [0] * 100 + [300], 2, 264, 64),
     (spread(5, 77, 4), 0, 1001, 333),
     (spread(9, 2000, 5), 12, 301, 75),
+    (spread(9, 2000, 5), 12, 302, 72), (spread(7, 3000, 11), 5, 1030, 136), (spread(5, 60, 12), 0, 522, 264),
 ]
 IDS = ["G%d_rows%d_N%d_K%d" % (len(s), sum(s), n, k) for s, _, n, k in GROUPS]
 
@@ -361,7 +369,7 @@ def test_grouped_strides_and_shared_matrix(layout, dtype):
     M, G = sum(sizes), len(sizes)
     ends = ends_of(sizes)
     e = torch.tensor(ends, dtype=torch.int32, device="cuda")
-    for pa, pb, pd, off in ((0, 0, 0, 0), (8, 8, 8, 8), (3, 1, 5, 1)):
+    for pa, pb, pd, off in ((0, 0, 0, 0), (8, 8, 8, 8), (3, 1, 5, 1), (2, 6, 0, 2)):
         A = rand(gen, M, K, dt=dt, pad=pa)
         B = rand(gen, *((G, N, K) if layout == "nt" else (G, K, N)), dt=dt, sigma=K ** -0.5, pad=pb,
                  off=off)
@@ -382,6 +390,7 @@ TN_GROUPS = [
     ([1], 0, 8, 8), ([0, 3, 0], 2, 100, 72), ([64, 0, 65, 63, 1], 3, 264, 300),
     ([0, 0], 5, 40, 40), ([3000, 10, 0, 700], 8, 256, 256), (spread(40, 3001, 6), 64, 520, 77),
     (spread(300, 900, 7), 1, 48, 300), ([20000], 0, 300, 100), (spread(6, 6000, 8), 0, 1030, 1800),
+    (spread(20, 900, 13), 2, 298, 202),
 ]
 
 

@@ -177,7 +177,9 @@ def test_layer_workspace():
         assert layer_bytes(op, 4096, 4352, 4096) == binding.workspace_size(
             layout, fmt, 4096, 4352, 4096, 256, 4096, 256, 4096 if layout == "nt" else 4352,
             num_cus=256) > 0
-        # operands off 16 bytes, copied
+        # rows of whole words at 4 bytes are read in place
+        assert layer_bytes(op, 300, 304, 80, A=260, lda=82, B=268, ldb=306) == 0
+        # operands off 4 bytes, copied
         assert layer_bytes(op, 300, 304, 80, A=258) == up256(300 * 80 * 2)
         assert layer_bytes(op, 300, 304, 80, B=258) == up256(304 * 80 * 2)
 
@@ -190,7 +192,9 @@ def test_grouped_workspace_holds_the_repacked_operands():
     # a distance between the matrices off 8 elements: B alone
     assert layer_bytes(NT_BF16, 500, 64, 128, groups=Gr(count=7, stride=64 * 128 + 1)) == \
         up256(7 * 64 * 128 * 2)
-    # A @ B with N off 8: B alone
+    assert layer_bytes(NT_BF16, 500, 64, 128, groups=Gr(count=7, stride=64 * 128 + 2)) == 0
+    assert layer_bytes(NN_F16, 500, 66, 128, groups=Gr(count=7, stride=128 * 66)) == 0
+    # A @ B with an odd N: B alone
     assert layer_bytes(NN_F16, 500, 65, 128, groups=Gr(count=7, stride=128 * 65)) == \
         up256(7 * 128 * 72 * 2)
 
@@ -198,6 +202,7 @@ def test_grouped_workspace_holds_the_repacked_operands():
 def test_tn_workspace():
     assert tn_bytes(4096, 4096, 4096) == 0
     assert tn_bytes(4096, 4096, 4096, A=258) == 4096 * 4096 * 2
+    assert tn_bytes(4098, 4094, 64, A=260) == 0
     assert tn_bytes(4097, 4096, 64) == up256(64 * 4104 * 2)
     # few tiles, long K: 128 x 128 partial tiles, at most one per CU
     n = tn_bytes(256, 512, 65536)
