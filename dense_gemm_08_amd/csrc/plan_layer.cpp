@@ -34,13 +34,13 @@ int64_t narrow_steps(int64_t steps, int64_t step, int64_t late) {
 
 int64_t round8(int64_t x) { return (x + 7) & ~(int64_t)7; }
 
-// Whether the 16-byte LDS-DMA loads read a matrix in place: they need 4-byte
+// Whether the LDS-DMA loads read a matrix in place: they need 4-byte
 // addresses, and a range that ends between words (their range check is by
-// word).  So rows of an even number of elements, at even distances; and
-// `cols` that are K values, of both operands in the same 16-byte piece, a
-// multiple of 8.
-bool direct(const void* p, int64_t ld, int64_t stride, int64_t cols, bool k) {
-  return ((uintptr_t)p & 3) == 0 && ((ld | stride) & 1) == 0 && (cols & (k ? 7 : 1)) == 0;
+// word).  So rows of an even number of elements, at even distances.  Rows of
+// K values in the small-output kernel (small_k): a multiple of 8, as it reads
+// the last 16-byte piece whole.
+bool direct(const void* p, int64_t ld, int64_t stride, int64_t cols, bool small_k) {
+  return ((uintptr_t)p & 3) == 0 && ((ld | stride) & 1) == 0 && (cols & (small_k ? 7 : 1)) == 0;
 }
 
 // A matrix of the epilogue: its leading dimension and alignment.
@@ -136,11 +136,11 @@ dense_gemm_status layer_plan(int layout, int64_t M, int64_t N, int64_t K, const 
   const dense_gemm_status st = plan_call(layout, M, N, K, A, lda, B, ldb, cus, nullptr, cp);
   if (st != DENSE_GEMM_OK) return st;
   // (the plain product reads fewer operands in place)
-  if (direct(A, lda, 0, K, true)) {
+  if (direct(A, lda, 0, K, cp->small())) {
     cp->a_direct = true;
     cp->a_bytes = 0;
   }
-  if (direct(B, ldb, 0, layout == NT ? K : N, layout == NT)) {
+  if (direct(B, ldb, 0, layout == NT ? K : N, layout == NT && cp->small())) {
     cp->b_direct = true;
     cp->b_bytes = 0;
   }
@@ -234,8 +234,8 @@ dense_gemm_status grouped_plan(int layout, int64_t M, int64_t N, int64_t K, cons
   const int64_t most = most_row_tiles(M, g.count, out->tile_m) * out->tiles_n;
   const int64_t slots = cus * resident(out->tile_m, out->tile_n);
   out->grid = out->small || most < slots ? most : slots;
-  out->a_direct = K == 0 || direct(A, lda, 0, K, true);
-  out->b_direct = K == 0 || direct(B, ldb, g.stride, layout == NT ? K : N, layout == NT);
+  out->a_direct = K == 0 || direct(A, lda, 0, K, out->small);
+  out->b_direct = K == 0 || direct(B, ldb, g.stride, layout == NT ? K : N, layout == NT && out->small);
   out->a_bytes = out->b_bytes = 0;
   if (!out->a_direct && !matrix_bytes(M, K8, &out->a_bytes)) return DENSE_GEMM_TOO_LARGE;
   if (!out->b_direct) {

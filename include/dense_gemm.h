@@ -319,9 +319,11 @@ dense_gemm_status gemm_nt_e4m3_mx_ex(int64_t M, int64_t N, int64_t K, const void
  * take the caller's workspace, as dense_gemm_ex does (the queries give its
  * size, often 0; the same rules hold for it), and allocate nothing.  Layouts,
  * alignment, ownership, stream order, reproducibility and errors are those
- * stated at the top of this file: an operand that the 16-byte loads cannot
- * read in place is repacked into the workspace, every other matrix or vector
- * needs only the alignment of its elements.
+ * stated at the top of this file, except that an operand is read in place
+ * where its rows begin at 4-byte addresses and hold an even number of elements
+ * (for small outputs, rows of K values a multiple of 8) and repacked into the
+ * workspace otherwise.  Every other matrix or vector needs only the alignment
+ * of its elements.
  *
  * Activations, computed in FP32 (F is the standard normal distribution
  * function, s(w) = 1 / (1 + exp(-w))); at infinite z they and their

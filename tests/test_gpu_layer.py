@@ -101,6 +101,10 @@ STRIDED = [  # (M, N, K, pads of A, B, D, residual, Z; offsets of A, B)
     (70, 90, 104, 2, 4, 1, 7, 2, 0, 0), (300, 522, 264, 6, 2, 8, 24, 8, 2, 6),
     (16, 1002, 336, 0, 0, 0, 5, 0, 2, 0), (129, 300, 4104, 2, 2, 0, 0, 8, 0, 4),
     (600, 1030, 200, 10, 0, 0, 0, 0, 6, 2), (128, 122, 8192, 2, 0, 0, 0, 0, 0, 0),
+    # and rows of K values whose last 16 bytes are not whole
+    (300, 520, 2, 0, 0, 0, 0, 0, 0, 0), (300, 264, 62, 2, 4, 0, 0, 0, 2, 0), (600, 1030, 66, 0, 2, 0, 0, 0, 0, 2),
+    (520, 700, 4102, 0, 0, 0, 0, 0, 0, 0), (256, 384, 8206, 2, 2, 0, 0, 0, 4, 2), (1, 600, 1002, 0, 0, 0, 0, 0, 0, 0),
+    (2100, 2600, 1004, 0, 0, 0, 0, 0, 0, 0), (300, 520, 130, 2, 1, 0, 0, 0, 0, 0),
 ]
 
 
@@ -323,6 +327,7 @@ GROUPS = [  # (sizes, rows behind the last, N, K)
     (spread(5, 77, 4), 0, 1001, 333),
     (spread(9, 2000, 5), 12, 301, 75),
     (spread(9, 2000, 5), 12, 302, 72), (spread(7, 3000, 11), 5, 1030, 136), (spread(5, 60, 12), 0, 522, 264),
+    (spread(9, 2000, 5), 12, 302, 74), (spread(3, 4000, 14), 0, 1300, 1002), ([3, 0, 9], 1, 72, 66),
 ]
 IDS = ["G%d_rows%d_N%d_K%d" % (len(s), sum(s), n, k) for s, _, n, k in GROUPS]
 

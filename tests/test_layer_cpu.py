@@ -179,6 +179,10 @@ def test_layer_workspace():
             num_cus=256) > 0
         # rows of whole words at 4 bytes are read in place
         assert layer_bytes(op, 300, 304, 80, A=260, lda=82, B=268, ldb=306) == 0
+        assert layer_bytes(op, 300, 304, 82) == 0
+        # (by the small-output kernel with K a multiple of 8)
+        assert layer_bytes(op, 8, 304, 82) == up256(8 * 88 * 2) + (
+            up256(304 * 88 * 2) if op in (NT_F16, NT_BF16) else 0)
         # operands off 4 bytes, copied
         assert layer_bytes(op, 300, 304, 80, A=258) == up256(300 * 80 * 2)
         assert layer_bytes(op, 300, 304, 80, B=258) == up256(304 * 80 * 2)
