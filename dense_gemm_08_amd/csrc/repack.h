@@ -1,7 +1,6 @@
-// repack.h -- copies of operands that the kernels' 16-byte loads cannot read
-// in place (a pointer off 16-byte alignment, a leading dimension or row
-// length not a multiple of 8 elements) into dense, zero-padded matrices, on
-// the MI355X (gfx950).
+// repack.h -- copies of operands that the layer products' LDS-DMA loads cannot
+// read in place (plan_layer.cpp: direct; rows of an odd length or at an odd
+// distance, mostly) into dense, zero-padded matrices, on the MI355X (gfx950).
 #pragma once
 
 #include <hip/hip_runtime.h>
