@@ -204,7 +204,11 @@ dense_gemm_status grouped_plan(int layout, int64_t M, int64_t N, int64_t K, cons
   //     than one round up to 32 K steps alone, as above.
   //   * A @ B also has 128 x 256 tiles (B's rows in longer pieces): 16 groups
   //     of 128 rows, N = K = 4096, 133 against 150 in 128 x 128 tiles, where
-  //     they are enough for the CUs; 4 of 250, N = K = 512, 13.7 against 12.8.
+  //     they are enough for the CUs, or by estimate one round of them that
+  //     fills three quarters (8 unequal groups of 128, N = K = 4096, 64
+  //     against 73; 32 of 128, N = 1024, K = 2048, 41 against 46); but 16 of
+  //     64, N = K = 2048 (half the CUs), 38 against 30, 48 of 104, N = 1400, K
+  //     = 1000 (1.5 rounds), 62 against 50.
   //   * The small-output kernel splits K among its waves, which pays where
   //     128 x 128 tiles would leave CUs idle or with one workgroup: A @ B.T
   //     with 8 groups of 1 to 16 rows, N = K = 4096 (256 such tiles), 42 to
@@ -228,7 +232,10 @@ dense_gemm_status grouped_plan(int layout, int64_t M, int64_t N, int64_t K, cons
     out->tile_n = narrow ? BN / 2 : BN;
   } else {
     out->tile_m = BM / 2;
-    out->tile_n = layout == NN && (M + BM / 2 - 1) / (BM / 2) * ((N + BN - 1) / BN) >= cus ? BN : BN / 2;
+    const int64_t rows = (M + BM / 4 * active) / (BM / 2), cols = (N + BN - 1) / BN;
+    out->tile_n = layout == NN && ((M + BM / 2 - 1) / (BM / 2) * cols >= cus ||
+                                   (rows * cols <= cus && 4 * rows * cols >= 3 * cus))
+                      ? BN : BN / 2;
   }
   out->tiles_n = (N + out->tile_n - 1) / out->tile_n;
   const int64_t most = most_row_tiles(M, g.count, out->tile_m) * out->tiles_n;
