@@ -18,7 +18,11 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) void lds_void;
 
-constexpr uint32_t OOB = 0x80000000u;  // a buffer offset past every range
+// A buffer offset past every range.  A tile's rows span less than 2^31 bytes
+// (the argument checks), but the first K step's range begins up to a K step
+// before them (k = -koff), so ranges reach a little past 2^31.  (Offsets added
+// to this one, at most a row of the small-output kernels, stay below 2^32.)
+constexpr uint32_t OOB = 0xc0000000u;
 
 // LDS layouts.
 // K-contiguous tiles (A, and B for NT): row r holds 64 elements = eight

@@ -292,12 +292,13 @@ __global__ __launch_bounds__(THREADS) void gemm_mx_kernel(MxParams p) {
       const int k0 = ks * BKE - p.koff;
       const bool live = ks < kend;
       st.k0 = k0;
+      // (a first stage's range may pass 2^31: unsigned)
       st.base = lds0 + slot * SLOT;
       st.wbase = st.base + (8 * wave) * 1024;
       st.ra = make_rsrc((uint64_t)(uintptr_t)(p.A + (int64_t)m0 * p.lda) + k0,
-                        live ? (uint32_t)((vm - 1) * p.lda + p.K - k0) : 0u);
+                        live ? (uint32_t)((vm - 1) * p.lda + p.K) - (uint32_t)k0 : 0u);
       st.rb = make_rsrc((uint64_t)(uintptr_t)(p.B + (int64_t)n0 * p.ldb) + k0,
-                        live ? (uint32_t)((vn - 1) * p.ldb + p.K - k0) : 0u);
+                        live ? (uint32_t)((vn - 1) * p.ldb + p.K) - (uint32_t)k0 : 0u);
       // even waves load the A panel, odd waves the B panel (each panel is
       // written twice with the same bytes: every wave issues the same
       // instruction stream, with no branch to split the loop body)
