@@ -494,7 +494,7 @@ def _layer(layout, A, B, ends, bias, act, residual, preact, grad, D, stream, wor
         stride, ldb = _stack(B)
         groups = Groups(ends.data_ptr(), G[0], stride)
     epi = None
-    if code or bias is not None or residual is not None or preact is not None:
+    if grad or code or bias is not None or residual is not None or preact is not None:
         epi = Epilogue(act=code, grad=grad)
         if bias is not None:
             _check_like(bias, dtype, dev, 1 + len(G), "bias", G + (N,))
