@@ -78,8 +78,14 @@ dense_gemm_status layer_validate(int op, int64_t M, int64_t N, int64_t K, const 
                                  const dense_gemm_groups* g, bool* done) {
   *done = true;
   if (!valid_op(op)) return DENSE_GEMM_BAD_ARG;
-  dense_gemm_status st = dense_gemm_validate(op_layout(op), M, N, K, A, lda, B, ldb, D, ldd);
-  if (st != DENSE_GEMM_OK) return st;
+  if (M < 0 || N < 0 || K < 0) return DENSE_GEMM_INVALID_DIM;
+  dense_gemm_status st;
+  // (without groups there is nothing to do, and an empty stack of matrices
+  // has no pointer)
+  if (g == nullptr || g->count != 0) {
+    st = dense_gemm_validate(op_layout(op), M, N, K, A, lda, B, ldb, D, ldd);
+    if (st != DENSE_GEMM_OK) return st;
+  }
   if (e != nullptr) {
     if (e->act < DENSE_GEMM_ACT_NONE || e->act > DENSE_GEMM_ACT_SILU || (e->grad & ~1) != 0)
       return DENSE_GEMM_BAD_ARG;

@@ -1,6 +1,8 @@
 """The Python entry points of the layer products: what they hand to the C ABI,
 and what they refuse.  On the CPU the device checks and the launch are replaced
 (nothing runs); the GPU tests make the same calls in earnest."""
+import ctypes
+
 import pytest
 import torch
 
@@ -41,6 +43,44 @@ def test_gradient_calls_always_carry_their_form(handed):
             epi = args[-2]
             assert epi is not None and epi.grad == 1 and epi.act == binding.ACTS[act]
             assert bool(epi.preact) == (zz is not None)
+
+
+def test_no_groups_need_no_operands():
+    lib = binding.load_library()
+    none = binding.Groups(None, 0, 0)
+    size = ctypes.c_size_t(7)
+    for op in range(4):
+        for A, D in ((None, None), (256, 256)):
+            assert lib.dense_gemm_layer(op, 5, 6, 8, A, 8, None, 8, D, 6, None, none, None, 0, None) == S.OK
+        assert lib.dense_gemm_layer_workspace_size(op, 5, 6, 8, 256, 8, None, 8, none, 256,
+                                                   ctypes.byref(size)) == S.OK and size.value == 0
+        # what is wrong whatever the groups hold stays refused
+        assert lib.dense_gemm_layer(op, -5, 6, 8, None, 8, None, 8, None, 6, None, none, None, 0,
+                                    None) == S.INVALID_DIM
+        assert lib.dense_gemm_layer(op, 5, 6, 8, None, 8, None, 8, None, 6, binding.Epilogue(act=9), none,
+                                    None, 0, None) == S.BAD_ARG
+        assert lib.dense_gemm_layer(op, 5, 6, 8, None, 8, None, 8, None, 6, None,
+                                    binding.Groups(None, 0, -1), None, 0, None) == S.BAD_ARG
+        one = binding.Groups(256, 1, 0)
+        assert lib.dense_gemm_layer(op, 5, 6, 8, 256, 8, None, 8, 256, 6, None, one, None, 0,
+                                    None) == S.NULL_PTR
+    assert lib.dense_gemm_tn(1, 5, 6, 8, None, 5, None, 6, None, 6, None, none, None, 0, None) == S.OK
+
+
+@pytest.mark.gpu
+def test_empty_stacks_of_matrices():
+    A = torch.ones((5, 8), dtype=torch.bfloat16, device="cuda")
+    ends = torch.empty((0,), dtype=torch.int32, device="cuda")
+    D = torch.full((5, 6), 77.0, dtype=torch.bfloat16, device="cuda")
+    z = torch.ones_like(D)
+    nt, nn = A.new_empty((0, 6, 8)), A.new_empty((0, 8, 6))
+    dg.gemm_nt_grouped(A, nt, ends, bias=A.new_empty((0, 6)), act="gelu", residual=z, D=D)
+    dg.gemm_nn_grouped(A, nn, ends, D=D)
+    dg.gemm_nt_grouped_dact(A, nt, ends, z, "relu", D=D)
+    dg.gemm_nn_grouped_dact(A, nn, ends, z, "relu", D=D)
+    assert bool((D == 77.0).all())
+    W, c = dg.gemm_tn_grouped(A, z, ends, colsum=True)
+    assert W.shape == (0, 8, 6) and c.shape == (0, 8)
 
 
 @pytest.mark.gpu
