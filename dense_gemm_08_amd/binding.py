@@ -373,19 +373,19 @@ def gemm_nt_e4m3_mx(A, SA, B, SB, D=None, stream=None, workspace=None):
 # before the launch counts: they look each property up once, and enter a
 # device context only where the operands are not on the current device.
 
-_FMTS = {}   # torch dtype -> (name, dense_gemm_fmt); filled by _torch()
+_FMTS = None   # torch dtype -> (name, dense_gemm_fmt); set by _torch()
 _raw_stream = None
 
 
 def _torch():
-    global _raw_stream
+    global _FMTS, _raw_stream
     import torch
-    if not _FMTS:
+    if _FMTS is None:
         # (the current stream's handle without building a Stream object,
         # where this torch has it: 0.1 against 2 us)
         _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-        _FMTS[torch.bfloat16] = ("bf16", 1)
-        _FMTS[torch.float16] = ("f16", 0)
+        # (last, and whole: another thread's call may come in between)
+        _FMTS = {torch.bfloat16: ("bf16", 1), torch.float16: ("f16", 0)}
     return torch
 
 

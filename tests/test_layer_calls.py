@@ -2,6 +2,8 @@
 and what they refuse.  On the CPU the device checks and the launch are replaced
 (nothing runs); the GPU tests make the same calls in earnest."""
 import ctypes
+import importlib.util
+import sys
 
 import pytest
 import torch
@@ -20,6 +22,26 @@ def handed(monkeypatch):
     monkeypatch.setattr(binding, "_check_first", lambda A: (binding._FMTS[A.dtype], A.dtype, -1))
     monkeypatch.setattr(binding, "_launch", lambda name, args, *rest: calls.append((name, args)))
     return calls
+
+
+def test_first_calls_of_two_threads(monkeypatch):
+    # a second thread's call may come in wherever the first one looks at torch:
+    # the table of types is then whole, or still to be made
+    spec = importlib.util.spec_from_file_location("fresh_binding", binding.__file__)
+    fresh = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(fresh)
+    seen = []
+
+    class Watched:
+        def __getattr__(self, name):
+            seen.append(set(fresh._FMTS or ()))
+            return getattr(torch, name)
+
+    monkeypatch.setitem(sys.modules, "torch", Watched())
+    fresh._torch()
+    whole = {torch.float16, torch.bfloat16}
+    assert seen and all(types in (set(), whole) for types in seen)
+    assert set(fresh._FMTS) == whole
 
 
 def gradient_calls(device):
