@@ -20,9 +20,10 @@ dense_gemm_status run_grouped(LayerCall c, const dense_gemm_groups& groups, void
   }
   Groups g = {(const int32_t*)groups.ends, (int)groups.count, (int)c.M, groups.stride};
   const int64_t b_rows = LAYOUT == NT ? c.N : c.K;
-  repack_operands(c, gp.a_direct ? nullptr : ws, groups.count, b_rows, LAYOUT == NT ? c.K : c.N,
+  // (one matrix for all groups is copied once, and stays one)
+  repack_operands(c, gp.a_direct ? nullptr : ws, gp.matrices, b_rows, LAYOUT == NT ? c.K : c.N,
                   g.stride, gp.b_direct ? nullptr : (char*)ws + gp.a_bytes);
-  if (!gp.b_direct) g.stride = b_rows * c.ldb;
+  if (!gp.b_direct && gp.matrices > 1) g.stride = b_rows * c.ldb;
   const dim3 grid((unsigned)gp.grid);
   if (gp.small) {
     SmallLayerParams p = small_params(c);

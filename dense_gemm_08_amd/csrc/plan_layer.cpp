@@ -248,12 +248,13 @@ dense_gemm_status grouped_plan(int layout, int64_t M, int64_t N, int64_t K, cons
   const int64_t slots = cus * resident(out->tile_m, out->tile_n);
   out->grid = out->small || most < slots ? most : slots;
   out->a_direct = K == 0 || direct(A, lda, 0, K, out->small);
+  out->matrices = g.stride == 0 ? 1 : g.count;
   out->b_direct = K == 0 || direct(B, ldb, g.stride, layout == NT ? K : N, layout == NT && out->small);
   out->a_bytes = out->b_bytes = 0;
   if (!out->a_direct && !matrix_bytes(M, K8, &out->a_bytes)) return DENSE_GEMM_TOO_LARGE;
   if (!out->b_direct) {
     int64_t rows;
-    if (__builtin_mul_overflow(g.count, layout == NT ? N : K, &rows) ||
+    if (__builtin_mul_overflow(out->matrices, layout == NT ? N : K, &rows) ||
         !matrix_bytes(rows, layout == NT ? K8 : N8, &out->b_bytes))
       return DENSE_GEMM_TOO_LARGE;
   }

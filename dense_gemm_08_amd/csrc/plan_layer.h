@@ -33,6 +33,7 @@ struct GroupedPlan {
   int64_t tiles_n;
   int64_t grid;              // workgroups of the launch
   bool a_direct, b_direct;   // operands read in place (else repacked)
+  int64_t matrices;          // matrices B there are: the groups', or one for all
   size_t a_bytes, b_bytes;   // workspace of the repacked copies
   size_t total() const { return a_bytes + b_bytes; }
 };

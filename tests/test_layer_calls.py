@@ -116,3 +116,42 @@ def test_gradient_calls_without_an_activation_or_z_are_refused():
             assert e.value.status == status
         call(z, "silu")
     torch.cuda.synchronize()
+
+
+def grouped_bytes(op, M, N, K, count, stride):
+    size = ctypes.c_size_t()
+    ld = K if op in (0, 2) else N
+    assert binding.load_library().dense_gemm_layer_workspace_size(
+        op, M, N, K, 256, K, 256, ld, binding.Groups(256, count, stride), 256, ctypes.byref(size)) == S.OK
+    return size.value
+
+
+def test_a_matrix_that_all_groups_share_is_copied_once():
+    rounded = lambda n: (n + 255) // 256 * 256  # noqa: E731
+    for op, rows, cols in ((0, 64, 129), (2, 64, 129), (1, 130, 65), (3, 130, 65)):
+        N, K = (rows, cols) if op in (0, 2) else (cols, rows)
+        a = rounded(500 * 136 * 2) if K % 2 else 0
+        one = rows * ((cols + 7) // 8 * 8) * 2
+        assert grouped_bytes(op, 500, N, K, 7, 0) == a + rounded(one)
+        assert grouped_bytes(op, 500, N, K, 7, rows * cols) == a + rounded(7 * one)
+        assert grouped_bytes(op, 500, N, K, 1, rows * cols) == a + rounded(one)
+    # 64 groups of 4096 x 4097: 34 MB, not 2.1 GB
+    assert grouped_bytes(2, 512, 4096, 4097, 64, 0) == 4096 * 4104 * 2 + 512 * 4104 * 2
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("layout", ["nt", "nn"])
+@pytest.mark.parametrize("sizes", [[30, 0, 200, 5], [3, 0, 1, 2], [700, 900, 0, 800]])
+def test_a_shared_copied_matrix_gives_what_a_stack_of_it_gives(sizes, layout):
+    gen = torch.Generator(device="cuda").manual_seed(len(sizes) + sizes[0])
+    M, N, K, G = sum(sizes), 91, 105, len(sizes)
+    ends = torch.tensor(sizes, device="cuda").cumsum(0).to(torch.int32)
+    A = torch.randn((M, K), generator=gen, device="cuda").bfloat16()
+    W = torch.randn((N, K) if layout == "nt" else (K, N), generator=gen, device="cuda").bfloat16()
+    f = dg.gemm_nt_grouped if layout == "nt" else dg.gemm_nn_grouped
+    # (a workspace of the size asked for and no more, the bytes behind it kept)
+    need = grouped_bytes(2 if layout == "nt" else 1, M, N, K, G, 0)
+    ws = torch.full((need + 256,), 55, dtype=torch.uint8, device="cuda")
+    D = f(A, W.expand(G, *W.shape), ends, workspace=ws[:need])
+    assert torch.equal(D, f(A, torch.stack([W] * G), ends))
+    assert bool((ws[need:] == 55).all())
