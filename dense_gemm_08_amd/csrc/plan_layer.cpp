@@ -127,7 +127,7 @@ dense_gemm_status layer_validate(int op, int64_t M, int64_t N, int64_t K, const 
 // SILU in the epilogue, operands from HBM), nk K steps of 64:
 //   * 256 x 256 tiles: waves x (133 nk + 1650); a split (choose_split) costs
 //     800 and 4 per partial tile, a split last wave 1500;
-//   * 256 x 128 and 128 x 256: one wave of 75 nk + 960, a split 600 and 1.5 a
+//   * 256 x 128 and 128 x 256: waves x (75 nk + 960), a split 600 and 1.5 a
 //     partial tile;
 //   * 128 x 128, two workgroups per CU: waves x (79 nk + 650); where each has
 //     a CU to itself 35 (A @ B.T) or 41 nk (later steps 90) + 550, and split-K
@@ -137,6 +137,9 @@ dense_gemm_status layer_validate(int op, int64_t M, int64_t N, int64_t K, const 
 // 1024 22 against 20, x 4096 56 against 57, 4096 x 4096 x 512 27 against 25;
 // A @ B 2048 x 2048 x 2048 51 against 23, 4096 x 2048 x 4096 88 against 60,
 // 512 x 512 x 4096 29 against 18 (in 8 parts), 100 x 8000 x 3000 25 against 21.
+// One tile row or column over several waves: 128 x 200000 x 512 80 against 64
+// (A @ B 79 and 64), 128 x 70000 x 1024 53 and 47, 150000 x 64 x 256 41 and
+// 27; A @ B 128 x 128256 x 1024, two full waves either way, 63 and 65.
 dense_gemm_status layer_plan(int layout, int64_t M, int64_t N, int64_t K, const void* A,
                              int64_t lda, const void* B, int64_t ldb, int64_t cus, CallPlan* cp) {
   const dense_gemm_status st = plan_call(layout, M, N, K, A, lda, B, ldb, cus, nullptr, cp);
@@ -154,13 +157,16 @@ dense_gemm_status layer_plan(int layout, int64_t M, int64_t N, int64_t K, const 
   const int64_t nk = (K + BK - 1) / BK;
   int64_t* plan = cp->plan;
   const int64_t had = plan[3] * plan[4], parts = cp->split_tiles * plan[8];
-  double cost;
-  if (plan[0] == BM && plan[1] == BN) {
-    const int64_t waves = (had + cus - 1) / cus;
-    cost = (double)(plan[8] > 1 ? waves - 1 : waves) * (133 * nk + 1650);
-    if (plan[8] > 1) cost += 133 * plan[9] + 1650 + (had < cus ? 800 + 4.0 * parts : 1500);
-  } else {
-    cost = 75.0 * plan[9] + 960 + (plan[8] > 1 ? 600 + 1.5 * parts : 0);
+  const int64_t waves = (had + cus - 1) / cus;
+  const bool large = plan[0] == BM && plan[1] == BN;
+  const int64_t step0 = large ? 133 : 75, fixed0 = large ? 1650 : 960;
+  double cost = (double)(plan[8] > 1 ? waves - 1 : waves) * (step0 * nk + fixed0);
+  if (plan[8] > 1) {
+    cost += step0 * plan[9] + fixed0;
+    if (large)
+      cost += had < cus ? 800 + 4.0 * parts : 1500;
+    else
+      cost += 600 + 1.5 * parts;
   }
   const int64_t tiles_m = (M + BM / 2 - 1) / (BM / 2), tiles_n = (N + BN / 2 - 1) / (BN / 2);
   const int64_t tasks = tiles_m * tiles_n, slots = cus * resident(BM / 2, BN / 2);
