@@ -39,15 +39,20 @@ dense_gemm_status run_grouped(LayerCall c, const dense_gemm_groups& groups, void
   p.group_m = choose_group_m(kMaxDim);
   p.e = device_epilogue(c.e);
   p.g = g;
-  if (gp.tile_n == BN / 2)
+  if (gp.tile_n == BN / 2) {
     hipLaunchKernelGGL((layer_gemm_kernel<T, LAYOUT, false, BN / 2, BM / 2, true>), grid,
                        dim3(THREADS), 0, c.stream, p);
-  else if (gp.tile_m == BM / 2)
-    hipLaunchKernelGGL((layer_gemm_kernel<T, LAYOUT, false, BN, BM / 2, true>), grid, dim3(THREADS), 0,
-                       c.stream, p);
-  else
-    hipLaunchKernelGGL((layer_gemm_kernel<T, LAYOUT, false, BN, BM, true>), grid, dim3(THREADS), 0,
-                       c.stream, p);
+    return launched();
+  }
+  if constexpr (LAYOUT == NN) {
+    if (gp.tile_m == BM / 2) {
+      hipLaunchKernelGGL((layer_gemm_kernel<T, LAYOUT, false, BN, BM / 2, true>), grid, dim3(THREADS),
+                         0, c.stream, p);
+      return launched();
+    }
+  }
+  hipLaunchKernelGGL((layer_gemm_kernel<T, LAYOUT, false, BN, BM, true>), grid, dim3(THREADS), 0,
+                     c.stream, p);
   return launched();
 }
 

@@ -1,9 +1,12 @@
 """The plans of the layer products for 256 CUs, on the CPU."""
+import re
 import shutil
+import subprocess
 
 import pytest
 
-from tests import _plans
+from dense_gemm_08_amd import binding
+from tests import _layer_cases, _plans
 from tests._plans import NN, NT
 
 pytestmark = pytest.mark.skipif(shutil.which("g++") is None, reason="g++ not available")
@@ -26,3 +29,29 @@ def test_rounds_of_tiles_are_counted_for_outputs_of_one_tile_row_or_column():
     assert tile("layer", NT, 200000, 128, 512) == (128, 128)
     assert tile("layer", NT, 150000, 64, 256) == (128, 128)
     assert tile("layer", NT, 200000, 128, 4096) == (256, 128)
+
+
+def compiled():
+    """The instantiations of the layer kernels in the library, as _plans.kernels
+    names them (FP16's; the types share the templates)."""
+    names = subprocess.run(["nm", binding.library_path()], capture_output=True, text=True, check=True).stdout
+    out = set()
+    for name, args in re.findall(r"__device_stub__(layer_gemm_kernel|gemm_small|column_sums)I((?:DF16_|L[ib]\d+E)+)E",
+                                 names):
+        if args.startswith("DF16_"):
+            values = re.findall(r"L([ib])(\d+)E", args)
+            out.add((name,) + tuple(bool(int(v)) if t == "b" else int(v) for t, v in values))
+    return {k for k in out if k[0] != "gemm_small" or k[4]}  # (the layer's form)
+
+
+def reached():
+    ps = _plans.plans(_layer_cases.CALLS)
+    return [(k, _plans.traits(c, p)) for c, p in zip(_layer_cases.CALLS, ps) for k in _plans.kernels(c, p)]
+
+
+@pytest.mark.skipif(shutil.which("nm") is None, reason="nm not available")
+def test_every_compiled_kernel_is_reached_by_a_call():
+    have, met = compiled(), {k for k, _ in reached()}
+    assert len(have) > 40
+    assert not have - met, sorted(have - met)
+    assert not {k for k in met if k[0] in ("layer_gemm_kernel", "gemm_small", "column_sums")} - have
