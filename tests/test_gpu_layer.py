@@ -49,9 +49,9 @@ def generator(seed):
     return torch.Generator(device="cuda").manual_seed(seed)
 
 
-# sizes of the small-output kernel's tile shapes, of every tile of the tiled
-# kernel (128 and 256 rows, 128 and 256 columns), of split-K (a few tiles, long
-# K; a last partial wave) and of the edges between them
+# sizes of the small-output kernel's tile shapes, of whole 128 x 128 tiles and
+# their split-K (a few tiles, long K), and of the edges between them (the other
+# tiles: test_gpu_layer_kernels.py)
 FUSED = [
     (1, 8, 8), (1, 1, 1), (7, 40, 64), (1, 4096, 2048), (16, 520, 1000), (33, 256, 320),
     (64, 2048, 512), (128, 128, 4096), (128, 16384, 256), (130, 120, 2048), (100, 16000, 640),
@@ -225,7 +225,7 @@ def test_activations_at_special_values(M, dtype):
 
 # ---- D = A.T @ B ------------------------------------------------------------
 
-TN = [  # (M, N, K): tiles at and past their edges; split and last-wave split K
+TN = [  # (M, N, K): tiles at and past their edges; split K
     (1, 1, 1), (8, 8, 3), (22, 34, 200), (256, 256, 64), (257, 300, 65), (264, 520, 1000),
     (120, 1000, 20000), (512, 640, 5003), (1001, 77, 4096), (4096, 4352, 600), (1500, 700, 63),
 ]

@@ -55,3 +55,30 @@ def test_every_compiled_kernel_is_reached_by_a_call():
     assert len(have) > 40
     assert not have - met, sorted(have - met)
     assert not {k for k in met if k[0] in ("layer_gemm_kernel", "gemm_small", "column_sums")} - have
+
+
+def test_the_listed_calls_meet_the_second_tile_and_the_last_wave():
+    """Where a workgroup's second tile follows its first, and where whole tiles
+    and parts share a launch, each kernel that can come to it does."""
+    met = {}
+    for kernel, traits in reached():
+        met.setdefault(kernel, []).append(traits)
+    for kernel, seen in met.items():
+        if kernel[0] != "layer_gemm_kernel":
+            continue
+        _, layout, split, tn, tm, groups, sums = kernel
+        if not split:
+            assert any("more than one round" in t for t in seen), kernel
+        elif tn == tm == 256 and not groups:
+            assert any("last wave in parts" in t for t in seen), kernel
+            assert any("last wave in parts" not in t for t in seen), kernel
+        if sums:
+            assert any("partial column sums" in t for t in seen), kernel
+            if not (split and tm == 256):  # (a split 256 x 256 tile has a long K)
+                assert any("column sums in the first tiles" in t for t in seen), kernel
+    # the sums of whole tiles and of a last wave's parts, added up together
+    assert any({"last wave in parts", "partial column sums"} <= t for ts in met.values() for t in ts)
+    # the reduction with one-wave and with 256-thread workgroups, and each tile
+    reductions = {k[1:4] for k in met if k[0] == "split_reduce"}
+    assert {(128, 64, 128), (128, 256, 128), (128, 256, 256), (256, 256, 128), (256, 64, 256),
+            (256, 256, 256)} <= reductions
