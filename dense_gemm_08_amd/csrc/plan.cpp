@@ -164,6 +164,7 @@ bool small_output(int layout, int64_t M, int64_t N, int64_t K) {
   if ((layout != NT && layout != NN) || M > SMALL_MAX || K > SMALL_K_MAX) return false;
   const int64_t tiles_m = (M + SMALL_TILE - 1) / SMALL_TILE;
   const int64_t tiles = tiles_m * ((N + SMALL_TILE - 1) / SMALL_TILE);
+  if (tiles > SMALL_MOST_TILES) return false;
   if (layout == NT) {
     const int64_t t32 = ((M + 31) / 32) * ((N + 31) / 32);
     return M <= SMALL_TILE || tiles <= SMALL_MAX_TILES || t32 * K <= SMALL_T32_K;
@@ -393,7 +394,7 @@ dense_gemm_status plan_call(int layout, int64_t M, int64_t N, int64_t K, const v
 // 16 x 16 as before; more rows: measured 1.0-1.9x as fast).
 bool mx_small_output(int64_t M, int64_t N, int64_t K) {
   if (M > SMALL_MAX || K > mx::MX_SMALL_K_MAX) return false;
-  if (M <= SMALL_TILE) return true;
+  if (M <= SMALL_TILE) return (N + SMALL_TILE - 1) / SMALL_TILE <= SMALL_MOST_TILES;
   const int64_t t32 = ((M + 31) / 32) * ((N + 31) / 32);
   return t32 <= mx::MX_SMALL_T32 || (t32 <= mx::MX_SMALL_T32_MAX && t32 * K <= mx::MX_SMALL_T32_K);
 }

@@ -34,7 +34,8 @@ struct CallPlan {
 // tiled kernel: M at most SMALL_MAX, K at most SMALL_K_MAX, and one tile
 // row or at most SMALL_MAX_TILES 16 x 16 tiles, or for A @ B.T tiles of
 // 32 x 32 x K at most SMALL_T32_K; for A @ B also K at most SMALL_NN_K_MAX
-// and tile rows x N x K at most SMALL_NN_ELEMS.
+// and tile rows x N x K at most SMALL_NN_ELEMS; never more than
+// SMALL_MOST_TILES.
 bool small_output(int layout, int64_t M, int64_t N, int64_t K);
 // The small-output kernel's tile rows and columns for a product with M
 // rows and N columns on a device with num_cus CUs: 16 x 16 where M <= 16,
@@ -85,7 +86,8 @@ struct MxPlan {
 
 // The FP8 small-output kernel's products (M <= 128, K <= MX_SMALL_K_MAX,
 // and one 16-row tile row, or at most MX_SMALL_T32 tiles of 32 x 32, or at
-// most MX_SMALL_T32_MAX of them with tiles x K at most MX_SMALL_T32_K).
+// most MX_SMALL_T32_MAX of them with tiles x K at most MX_SMALL_T32_K; never
+// more than SMALL_MOST_TILES of 16 x 16).
 bool mx_small_output(int64_t M, int64_t N, int64_t K);
 // (Its tile: small_tile, as for FP16 A @ B.T.)
 // The plan of an FP8 call with M, N > 0 and K a multiple of 32 on a device

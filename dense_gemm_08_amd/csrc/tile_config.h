@@ -33,6 +33,10 @@ constexpr long long SMALL_T32_K = 1LL << 21;
 // elements its tiles stream, at most SMALL_NN_ELEMS (plan.cpp: small_output).
 constexpr int SMALL_NN_K_MAX = 4096;
 constexpr long long SMALL_NN_ELEMS = 21LL << 20;
+// A launch holds fewer than 2^32 threads (past that the runtime reports no
+// error and starts the remainder alone): more tiles than this, a row of D of
+// 134 million columns, go to the tiled kernels, whose grids follow the CUs.
+constexpr long long SMALL_MOST_TILES = 0xffffffffLL / SMALL_THREADS;
 
 // The FP8 block-scaled GEMM (gemm_mx_kernel.h): 256 x 256 tiles, 128-deep
 // K stages (128 bytes per row), one E8M0 scale per GROUP K values.  Its
