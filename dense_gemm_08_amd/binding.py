@@ -525,7 +525,7 @@ def gemm_nt_fused(A, B, bias=None, act="none", residual=None, preact=None, D=Non
     accumulation and one rounding; A is M x K, B is N x K, bias has N values,
     residual is M x N and may be D itself.  ``act``: "none", "relu", "gelu",
     "gelu_tanh" or "silu".  ``preact``: an M x N tensor that receives Z (for
-    :func:`gemm_nn_dact`).  ``workspace``: a device tensor (256-byte aligned,
+    :func:`gemm_nn_dact`); it must overlap no other.  ``workspace``: a device tensor (256-byte aligned,
     dense_gemm_layer_workspace_size bytes), or None to take one from torch's
     allocator where the call needs it.  The call is asynchronous on
     ``stream`` (None: the current stream)."""
@@ -557,8 +557,8 @@ def gemm_nt_grouped(A, B, ends, bias=None, act="none", residual=None, preact=Non
     layer): rows ends[g - 1] .. ends[g] - 1 of A (M x K) are multiplied with
     B[g] (G x N x K) and take bias[g] (G x N).  ``ends``: G int32 values on
     the device, not decreasing; the host never reads them.  Rows at or past
-    the last end are neither read nor written (with D None they hold
-    whatever the allocator returned)."""
+    the last end are not written (with D None they hold whatever the
+    allocator returned), and what the operands hold there changes nothing."""
     return _layer("nt", A, B, ends, bias, act, residual, preact, 0, D, stream, workspace)
 
 

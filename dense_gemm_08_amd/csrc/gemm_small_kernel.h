@@ -1,7 +1,8 @@
 // gemm_small_kernel.h -- the small-output kernel for the MI355X (gfx950):
 // D = A @ B.T or D = A @ B (FP16 or BF16) with M <= 128, such as a 128 x
 // 128 output, whose one 256 x 128 tile would leave almost every CU idle, a
-// single row of 16 x 16 tiles (M <= 16) of any width, or a few rows of
+// single row of 16 x 16 tiles (M <= 16) of any width that one launch's threads
+// cover (SMALL_MOST_TILES in tile_config.h), or a few rows of
 // A @ B.T tiles over a short enough K.  (Which products run it:
 // small_output in plan.cpp.)
 //

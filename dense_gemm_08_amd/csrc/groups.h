@@ -10,7 +10,9 @@
 // tile's group is then a compare and a ballot.  Every end is clamped to [0,
 // rows] and raised to the ends before it, so whatever the array holds, no row
 // outside [0, rows) is addressed, no row belongs to two groups, and the tiles
-// number no more than the host allowed for.
+// number no more than the host allowed for.  (A.T @ B, whose tiles' places the
+// host knows, reads a group's two ends alone, clamped but not raised: where
+// ends decrease, groups may share rows.)
 #pragma once
 
 #include <hip/hip_runtime.h>

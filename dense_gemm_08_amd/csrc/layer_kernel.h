@@ -12,7 +12,8 @@
 //   * 128 x 128 tiles, two workgroups to a CU, or one with deeper rings;
 //   * A.T @ B finds its next tile and starts that tile's first loads before
 //     it writes the last one's outputs, so that the loads' latency lies under
-//     the epilogue and the stores drain under the next tile's first step;
+//     the epilogue (the stores have until the barrier in the next tile's first
+//     step, whose counted wait includes them);
 //   * the epilogue works on FP32 values staged in LDS (epilogue.h);
 //   * row groups (groups.h): the tiles' places and K come from the device.
 #pragma once
@@ -211,6 +212,8 @@ __global__ __launch_bounds__(THREADS, (per_cu<SPLIT, TN, TM>())) void layer_gemm
     // A's steps in L2 (16 groups of 1024, N = K = 4096: 507 us, 527 with a
     // turn per tile).
     t.turn = 0;
+    // (K a multiple of 64 alone: the step that begins below k = 0 has to be the
+    // first, the only one whose loads are masked.)
     if constexpr (ROWS && LAYOUT == NT) {
       if (t.koff == 0 && t.nk > 0) t.turn = ((TM == BM ? 0 : t.tn * 5) + t.group * 3) % t.nk;
     }

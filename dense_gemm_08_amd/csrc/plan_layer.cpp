@@ -216,9 +216,11 @@ dense_gemm_status grouped_plan(int layout, int64_t M, int64_t N, int64_t K, cons
   //     than one round up to 32 K steps alone, as above.
   //   * A @ B also has 128 x 256 tiles (B's rows in longer pieces): 16 groups
   //     of 128 rows, N = K = 4096, 133 against 150 in 128 x 128 tiles, where
-  //     they are enough for the CUs, or by estimate one round of them that
-  //     fills three quarters (8 unequal groups of 128, N = K = 4096, 64
-  //     against 73; 32 of 128, N = 1024, K = 2048, 41 against 46); but 16 of
+  //     they are enough for the CUs, or by the count estimated as above one
+  //     round of them that fills three quarters: limits between the shapes
+  //     measured here, with no model of the time behind them, and groups
+  //     without rows count as ones with (8 unequal groups of 128, N = K =
+  //     4096, 64 against 73; 32 of 128, N = 1024, K = 2048, 41 against 46); but 16 of
   //     64, N = K = 2048 (half the CUs), 38 against 30, 48 of 104, N = 1400, K
   //     = 1000 (1.5 rounds), 62 against 50.
   //   * The small-output kernel splits K among its waves, which pays where

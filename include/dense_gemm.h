@@ -350,6 +350,7 @@ typedef enum dense_gemm_fmt { DENSE_GEMM_F16 = 0, DENSE_GEMM_BF16 = 1 } dense_ge
  *            (same pointer and leading dimension).
  * preact     Z, M x N with leading dimension ldz.  grad 0: receives Z rounded
  *            to the output type, or null; grad 1: read, and may be D itself.
+ *            A Z that is written must overlap nothing else.
  * act        a dense_gemm_act; grad 1 takes any but NONE, and no bias and no
  *            residual (DENSE_GEMM_BAD_ARG).
  * Z, the activation and the residual's sum are formed in FP32 from the
@@ -386,8 +387,9 @@ typedef struct dense_gemm_groups {
  *     D[i] = epilogue(A[i] @ Bhat_g),  i in group g
  * with B_g = B + g * groups->stride, N x K or K x N by op, leading dimension
  * ldb.  M is the number of rows of A, D, residual and preact; rows that no
- * group holds (those from ends[count - 1] on) are neither read nor written.
- * count 0 does nothing.  The plan, and with it the order of the sums, may
+ * group holds (those from ends[count - 1] on) are not written, and what A,
+ * residual and preact hold there changes nothing (a repacked A is copied
+ * whole).  count 0 does nothing, whatever the operands' pointers.  The plan, and with it the order of the sums, may
  * differ from the plain product's; with groups it depends on M, N, K, the
  * count and the device alone, not on the ends.  DENSE_GEMM_TOO_LARGE: M, N or
  * K above 2^31 - 1024, more than 2^20 groups, or more than 2^31 - 2^20 output
