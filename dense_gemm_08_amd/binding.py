@@ -525,10 +525,10 @@ def gemm_nt_fused(A, B, bias=None, act="none", residual=None, preact=None, D=Non
     accumulation and one rounding; A is M x K, B is N x K, bias has N values,
     residual is M x N and may be D itself.  ``act``: "none", "relu", "gelu",
     "gelu_tanh" or "silu".  ``preact``: an M x N tensor that receives Z (for
-    :func:`gemm_nn_dact`); it must overlap no other.  ``workspace``: a device tensor (256-byte aligned,
-    dense_gemm_layer_workspace_size bytes), or None to take one from torch's
-    allocator where the call needs it.  The call is asynchronous on
-    ``stream`` (None: the current stream)."""
+    :func:`gemm_nn_dact`); it must overlap no other.  ``workspace``: a device
+    tensor (256-byte aligned, dense_gemm_layer_workspace_size bytes), or None
+    to take one from torch's allocator where the call needs it.  The call is
+    asynchronous on ``stream`` (None: the current stream)."""
     return _layer("nt", A, B, None, bias, act, residual, preact, 0, D, stream, workspace)
 
 
