@@ -2,7 +2,9 @@
 FP8 block-scaled D = A.B^T (E4M3 with E8M0 scales per 32 K values), and the
 products of a transformer's dense and expert layers: bias, activation and
 residual in the epilogue, the input, weight and bias gradients, and a weight
-matrix per group of rows.
+matrix per group of rows; the same products in int8 with a scale per row of each
+operand; and what stands around an expert layer's products: routing, rows
+quantised, rows combined.
 
 The arithmetic runs in the hand-written HIP kernels of ``libdense_gemm.so``
 (built from ``csrc/``).  This package only marshals arguments to its C ABI;
@@ -27,6 +29,14 @@ from .binding import (  # noqa: F401
     gemm_nt_grouped_dact,
     gemm_nn_grouped_dact,
     gemm_tn_grouped,
+    gemm_nt_i8,
+    gemm_nt_i8_grouped,
+    quantize_rows,
+    Routes,
+    route,
+    route_grad,
+    combine_rows,
+    combine_rows_grad,
     library_path,
     load_library,
 )

@@ -11,6 +11,7 @@ from __future__ import annotations
 import ctypes
 import enum
 import os
+from typing import Any, NamedTuple
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIBNAME = "libdense_gemm.so"
@@ -60,6 +61,18 @@ class Groups(ctypes.Structure):
     _fields_ = [("ends", ctypes.c_void_p), ("count", ctypes.c_int64), ("stride", ctypes.c_int64)]
 
 
+# dense_gemm_score: how route() turns logits into scores
+SCORES = {"softmax": 0, "sigmoid": 1}
+
+
+class Routing(ctypes.Structure):
+    """dense_gemm_routing: the choice of experts (bias: E floats on the
+    device)."""
+    _fields_ = [("bias", ctypes.c_void_p), ("score", ctypes.c_int32), ("renorm", ctypes.c_int32),
+                ("scale", ctypes.c_float), ("groups", ctypes.c_int32),
+                ("top_groups", ctypes.c_int32), ("group_top", ctypes.c_int32)]
+
+
 class DenseGemmError(RuntimeError):
     def __init__(self, status: int, where: str):
         self.status = Status(status) if status in Status._value2member_map_ else status
@@ -106,6 +119,22 @@ SIGNATURES = {
     "dense_gemm_tn_workspace_size": ([_i64, _i64, _i64, _vp, _i64, _vp, _i64, _i32,
                                       ctypes.POINTER(Groups), _i64,
                                       ctypes.POINTER(ctypes.c_size_t)], _i32),
+    "dense_gemm_i8": ([_i32, _i64, _i64, _i64, _vp, _i64, _vp, _vp, _i64, _vp, _i64, _vp, _i64,
+                       ctypes.POINTER(Epilogue), ctypes.POINTER(Groups), _vp, ctypes.c_size_t, _vp],
+                      _i32),
+    "dense_gemm_i8_workspace_size": ([_i64, _i64, _i64, _vp, _i64, _vp, _i64,
+                                      ctypes.POINTER(Groups), _i64,
+                                      ctypes.POINTER(ctypes.c_size_t)], _i32),
+    "dense_gemm_quantize_i8": ([_i32, _i64, _i64, _vp, _i64, _i64, _vp, _vp, _i64, _vp, _vp], _i32),
+    "dense_gemm_route": ([_i32, _i64, _i64, _i64, _vp, _i64, ctypes.POINTER(Routing), _vp, _vp, _vp,
+                          _vp, _vp, _vp, ctypes.c_size_t, _vp], _i32),
+    "dense_gemm_route_workspace_size": ([_i64, _i64, _i64, ctypes.POINTER(ctypes.c_size_t)], _i32),
+    "dense_gemm_route_grad": ([_i32, _i64, _i64, _i64, _vp, _i64, ctypes.POINTER(Routing), _vp, _vp,
+                               _vp, _i64, _vp], _i32),
+    "dense_gemm_combine": ([_i32, _i64, _i64, _i64, _vp, _i64, _i64, _vp, _vp, _vp, _i64, _vp, _i64,
+                            _vp], _i32),
+    "dense_gemm_combine_grad": ([_i32, _i64, _i64, _i64, _vp, _i64, _vp, _i64, _i64, _vp, _vp, _vp,
+                                 _i64, _vp, _vp], _i32),
     "gemm_nt_e4m3_mx_ex": ([_i64, _i64, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp,
                             _i64, _vp, ctypes.c_size_t, _vp], _i32),
 }
@@ -639,3 +668,336 @@ def gemm_tn_grouped(A, B, ends, D=None, colsum=None, stream=None, workspace=None
     :func:`gemm_nt_grouped`): D is G x M x N and colsum G x M, each group's
     sums over its own rows, zero for an empty group."""
     return _tn(A, B, ends, D, colsum, stream, workspace)
+
+
+# ---- int8 products, and the operators around an expert layer's products ------
+
+def _check_scales(t, dev: int, shape, what: str):
+    """FP32 scales on device number ``dev``, contiguous in their last
+    dimension."""
+    if t.dtype is not _torch().float32:
+        raise TypeError("%s must be float32, got %s" % (what, t.dtype))
+    if t.get_device() != dev:
+        raise ValueError("operands on different devices: %s on %s" % (what, t.device))
+    if t.shape != shape or (t.shape[-1] > 1 and t.stride(-1) != 1):
+        raise ValueError("%s must have shape %s with unit stride in its last dimension, got %s"
+                         % (what, tuple(shape), tuple(t.shape)))
+
+
+def _i8(A, SA, B, SB, ends, bias, act, residual, preact, D, dtype, stream, workspace):
+    if _lib is None:
+        load_library()
+    torch = _torch()
+    int8 = torch.int8
+    if A.dtype is not int8:
+        raise TypeError("A must be int8, got %s" % A.dtype)
+    if not A.is_cuda:
+        raise ValueError("A must be a device tensor")
+    if A.dim() != 2 or (A.stride(1) != 1 and A.shape[1] > 1):
+        raise ValueError("A must be 2-D with unit column stride")
+    dev = A.get_device()
+    code = ACTS.get(act)
+    if code is None:
+        raise ValueError("act must be one of %s, got %r" % (", ".join(ACTS), act))
+    M, K = A.shape
+    _check_like(B, int8, dev, 2 if ends is None else 3, "B")
+    N = B.shape[-2]
+    if B.shape[-1] != K:
+        raise ValueError("inner dimensions differ: A is %s, B is %s"
+                         % (tuple(A.shape), tuple(B.shape)))
+    if D is not None:
+        dtype = D.dtype
+    elif dtype is None:
+        dtype = torch.bfloat16
+    fmt = _FMTS.get(dtype)
+    if fmt is None:
+        raise TypeError("D must be float16 or bfloat16, got %s" % dtype)
+    groups, G, sb_stride = None, (), 0
+    if ends is None:
+        ldb = _ld(B)
+    else:
+        _check_ends(ends, dev, torch)
+        G = (B.shape[0],)
+        if ends.shape[0] != G[0]:
+            raise ValueError("%d group ends for %d matrices B" % (ends.shape[0], G[0]))
+        stride, ldb = _stack(B)
+        groups = Groups(ends.data_ptr(), G[0], stride)
+        if G[0] > 1 and SB.dim() == 2:
+            sb_stride = SB.stride(0)
+    _check_scales(SA, dev, (M,), "SA")
+    _check_scales(SB, dev, G + (N,), "SB")
+    epi = None
+    if code or bias is not None or residual is not None or preact is not None:
+        epi = Epilogue(act=code)
+        if bias is not None:
+            _check_like(bias, dtype, dev, 1 + len(G), "bias", G + (N,))
+            epi.bias = bias.data_ptr()
+            if G and G[0] > 1:
+                epi.bias_stride = bias.stride(0)
+        if residual is not None:
+            _check_like(residual, dtype, dev, 2, "residual", (M, N))
+            epi.residual, epi.ldr = residual.data_ptr(), _ld(residual)
+        if preact is not None:
+            _check_like(preact, dtype, dev, 2, "preact", (M, N))
+            epi.preact, epi.ldz = preact.data_ptr(), _ld(preact)
+    if D is None:
+        D = torch.empty((M, N), dtype=dtype, device=A.device)
+        if stream is not None:
+            _used_by(D, stream, A.device)
+    else:
+        _check_like(D, dtype, dev, 2, "D", (M, N))
+    a, lda, b = A.data_ptr(), _ld(A), B.data_ptr()
+    _launch("dense_gemm_i8",
+            (fmt[1], M, N, K, a, lda, SA.data_ptr(), b, ldb, SB.data_ptr(), sb_stride, D.data_ptr(),
+             _ld(D), epi, groups),
+            ("dense_gemm_i8_workspace_size", M, N, K, a, lda, b, ldb, groups, 0), workspace, stream,
+            dev, torch)
+    return D
+
+
+def gemm_nt_i8(A, SA, B, SB, bias=None, act="none", residual=None, preact=None, D=None, dtype=None,
+               stream=None, workspace=None):
+    """D = act(Z) + residual with Z = (A @ B.T) * SA[:, None] * SB + bias: A
+    (M x K) and B (N x K) int8, SA (M) and SB (N) float32, the product exact in
+    32-bit integers, the rest in FP32 with one rounding.  D, bias, residual and
+    preact are float16 or bfloat16 (``dtype``, or D's; bfloat16 by default).
+    K at most 131071.  Other arguments as for :func:`gemm_nt_fused`
+    (``workspace``: dense_gemm_i8_workspace_size bytes)."""
+    return _i8(A, SA, B, SB, None, bias, act, residual, preact, D, dtype, stream, workspace)
+
+
+def gemm_nt_i8_grouped(A, SA, B, SB, ends, bias=None, act="none", residual=None, preact=None, D=None,
+                       dtype=None, stream=None, workspace=None):
+    """:func:`gemm_nt_i8` for rows sorted into G groups: B is G x N x K, SB and
+    bias G x N, ``ends`` as for :func:`gemm_nt_grouped`."""
+    return _i8(A, SA, B, SB, ends, bias, act, residual, preact, D, dtype, stream, workspace)
+
+
+def _call_rows(name, args, stream, dev, torch):
+    """Calls ``name(*args, stream)``, which takes no workspace, on device number
+    ``dev``."""
+    if torch.cuda.current_device() != dev:
+        with torch.cuda.device(dev):
+            return _call_rows(name, args, stream, dev, torch)
+    if stream is None and _raw_stream is not None:
+        sh = _raw_stream(dev)
+    else:
+        sh = _stream_handle(stream, dev)
+    st = getattr(_lib, name)(*args, sh)
+    if st != 0:
+        raise DenseGemmError(st, name)
+
+
+def _check_dense(t, dtype, dev: int, shape, what: str):
+    """A contiguous tensor of this type and shape on device number ``dev``."""
+    if t.dtype is not dtype:
+        raise TypeError("%s must be %s, got %s" % (what, dtype, t.dtype))
+    if t.get_device() != dev:
+        raise ValueError("operands on different devices: %s on %s, not cuda:%d" % (what, t.device, dev))
+    if t.shape != shape or not t.is_contiguous():
+        raise ValueError("%s must be contiguous with shape %s, got %s"
+                         % (what, tuple(shape), tuple(t.shape)))
+
+
+def _new(shape, dtype, like, stream, torch):
+    t = torch.empty(shape, dtype=dtype, device=like.device)
+    if stream is not None:
+        _used_by(t, stream, like.device)
+    return t
+
+
+def quantize_rows(X, rows=None, Q=None, S=None, stream=None):
+    """(Q, S): the rows of X (float16 or bfloat16) as int8 with a float32 scale
+    each, X[i] ~ Q[i] * S[i], as :func:`gemm_nt_i8` takes them: S is the row's
+    largest absolute value / 127 and Q the nearest whole numbers (half-way cases
+    to even).  ``rows``: int32 indices on the device, one for each row of Q, of
+    the rows of X that they are made of (:func:`route`'s ``tokens``); an index
+    outside X gives zeros with scale 0.  A row that holds an infinity or NaN gets
+    the scale NaN.  Weights: a row per output channel."""
+    if _lib is None:
+        load_library()
+    torch = _torch()
+    fmt, _, dev = _check_first(X)
+    T, K = X.shape
+    R = T
+    if rows is not None:
+        if rows.dim() != 1:
+            raise ValueError("rows must be 1-D")
+        R = rows.shape[0]
+        _check_dense(rows, torch.int32, dev, (R,), "rows")
+    if Q is None:
+        Q = _new((R, K), torch.int8, X, stream, torch)
+    else:
+        _check_like(Q, torch.int8, dev, 2, "Q", (R, K))
+    if S is None:
+        S = _new((R,), torch.float32, X, stream, torch)
+    else:
+        _check_dense(S, torch.float32, dev, (R,), "S")
+    _call_rows("dense_gemm_quantize_i8",
+               (fmt[1], R, K, X.data_ptr(), _ld(X), T, None if rows is None else rows.data_ptr(),
+                Q.data_ptr(), _ld(Q), S.data_ptr()), stream, dev, torch)
+    return Q, S
+
+
+class Routes(NamedTuple):
+    """What :func:`route` returns, on the device: ``weights`` (T x k float32),
+    ``experts`` and ``places`` (T x k int32), ``ends`` (E int32) and ``tokens``
+    (T k int32)."""
+    weights: Any
+    experts: Any
+    places: Any
+    ends: Any
+    tokens: Any
+
+
+def _check_logits(logits, torch):
+    if logits.dtype is torch.float32:
+        fmt = 2
+    else:
+        known = _FMTS.get(logits.dtype)
+        if known is None:
+            raise TypeError("logits must be float32, float16 or bfloat16, got %s" % logits.dtype)
+        fmt = known[1]
+    if not logits.is_cuda:
+        raise ValueError("logits must be a device tensor")
+    if logits.dim() != 2 or (logits.stride(1) != 1 and logits.shape[1] > 1):
+        raise ValueError("logits must be 2-D with unit column stride")
+    return fmt, logits.get_device()
+
+
+def _score(score):
+    code = SCORES.get(score)
+    if code is None:
+        raise ValueError("score must be one of %s, got %r" % (", ".join(SCORES), score))
+    return code
+
+
+def route(logits, k, score="softmax", bias=None, groups=1, top_groups=1, group_top=1, renorm=True,
+          scale=1.0, stream=None, workspace=None):
+    """The k experts of each token from its router logits (T x E, float32,
+    float16 or bfloat16), their weights, and the order of the rows by expert, as
+    a :class:`Routes`:
+
+    * scores s: ``"softmax"`` over the experts, or ``"sigmoid"`` of each;
+    * choice: the k experts of the largest s + bias (``bias``: E float32, it
+      decides the choice alone), ties to the lowest index.  With ``groups`` > 1
+      the experts lie in that many equal runs, and only those of the
+      ``top_groups`` runs of the largest values can be chosen, a run's value
+      being the sum of its ``group_top`` (1 or 2) best;
+    * ``weights``: s of the chosen, with ``renorm`` divided by their sum, times
+      ``scale``; in descending order of the choice;
+    * ``ends``: the experts' row ends for :func:`gemm_nt_grouped` and the like;
+    * ``tokens``: the token of every row in that order (-1 behind the last end),
+      for :func:`quantize_rows`;
+    * ``places``: the row of every choice, for :func:`combine_rows`.
+
+    An expert whose logit is -inf is never chosen; a choice that a token does not
+    have (all logits -inf: none) has expert -1, weight 0, place -1.  A token with
+    a logit that is NaN or +inf has no experts and weights of NaN.  k <= 64,
+    E <= 1024.  ``workspace``: dense_gemm_route_workspace_size bytes, or None to
+    take one from torch's allocator where the call needs it."""
+    if _lib is None:
+        load_library()
+    torch = _torch()
+    fmt, dev = _check_logits(logits, torch)
+    T, E = logits.shape
+    r = Routing(None, _score(score), bool(renorm), scale, groups, top_groups, group_top)
+    if bias is not None:
+        _check_dense(bias, torch.float32, dev, (E,), "bias")
+        r.bias = bias.data_ptr()
+    weights = _new((T, k), torch.float32, logits, stream, torch)
+    experts = _new((T, k), torch.int32, logits, stream, torch)
+    places = _new((T, k), torch.int32, logits, stream, torch)
+    ends = _new((E,), torch.int32, logits, stream, torch)
+    tokens = _new((T * k,), torch.int32, logits, stream, torch)
+    _launch("dense_gemm_route",
+            (fmt, T, E, k, logits.data_ptr(), _ld(logits), r, weights.data_ptr(), experts.data_ptr(),
+             places.data_ptr(), ends.data_ptr(), tokens.data_ptr()),
+            ("dense_gemm_route_workspace_size", T, E, k), workspace, stream, dev, torch)
+    return Routes(weights, experts, places, ends, tokens)
+
+
+def route_grad(logits, experts, dweights, score="softmax", renorm=True, scale=1.0, D=None, stream=None):
+    """The gradient of the logits (T x E, like them) from that of the weights
+    (``dweights``: T x k float32) for the ``experts`` that :func:`route` chose
+    with the same ``score``, ``renorm`` and ``scale``.  The choice and its bias
+    have no gradient; choices of -1 take no part."""
+    if _lib is None:
+        load_library()
+    torch = _torch()
+    fmt, dev = _check_logits(logits, torch)
+    T, E = logits.shape
+    if experts.dim() != 2:
+        raise ValueError("experts must be 2-D")
+    k = experts.shape[1]
+    _check_dense(experts, torch.int32, dev, (T, k), "experts")
+    _check_dense(dweights, torch.float32, dev, (T, k), "dweights")
+    if D is None:
+        D = _new((T, E), logits.dtype, logits, stream, torch)
+    else:
+        _check_like(D, logits.dtype, dev, 2, "D", (T, E))
+    r = Routing(None, _score(score), bool(renorm), scale, 1, 1, 1)
+    _call_rows("dense_gemm_route_grad",
+               (fmt, T, E, k, logits.data_ptr(), _ld(logits), r, experts.data_ptr(),
+                dweights.data_ptr(), D.data_ptr(), _ld(D)), stream, dev, torch)
+    return D
+
+
+def _check_choices(places, weights, dev, torch):
+    if places.dim() != 2:
+        raise ValueError("places must be 2-D")
+    _check_dense(places, torch.int32, dev, places.shape, "places")
+    if weights is not None:
+        _check_dense(weights, torch.float32, dev, places.shape, "weights")
+    return places.shape
+
+
+def combine_rows(H, places, weights=None, residual=None, D=None, stream=None):
+    """D[t] = sum_j weights[t, j] * H[places[t, j]] + residual[t], FP16 or BF16
+    with FP32 sums and one rounding: the experts' rows back to their tokens, by
+    the ``places`` (T x k int32) and ``weights`` (T x k float32; None: ones, as
+    for the gradient of rows gathered by ``tokens``) of :func:`route`.  A place
+    outside H adds its weight times zero.  ``residual`` may be D itself."""
+    if _lib is None:
+        load_library()
+    torch = _torch()
+    fmt, dtype, dev = _check_first(H)
+    R, N = H.shape
+    T, k = _check_choices(places, weights, dev, torch)
+    if residual is not None:
+        _check_like(residual, dtype, dev, 2, "residual", (T, N))
+    if D is None:
+        D = _new((T, N), dtype, H, stream, torch)
+    else:
+        _check_like(D, dtype, dev, 2, "D", (T, N))
+    _call_rows("dense_gemm_combine",
+               (fmt[1], T, N, k, H.data_ptr(), _ld(H), R, places.data_ptr(),
+                None if weights is None else weights.data_ptr(),
+                None if residual is None else residual.data_ptr(),
+                0 if residual is None else _ld(residual), D.data_ptr(), _ld(D)), stream, dev, torch)
+    return D
+
+
+def combine_rows_grad(dY, H, places, weights=None, dh=None, stream=None):
+    """(dh, dweights), the gradients of :func:`combine_rows`: dh[places[t, j]] =
+    weights[t, j] * dY[t] and dweights[t, j] = dY[t] . H[places[t, j]] (T x k
+    float32).  Rows of dh (like H) that no place names are not written: with dh
+    None they hold whatever the allocator returned.  A place outside H writes no
+    row and a dweights of 0."""
+    if _lib is None:
+        load_library()
+    torch = _torch()
+    fmt, dtype, dev = _check_first(H)
+    R, N = H.shape
+    T, k = _check_choices(places, weights, dev, torch)
+    _check_like(dY, dtype, dev, 2, "dY", (T, N))
+    if dh is None:
+        dh = _new((R, N), dtype, H, stream, torch)
+    else:
+        _check_like(dh, dtype, dev, 2, "dh", (R, N))
+    dweights = _new((T, k), torch.float32, H, stream, torch)
+    _call_rows("dense_gemm_combine_grad",
+               (fmt[1], T, N, k, dY.data_ptr(), _ld(dY), H.data_ptr(), _ld(H), R, places.data_ptr(),
+                None if weights is None else weights.data_ptr(), dh.data_ptr(), _ld(dh),
+                dweights.data_ptr()), stream, dev, torch)
+    return dh, dweights

@@ -1,12 +1,14 @@
 """Build step for libdense_gemm.so (hipcc, gfx950 only).
 
-``python -m dense_gemm_08_amd.build`` compiles ``csrc/plan.cpp`` and
-``csrc/plan_layer.cpp`` (host-side argument checks and launch planning, plain
+``python -m dense_gemm_08_amd.build`` compiles ``csrc/plan.cpp``,
+``csrc/plan_layer.cpp`` and ``csrc/plan_experts.cpp`` (host-side argument checks and launch planning, plain
 C++), ``csrc/dense_gemm.hip`` (the FP16/BF16 entry points, kernels in
 ``gemm_kernel.h``), ``csrc/ladder.hip`` (the optimisation-step kernels),
 ``csrc/gemm_mx.hip`` (the FP8 block-scaled product, kernels in
-``gemm_mx_kernel.h``) and ``csrc/layer.hip``, ``csrc/grouped.hip`` and
-``csrc/tn.hip`` (a layer's products and their gradients) into
+``gemm_mx_kernel.h``), ``csrc/layer.hip``, ``csrc/grouped.hip`` and
+``csrc/tn.hip`` (a layer's products and their gradients), ``csrc/i8.hip`` (the
+same products in int8), ``csrc/route.hip`` (routing to experts) and
+``csrc/rows.hip`` (rows quantised, and the experts' rows combined) into
 ``dense_gemm_08_amd/libdense_gemm.so`` in place.  The sources are compiled
 side by side, then linked.
 """
@@ -21,8 +23,9 @@ import tempfile
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 SRCS = [os.path.join(HERE, "csrc", n)
-        for n in ("plan.cpp", "plan_layer.cpp", "dense_gemm.hip", "ladder.hip", "gemm_mx.hip",
-                  "layer.hip", "grouped.hip", "tn.hip")]
+        for n in ("plan.cpp", "plan_layer.cpp", "plan_experts.cpp", "dense_gemm.hip", "ladder.hip",
+                  "gemm_mx.hip", "layer.hip", "grouped.hip", "tn.hip", "i8.hip", "route.hip",
+                  "rows.hip")]
 OUT = os.path.join(HERE, "libdense_gemm.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 

@@ -269,4 +269,28 @@ __device__ __forceinline__ void apply_slope(int act, float (&v)[R][C], const uin
   }
 }
 
+// The forward epilogue of C scaled sums of a row, from column col on: bias, Z,
+// activation, residual.
+template <typename O, int C>
+__device__ __forceinline__ void finish_row(const Epilogue& e, int group, int64_t row, int col, int N,
+                                           float (&x)[1][C]) {
+  uint32_t w[C / 2];
+  if (e.bias != nullptr) {
+    load_row<C / 2>(e.bias + group * e.bias_stride, col, N, w);
+#pragma unroll
+    for (int k = 0; k < C; ++k) x[0][k] += unpack<O>(w[k >> 1], k & 1);
+  }
+  if (e.z != nullptr) {
+#pragma unroll
+    for (int k = 0; k < C / 2; ++k) w[k] = pack2<O>(x[0][2 * k], x[0][2 * k + 1]);
+    store_row<C / 2>(e.z + row * e.ldz, col, N, w);
+  }
+  apply_act(e.act, x);
+  if (e.res != nullptr) {
+    load_row<C / 2>(e.res + row * e.ldr, col, N, w);
+#pragma unroll
+    for (int k = 0; k < C; ++k) x[0][k] += unpack<O>(w[k >> 1], k & 1);
+  }
+}
+
 }  // namespace dg

@@ -21,9 +21,12 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "cdna_ops.h"
 #include "epilogue.h"
 #include "groups.h"
+#include "i8.h"
 #include "tile_config.h"
 #include "tile_sched.h"
 
@@ -50,6 +53,12 @@ struct LayerParams {
   // colsum (M a group)
   float* colsum_ws;
   uint16_t* colsum;
+};
+
+// The int8 products (i8.h): A, B, K, lda, ldb and the groups' stride count pairs
+// of int8 values.
+struct LayerI8Params : LayerParams {
+  I8Scales s;
 };
 
 // Stages loaded ahead of the one in use.  Two, with rings of three slots for
@@ -85,8 +94,13 @@ struct TileAt {
 // TM: tile columns and rows; GROUP: row groups (NT, NN: groups of rows of A
 // and D with a B each; TA: sums over a group's rows, a D per group); SUMS:
 // (TA) column sums of A.  NT and NN apply the epilogue p.e.
+// T I8<O>: int8 operands (NT alone) and results of type O, the accumulators
+// whole numbers in the same registers.
 template <typename T, int LAYOUT, bool SPLIT, int TN, int TM, bool GROUP, bool SUMS = false>
-__global__ __launch_bounds__(THREADS, (per_cu<SPLIT, TN, TM>())) void layer_gemm_kernel(LayerParams p) {
+__global__ __launch_bounds__(THREADS, (per_cu<SPLIT, TN, TM>())) void layer_gemm_kernel(
+    std::conditional_t<is_i8<T>, LayerI8Params, LayerParams> p) {
+  using O = output_of<T>;
+  static_assert(!is_i8<T> || LAYOUT == NT, "int8 operands are rows of K values");
   static_assert(BK == 64, "the swizzles and offsets below assume 128-byte rows of k");
   static_assert(LAYOUT != TA || TM == TN, "A.T @ B takes square tiles");
   static_assert(!SUMS || LAYOUT == TA, "column sums of A where its rows are k");
@@ -595,10 +609,16 @@ __global__ __launch_bounds__(THREADS, (per_cu<SPLIT, TN, TM>())) void layer_gemm
       // the operand each output needs: the residual, or the gradient's Z
       const uint16_t* side = ep.grad ? ep.z : ep.res;
       const int64_t ld_side = ep.grad ? ep.ldz : ep.ldr;
-      auto fetch = [&](int pass, uint32_t(&w)[R][4]) {
+      // (int8: the columns' scales, and with the side values the rows')
+      [[maybe_unused]] float sb[8] = {};
+      if constexpr (is_i8<T>) {
+        if (!out.part) load_scales(p.s.b + out.group * p.s.b_stride, col, p.N, sb);
+      }
+      auto fetch = [&](int pass, uint32_t(&w)[R][4], [[maybe_unused]] float(&sa)[R]) {
 #pragma unroll
         for (int t = 0; t < R; ++t) {
           const int row = row0 + pass * 16 + t * RPI + rl;
+          if constexpr (is_i8<T>) sa[t] = !out.part && row < out.M ? p.s.a[row] : 0.0f;
 #pragma unroll
           for (int k = 0; k < 4; ++k) w[t][k] = 0u;
           if (side != nullptr && !out.part && row < out.M && col < p.N)
@@ -626,7 +646,8 @@ __global__ __launch_bounds__(THREADS, (per_cu<SPLIT, TN, TM>())) void layer_gemm
         }
       };
       uint32_t w[R][4], w_next[R][4] = {};
-      fetch(0, w);
+      float sa[R] = {}, sa_next[R] = {};
+      fetch(0, w, sa);
       stage(0);
       // Loads are waited for on every path (the empty asm uses their
       // results): one that the compiler believes pending when the next tile's
@@ -635,6 +656,12 @@ __global__ __launch_bounds__(THREADS, (per_cu<SPLIT, TN, TM>())) void layer_gemm
 #pragma unroll
       for (int t = 0; t < R; ++t)
         asm volatile("" : "+v"(w[t][0]), "+v"(w[t][1]), "+v"(w[t][2]), "+v"(w[t][3]));
+      if constexpr (is_i8<T>) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) asm volatile("" : "+v"(sb[k]));
+#pragma unroll
+        for (int t = 0; t < R; ++t) asm volatile("" : "+v"(sa[t]));
+      }
       float v[R][8];
       [[maybe_unused]] float v_next[R][8];
       if constexpr (PIPE) read_staged(v);
@@ -653,7 +680,7 @@ __global__ __launch_bounds__(THREADS, (per_cu<SPLIT, TN, TM>())) void layer_gemm
           default: break;
         }
         if (pass + 1 < MI) {
-          fetch(pass + 1, w_next);
+          fetch(pass + 1, w_next, sa_next);
           if constexpr (PIPE) read_staged(v_next);
         }
         if constexpr (!PIPE) read_staged(v);
@@ -669,20 +696,26 @@ __global__ __launch_bounds__(THREADS, (per_cu<SPLIT, TN, TM>())) void layer_gemm
               *(f32x4*)(ws + r * TN + 4) = (f32x4){v[t][4], v[t][5], v[t][6], v[t][7]};
             }
           }
-        } else if (ep.grad) {
-          apply_slope<T>(ep.act, v, w);
+        } else if (!is_i8<T> && ep.grad) {
+          if constexpr (!is_i8<T>) apply_slope<T>(ep.act, v, w);
         } else {
+          if constexpr (is_i8<T>) {
+#pragma unroll
+            for (int t = 0; t < R; ++t)
+#pragma unroll
+              for (int k = 0; k < 8; ++k) v[t][k] = scaled(v[t][k], sa[t], sb[k]);
+          }
 #pragma unroll
           for (int t = 0; t < R; ++t)
 #pragma unroll
-            for (int k = 0; k < 8; ++k) v[t][k] += unpack<T>(bias[k >> 1], k & 1);
+            for (int k = 0; k < 8; ++k) v[t][k] += unpack<O>(bias[k >> 1], k & 1);
           if (ep.z != nullptr) {
 #pragma unroll
             for (int t = 0; t < R; ++t) {
               const int row = row0 + pass * 16 + t * RPI + rl;
               uint32_t o[4];
 #pragma unroll
-              for (int k = 0; k < 4; ++k) o[k] = pack2<T>(v[t][2 * k], v[t][2 * k + 1]);
+              for (int k = 0; k < 4; ++k) o[k] = pack2<O>(v[t][2 * k], v[t][2 * k + 1]);
               if (row < out.M && col < p.N)
                 store_row<4>(ep.z + (int64_t)row * ep.ldz, col, p.N, o);
             }
@@ -692,19 +725,24 @@ __global__ __launch_bounds__(THREADS, (per_cu<SPLIT, TN, TM>())) void layer_gemm
 #pragma unroll
             for (int t = 0; t < R; ++t)
 #pragma unroll
-              for (int k = 0; k < 8; ++k) v[t][k] += unpack<T>(w[t][k >> 1], k & 1);
+              for (int k = 0; k < 8; ++k) v[t][k] += unpack<O>(w[t][k >> 1], k & 1);
           }
         }
 #pragma unroll
-        for (int t = 0; t < R; ++t)
+        for (int t = 0; t < R; ++t) {
           asm volatile("" : "+v"(w_next[t][0]), "+v"(w_next[t][1]), "+v"(w_next[t][2]),
                        "+v"(w_next[t][3]));
+          if constexpr (is_i8<T>) {
+            asm volatile("" : "+v"(sa_next[t]));
+            sa[t] = sa_next[t];
+          }
+        }
 #pragma unroll
         for (int t = 0; t < R; ++t) {
           const int row = row0 + pass * 16 + t * RPI + rl;
           uint32_t o[4];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) o[k] = pack2<T>(v[t][2 * k], v[t][2 * k + 1]);
+          for (int k = 0; k < 4; ++k) o[k] = pack2<O>(v[t][2 * k], v[t][2 * k + 1]);
           if (!out.part && row < out.M && col < p.N)
             store_row<4>(out.D + (int64_t)row * p.ldd, col, p.N, o);
 #pragma unroll

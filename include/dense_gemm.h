@@ -338,8 +338,14 @@ typedef enum dense_gemm_act {
   DENSE_GEMM_ACT_SILU = 4
 } dense_gemm_act;
 
-/* The element type of dense_gemm_tn's operands and results. */
-typedef enum dense_gemm_fmt { DENSE_GEMM_F16 = 0, DENSE_GEMM_BF16 = 1 } dense_gemm_fmt;
+/* The element type of a call's matrices: of dense_gemm_tn's operands and
+ * results, of the results of dense_gemm_i8, of the rows of the calls below it.
+ * (F32: logits alone.) */
+typedef enum dense_gemm_fmt {
+  DENSE_GEMM_F16 = 0,
+  DENSE_GEMM_BF16 = 1,
+  DENSE_GEMM_F32 = 2
+} dense_gemm_fmt;
 
 /* What dense_gemm_layer does to the accumulated product P.
  *   grad 0   Z = P + bias,  D = act(Z) + residual
@@ -431,6 +437,139 @@ dense_gemm_status dense_gemm_tn_workspace_size(int64_t M, int64_t N, int64_t K, 
                                                int64_t lda, const void* B, int64_t ldb, int colsum,
                                                const dense_gemm_groups* groups, int64_t num_cus,
                                                size_t* bytes);
+
+/* ---- a layer's products in 8-bit integers --------------------------------
+ * D = act(Z) + residual, Z = (A @ B.T) * sa * sb + bias, with int8 A and B and
+ * one FP32 scale per row of each (a scale per token and per output channel):
+ *     P[i][j] = sum_{k < K} A[i][k] * B[j][k]         exactly, in 32 bits
+ *     Z[i][j] = P[i][j] * SA[i] * SB[j] + bias[j]     in FP32
+ * fmt: the type of D, bias, residual and preact (DENSE_GEMM_F16 or _BF16).
+ *   A   M x K bytes, element (i, k) at A[i * lda + k]
+ *   B   N x K bytes, element (j, k) at B[j * ldb + k]
+ *   SA  M floats,  SB  N floats (4-byte aligned)
+ * epilogue as for dense_gemm_layer, with grad 0 (null: none).  With groups,
+ * group g's rows are multiplied with B + g * groups->stride bytes and its
+ * columns' scales are SB + g * sb_stride floats (sb_stride is not looked at
+ * otherwise); rows that no group holds are not written.  A and B may begin
+ * anywhere; they are read in place where their rows begin at 4-byte addresses
+ * and K is a multiple of 4 (small outputs: any K), and copied into the workspace
+ * otherwise.  K at most 131071 (DENSE_GEMM_TOO_LARGE), so that no sum passes 32
+ * bits.  The sums are exact: results do not depend on the plan.  Workspace,
+ * groups, limits and errors as for dense_gemm_layer. */
+dense_gemm_status dense_gemm_i8(int fmt, int64_t M, int64_t N, int64_t K, const void* A, int64_t lda,
+                                const void* SA, const void* B, int64_t ldb, const void* SB,
+                                int64_t sb_stride, void* D, int64_t ldd,
+                                const dense_gemm_epilogue* epilogue, const dense_gemm_groups* groups,
+                                void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* Bytes of workspace dense_gemm_i8 needs (groups may be null; its `ends` is not
+ * read).  num_cus as for dense_gemm_workspace_size. */
+dense_gemm_status dense_gemm_i8_workspace_size(int64_t M, int64_t N, int64_t K, const void* A,
+                                               int64_t lda, const void* B, int64_t ldb,
+                                               const dense_gemm_groups* groups, int64_t num_cus,
+                                               size_t* bytes);
+
+/* Rows quantised to int8, as dense_gemm_i8 takes them: for 0 <= i < R, with x
+ * row rows[i] of X (rows null: row i) and m its largest absolute value,
+ *     S[i] = m / 127,   Q[i][k] = round(127 * x[k] / m)
+ * each Q the nearest whole number to the exact quotient (half-way: the even
+ * one), S the nearest float.  X is x_rows x K of type fmt (DENSE_GEMM_F16 or
+ * _BF16), leading dimension ldx; Q has ldq bytes between its rows and may begin
+ * anywhere; rows is R int32 on the device (the `tokens` of dense_gemm_route), S
+ * R floats.  A row of zeros gets zeros and scale 0, one that holds an infinity
+ * or NaN zeros and the scale NaN, and one whose index lies outside [0, x_rows)
+ * zeros and scale 0.  Without rows, R may not exceed x_rows
+ * (DENSE_GEMM_BAD_ARG). */
+dense_gemm_status dense_gemm_quantize_i8(int fmt, int64_t R, int64_t K, const void* X, int64_t ldx,
+                                         int64_t x_rows, const void* rows, void* Q, int64_t ldq,
+                                         void* S, hipStream_t stream);
+
+/* ---- routing to experts ---------------------------------------------------
+ * What stands before and behind the products of row groups: from the logits of
+ * T tokens for E experts (T x E, type fmt: any dense_gemm_fmt, leading dimension
+ * ldl) each token's k experts and their weights, the order of the rows by
+ * expert, and the sum that brings the experts' rows back.
+ *
+ *   s  the scores: softmax over the token's E logits, or logistic of each
+ *   c  s + bias (bias decides the choice alone; without one the experts rank as
+ *      their logits do)
+ *   groups: the experts lie in `groups` runs of E / groups; a group's value is
+ *      the sum of its group_top (1 or 2) largest c, as many as it has; only the
+ *      top_groups groups of the largest values stay (groups = top_groups = 1:
+ *      no such choice)
+ *   chosen: the k experts of the largest c that stay, in descending order; equal
+ *      ones (of groups too) in that of their index
+ *   weights: s of the chosen, divided by their sum with renorm, times scale
+ *
+ * An expert whose logit is -infinity, or whose c is -infinity or NaN, is never
+ * chosen.  Where a token has fewer than k to choose from (a row masked out has
+ * none), the choices left over have expert -1, weight 0 and place -1.  A token
+ * with a logit that is NaN or +infinity gets no experts and weights of NaN.
+ * Scores are compared as 64 bits tell them apart.
+ *
+ *   weights  T x k floats      experts  T x k int32
+ *   ends     E int32: the number of choices of experts 0 .. e, as
+ *            dense_gemm_groups takes them
+ *   tokens   T k int32: the token of every row in the experts' order, within an
+ *            expert in the tokens' order; -1 from ends[E - 1] on
+ *   places   T x k int32: the row of every choice in that order
+ * All 4-byte aligned, without gaps.  1 <= k <= 64, k at most the experts that
+ * can stay, E <= 1024, groups <= 64 and a divisor of E.  Every output is
+ * written whole and depends on the inputs alone.  T == 0 writes the ends. */
+typedef enum dense_gemm_score { DENSE_GEMM_SOFTMAX = 0, DENSE_GEMM_SIGMOID = 1 } dense_gemm_score;
+
+typedef struct dense_gemm_routing {
+  const void* bias; /* E floats, or null */
+  int32_t score;    /* a dense_gemm_score */
+  int32_t renorm;   /* 0 or 1 */
+  float scale;
+  int32_t groups;
+  int32_t top_groups;
+  int32_t group_top;
+} dense_gemm_routing;
+
+dense_gemm_status dense_gemm_route(int fmt, int64_t T, int64_t E, int64_t k, const void* logits,
+                                   int64_t ldl, const dense_gemm_routing* routing, void* weights,
+                                   void* experts, void* places, void* ends, void* tokens,
+                                   void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* Bytes of workspace dense_gemm_route needs: the choices per expert of every 64
+ * tokens (or more), beyond 128 tokens. */
+dense_gemm_status dense_gemm_route_workspace_size(int64_t T, int64_t E, int64_t k, size_t* bytes);
+
+/* The gradient of the logits (dlogits: T x E, type fmt, leading dimension ldd)
+ * from that of the weights, for the experts that dense_gemm_route chose.  Of
+ * `routing` only score, renorm and scale count; the bias and the choice have no
+ * gradient.  A choice outside [0, E) takes no part. */
+dense_gemm_status dense_gemm_route_grad(int fmt, int64_t T, int64_t E, int64_t k, const void* logits,
+                                        int64_t ldl, const dense_gemm_routing* routing,
+                                        const void* experts, const void* dweights, void* dlogits,
+                                        int64_t ldd, hipStream_t stream);
+
+/* The experts' rows back to their tokens: for 0 <= t < T
+ *     Y[t] = round( sum_j weights[t][j] * H[places[t][j]] + residual[t] )
+ * summed in FP32 in the order of j.  H is h_rows x N of type fmt (DENSE_GEMM_F16
+ * or _BF16), residual (or null) and Y T x N; places T x k int32, weights T x k
+ * floats (null: ones, e.g. for the gradient of rows that were gathered by
+ * `tokens`).  1 <= k <= 64.  A place outside [0, h_rows) adds its weight times
+ * zero.  residual may be Y itself; Y must overlap nothing else. */
+dense_gemm_status dense_gemm_combine(int fmt, int64_t T, int64_t N, int64_t k, const void* H,
+                                     int64_t ldh, int64_t h_rows, const void* places,
+                                     const void* weights, const void* residual, int64_t ldr, void* Y,
+                                     int64_t ldy, hipStream_t stream);
+
+/* Its gradients:
+ *     DH[places[t][j]] = round( weights[t][j] * DY[t] )
+ *     dweights[t][j]   = sum_n DY[t][n] * H[places[t][j]][n]   (FP32)
+ * Either may be null (H is read for dweights alone, and dweights needs N > 0:
+ * DENSE_GEMM_BAD_ARG).  Rows of DH that no place names are left as they were;
+ * the places of dense_gemm_route name each row once (of one named twice, either
+ * may stay).  A place outside [0, h_rows) writes no row and a dweights of 0.
+ * DH must overlap neither H nor DY. */
+dense_gemm_status dense_gemm_combine_grad(int fmt, int64_t T, int64_t N, int64_t k, const void* DY,
+                                          int64_t lddy, const void* H, int64_t ldh, int64_t h_rows,
+                                          const void* places, const void* weights, void* DH,
+                                          int64_t lddh, void* dweights, hipStream_t stream);
 
 /* A static, human-readable name for a status code (never NULL). */
 const char* dense_gemm_status_string(int status);
