@@ -9,15 +9,19 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+#include <utility>
+
 namespace dg {
 
+// x of another lane of the row (all these patterns read lanes that there are).
 template <int CTRL>
 __device__ __forceinline__ uint32_t dpp_move(uint32_t x) {
-  return (uint32_t)__builtin_amdgcn_update_dpp((int)x, (int)x, CTRL, 0xf, 0xf, false);
+  return (uint32_t)__builtin_amdgcn_mov_dpp((int)x, CTRL, 0xf, 0xf, true);
 }
 template <int CTRL>
 __device__ __forceinline__ int dpp_move(int x) {
-  return __builtin_amdgcn_update_dpp(x, x, CTRL, 0xf, 0xf, false);
+  return __builtin_amdgcn_mov_dpp(x, CTRL, 0xf, 0xf, true);
 }
 template <int CTRL>
 __device__ __forceinline__ float dpp_move(float x) {
@@ -30,6 +34,32 @@ __device__ __forceinline__ double dpp_move(double x) {
   return __builtin_bit_cast(double, lo | (hi << 32));
 }
 
+// x of the even rows of 16 (S 16) or of the first two (S 32), `which` 0, or of the
+// others, 1, in both rows of a pair: v_permlane16_swap and v_permlane32_swap of x
+// with itself.
+template <int S>
+__device__ __forceinline__ uint32_t across(uint32_t x, int which) {
+  typedef uint32_t pair __attribute__((ext_vector_type(2)));
+  if constexpr (S == 16)
+    return __builtin_bit_cast(pair, __builtin_amdgcn_permlane16_swap(x, x, false, false))[which];
+  else
+    return __builtin_bit_cast(pair, __builtin_amdgcn_permlane32_swap(x, x, false, false))[which];
+}
+template <int S>
+__device__ __forceinline__ int across(int x, int which) {
+  return (int)across<S>((uint32_t)x, which);
+}
+template <int S>
+__device__ __forceinline__ float across(float x, int which) {
+  return __builtin_bit_cast(float, across<S>(__builtin_bit_cast(uint32_t, x), which));
+}
+template <int S>
+__device__ __forceinline__ double across(double x, int which) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, x);
+  const uint64_t lo = across<S>((uint32_t)b, which), hi = across<S>((uint32_t)(b >> 32), which);
+  return __builtin_bit_cast(double, lo | (hi << 32));
+}
+
 // x of L lanes (16 or 64) combined by op(a, b), a commutative one.
 template <int L, typename X, typename Op>
 __device__ __forceinline__ X reduce_lanes(X x, Op&& op) {
@@ -39,23 +69,54 @@ __device__ __forceinline__ X reduce_lanes(X x, Op&& op) {
   x = op(x, dpp_move<0x141>(x));  // row_half_mirror
   x = op(x, dpp_move<0x140>(x));  // row_mirror
   if constexpr (L == 64) {
-    x = op(x, (X)__shfl_xor(x, 16));
-    x = op(x, (X)__shfl_xor(x, 32));
+    x = op(across<16>(x, 0), across<16>(x, 1));
+    x = op(across<32>(x, 0), across<32>(x, 1));
   }
   return x;
 }
 
-template <int L, typename X>
-__device__ __forceinline__ X max_lanes(X x) {
-  return reduce_lanes<L>(x, [](X a, X b) { return b > a ? b : a; });
+// (whole numbers: max and min take a DPP operand)
+template <typename X>
+__device__ __forceinline__ X larger(X a, X b) {
+  if constexpr (std::is_integral_v<X>)
+    return max(a, b);
+  else
+    return b > a ? b : a;
 }
 template <int L, typename X>
-__device__ __forceinline__ X min_lanes(X x) {
-  return reduce_lanes<L>(x, [](X a, X b) { return b < a ? b : a; });
+__device__ __forceinline__ X max_lanes(X x) {
+  return reduce_lanes<L>(x, [](X a, X b) { return larger(a, b); });
+}
+template <int L>
+__device__ __forceinline__ int min_lanes(int x) {
+  return reduce_lanes<L>(x, [](int a, int b) { return min(a, b); });
 }
 template <int L, typename X>
 __device__ __forceinline__ X sum_lanes(X x) {
   return reduce_lanes<L>(x, [](X a, X b) { return a + b; });
+}
+
+// x of the lane N places back in its row of 16, counted around.
+template <int N, typename X>
+__device__ __forceinline__ X rotated(X x) {
+  return dpp_move<0x120 + N>(x);
+}
+// f(std::integral_constant<int, N>) for N = 1 .. 15.
+template <typename F, int... N>
+__device__ __forceinline__ void for_others(F&& f, std::integer_sequence<int, N...>) {
+  (f(std::integral_constant<int, N + 1>()), ...);
+}
+template <typename F>
+__device__ __forceinline__ void for_others(F&& f) {
+  for_others(f, std::make_integer_sequence<int, 15>());
+}
+
+// Values that lanes of this wave left in LDS for each other: the accesses after
+// this follow those before it (a wave's LDS accesses complete in order).
+__device__ __forceinline__ void wave_lds_order() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
 }  // namespace dg

@@ -98,6 +98,14 @@ dense_gemm_status dense_gemm_route(int fmt, int64_t T, int64_t E, int64_t k, con
   p.top_groups = routing->top_groups;
   // (where all groups stay their values do not matter)
   p.group_top = p.top_groups < p.groups ? routing->group_top : 1;
+  p.ranked = p.bias == nullptr;
+  // (up to 1024 experts, a group of m: e (2^20 + m) / m 2^-20 exceeds e / m by
+  // less than 1 / m)
+  p.group_inverse = (int)(((1 << 20) + p.group_size - 1) / p.group_size);
+  const int lanes = E <= 256 ? 16 : 64;
+  p.group_lanes = 1;
+  while (p.group_lanes < 16 && 2 * p.group_lanes * p.groups <= lanes) p.group_lanes *= 2;
+  p.k_inverse = (int)(((1 << 20) + k - 1) / k);
   p.chunks = (int)plan.chunks;
   if (fmt == DENSE_GEMM_F32) return run_route<float>(p, plan, stream);
   return fmt == DENSE_GEMM_BF16 ? run_route<__bf16>(p, plan, stream) : run_route<_Float16>(p, plan, stream);
