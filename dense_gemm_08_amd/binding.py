@@ -404,18 +404,22 @@ def gemm_nt_e4m3_mx(A, SA, B, SB, D=None, stream=None, workspace=None):
 
 _FMTS = None   # torch dtype -> (name, dense_gemm_fmt); set by _torch()
 _raw_stream = None
+_current_device = None
+_module = None
 
 
 def _torch():
-    global _FMTS, _raw_stream
-    import torch
+    global _FMTS, _raw_stream, _current_device, _module
     if _FMTS is None:
+        import torch
+        _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
         # (the current stream's handle without building a Stream object,
         # where this torch has it: 0.1 against 2 us)
         _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        _module = torch  # (an import statement at every call: 0.4 us)
         # (last, and whole: another thread's call may come in between)
         _FMTS = {torch.bfloat16: ("bf16", 1), torch.float16: ("f16", 0)}
-    return torch
+    return _module
 
 
 def _check_like(t, dtype, dev: int, dims: int, what: str, shape=None):
@@ -467,7 +471,7 @@ def _launch(name, args, size_of, workspace, stream, dev, torch):
     ``dev``.  Without a workspace of the caller's, one is taken from torch's
     allocator if the call turns out to need it (``size_of``: its size query
     and that query's arguments)."""
-    if torch.cuda.current_device() != dev:
+    if _current_device() != dev:
         with torch.cuda.device(dev):
             return _launch(name, args, size_of, workspace, stream, dev, torch)
     fn = getattr(_lib, name)
@@ -671,24 +675,52 @@ def gemm_tn_grouped(A, B, ends, D=None, colsum=None, stream=None, workspace=None
 
 
 # ---- int8 products, and the operators around an expert layer's products ------
+#
+# What an operand has to be is asked in one expression; only where it is not do
+# the checks that name the reason run.
 
-def _check_scales(t, dev: int, shape, what: str):
-    """FP32 scales on device number ``dev``, contiguous in their last
-    dimension."""
-    if t.dtype is not _torch().float32:
-        raise TypeError("%s must be float32, got %s" % (what, t.dtype))
+def _check_dense(t, dtype, dev: int, shape, what: str):
+    """A contiguous tensor of this type and shape on device number ``dev``."""
+    if t.dtype is dtype and t.get_device() == dev and t.shape == shape and t.is_contiguous():
+        return
+    if t.dtype is not dtype:
+        raise TypeError("%s must be %s, got %s" % (what, dtype, t.dtype))
     if t.get_device() != dev:
-        raise ValueError("operands on different devices: %s on %s" % (what, t.device))
-    if t.shape != shape or (t.shape[-1] > 1 and t.stride(-1) != 1):
-        raise ValueError("%s must have shape %s with unit stride in its last dimension, got %s"
-                         % (what, tuple(shape), tuple(t.shape)))
+        raise ValueError("operands on different devices: %s on %s, not cuda:%d" % (what, t.device, dev))
+    raise ValueError("%s must be contiguous with shape %s, got %s"
+                     % (what, tuple(shape), tuple(t.shape)))
+
+
+def _check_rows(t, dtype, dev: int, shape, what: str):
+    """A 2-D tensor with unit column stride, of this type and shape on device
+    number ``dev``; returns its leading dimension."""
+    if t.dtype is dtype and t.get_device() == dev and t.shape == shape:
+        ld, one = t.stride()
+        if one == 1:
+            return ld if shape[0] > 1 else max(shape[1], 1)
+    _check_like(t, dtype, dev, 2, what, shape)
+    return _ld(t)
+
+
+def _run(fn, name, args, stream, dev):
+    """``fn(*args, stream)``, a call that takes no workspace, on device number
+    ``dev``."""
+    if _current_device() != dev:
+        with _module.cuda.device(dev):
+            return _run(fn, name, args, stream, dev)
+    if stream is None and _raw_stream is not None:
+        st = fn(*args, _raw_stream(dev))
+    else:
+        st = fn(*args, _stream_handle(stream, dev))
+    if st != 0:
+        raise DenseGemmError(st, name)
 
 
 def _i8(A, SA, B, SB, ends, bias, act, residual, preact, D, dtype, stream, workspace):
     if _lib is None:
         load_library()
     torch = _torch()
-    int8 = torch.int8
+    int8, f32 = torch.int8, torch.float32
     if A.dtype is not int8:
         raise TypeError("A must be int8, got %s" % A.dtype)
     if not A.is_cuda:
@@ -712,7 +744,7 @@ def _i8(A, SA, B, SB, ends, bias, act, residual, preact, D, dtype, stream, works
     fmt = _FMTS.get(dtype)
     if fmt is None:
         raise TypeError("D must be float16 or bfloat16, got %s" % dtype)
-    groups, G, sb_stride = None, (), 0
+    groups, G, sb_stride = None, (), N
     if ends is None:
         ldb = _ld(B)
     else:
@@ -722,10 +754,8 @@ def _i8(A, SA, B, SB, ends, bias, act, residual, preact, D, dtype, stream, works
             raise ValueError("%d group ends for %d matrices B" % (ends.shape[0], G[0]))
         stride, ldb = _stack(B)
         groups = Groups(ends.data_ptr(), G[0], stride)
-        if G[0] > 1 and SB.dim() == 2:
-            sb_stride = SB.stride(0)
-    _check_scales(SA, dev, (M,), "SA")
-    _check_scales(SB, dev, G + (N,), "SB")
+    _check_dense(SA, f32, dev, (M,), "SA")
+    _check_dense(SB, f32, dev, G + (N,), "SB")
     epi = None
     if code or bias is not None or residual is not None or preact is not None:
         epi = Epilogue(act=code)
@@ -735,21 +765,22 @@ def _i8(A, SA, B, SB, ends, bias, act, residual, preact, D, dtype, stream, works
             if G and G[0] > 1:
                 epi.bias_stride = bias.stride(0)
         if residual is not None:
-            _check_like(residual, dtype, dev, 2, "residual", (M, N))
-            epi.residual, epi.ldr = residual.data_ptr(), _ld(residual)
+            epi.ldr = _check_rows(residual, dtype, dev, (M, N), "residual")
+            epi.residual = residual.data_ptr()
         if preact is not None:
-            _check_like(preact, dtype, dev, 2, "preact", (M, N))
-            epi.preact, epi.ldz = preact.data_ptr(), _ld(preact)
+            epi.ldz = _check_rows(preact, dtype, dev, (M, N), "preact")
+            epi.preact = preact.data_ptr()
     if D is None:
-        D = torch.empty((M, N), dtype=dtype, device=A.device)
+        D = A.new_empty((M, N), dtype=dtype)
+        ldd = max(N, 1)
         if stream is not None:
             _used_by(D, stream, A.device)
     else:
-        _check_like(D, dtype, dev, 2, "D", (M, N))
+        ldd = _check_rows(D, dtype, dev, (M, N), "D")
     a, lda, b = A.data_ptr(), _ld(A), B.data_ptr()
     _launch("dense_gemm_i8",
             (fmt[1], M, N, K, a, lda, SA.data_ptr(), b, ldb, SB.data_ptr(), sb_stride, D.data_ptr(),
-             _ld(D), epi, groups),
+             ldd, epi, groups),
             ("dense_gemm_i8_workspace_size", M, N, K, a, lda, b, ldb, groups, 0), workspace, stream,
             dev, torch)
     return D
@@ -773,39 +804,6 @@ def gemm_nt_i8_grouped(A, SA, B, SB, ends, bias=None, act="none", residual=None,
     return _i8(A, SA, B, SB, ends, bias, act, residual, preact, D, dtype, stream, workspace)
 
 
-def _call_rows(name, args, stream, dev, torch):
-    """Calls ``name(*args, stream)``, which takes no workspace, on device number
-    ``dev``."""
-    if torch.cuda.current_device() != dev:
-        with torch.cuda.device(dev):
-            return _call_rows(name, args, stream, dev, torch)
-    if stream is None and _raw_stream is not None:
-        sh = _raw_stream(dev)
-    else:
-        sh = _stream_handle(stream, dev)
-    st = getattr(_lib, name)(*args, sh)
-    if st != 0:
-        raise DenseGemmError(st, name)
-
-
-def _check_dense(t, dtype, dev: int, shape, what: str):
-    """A contiguous tensor of this type and shape on device number ``dev``."""
-    if t.dtype is not dtype:
-        raise TypeError("%s must be %s, got %s" % (what, dtype, t.dtype))
-    if t.get_device() != dev:
-        raise ValueError("operands on different devices: %s on %s, not cuda:%d" % (what, t.device, dev))
-    if t.shape != shape or not t.is_contiguous():
-        raise ValueError("%s must be contiguous with shape %s, got %s"
-                         % (what, tuple(shape), tuple(t.shape)))
-
-
-def _new(shape, dtype, like, stream, torch):
-    t = torch.empty(shape, dtype=dtype, device=like.device)
-    if stream is not None:
-        _used_by(t, stream, like.device)
-    return t
-
-
 def quantize_rows(X, rows=None, Q=None, S=None, stream=None):
     """(Q, S): the rows of X (float16 or bfloat16) as int8 with a float32 scale
     each, X[i] ~ Q[i] * S[i], as :func:`gemm_nt_i8` takes them: S is the row's
@@ -819,23 +817,28 @@ def quantize_rows(X, rows=None, Q=None, S=None, stream=None):
     torch = _torch()
     fmt, _, dev = _check_first(X)
     T, K = X.shape
-    R = T
+    R, index = T, None
     if rows is not None:
         if rows.dim() != 1:
             raise ValueError("rows must be 1-D")
         R = rows.shape[0]
         _check_dense(rows, torch.int32, dev, (R,), "rows")
+        index = rows.data_ptr()
     if Q is None:
-        Q = _new((R, K), torch.int8, X, stream, torch)
+        Q = X.new_empty((R, K), dtype=torch.int8)
+        ldq = max(K, 1)
+        if stream is not None:
+            _used_by(Q, stream, X.device)
     else:
-        _check_like(Q, torch.int8, dev, 2, "Q", (R, K))
+        ldq = _check_rows(Q, torch.int8, dev, (R, K), "Q")
     if S is None:
-        S = _new((R,), torch.float32, X, stream, torch)
+        S = X.new_empty((R,), dtype=torch.float32)
+        if stream is not None:
+            _used_by(S, stream, X.device)
     else:
         _check_dense(S, torch.float32, dev, (R,), "S")
-    _call_rows("dense_gemm_quantize_i8",
-               (fmt[1], R, K, X.data_ptr(), _ld(X), T, None if rows is None else rows.data_ptr(),
-                Q.data_ptr(), _ld(Q), S.data_ptr()), stream, dev, torch)
+    _run(_lib.dense_gemm_quantize_i8, "dense_gemm_quantize_i8",
+         (fmt[1], R, K, X.data_ptr(), _ld(X), T, index, Q.data_ptr(), ldq, S.data_ptr()), stream, dev)
     return Q, S
 
 
@@ -905,14 +908,24 @@ def route(logits, k, score="softmax", bias=None, groups=1, top_groups=1, group_t
     if bias is not None:
         _check_dense(bias, torch.float32, dev, (E,), "bias")
         r.bias = bias.data_ptr()
-    weights = _new((T, k), torch.float32, logits, stream, torch)
-    experts = _new((T, k), torch.int32, logits, stream, torch)
-    places = _new((T, k), torch.int32, logits, stream, torch)
-    ends = _new((E,), torch.int32, logits, stream, torch)
-    tokens = _new((T * k,), torch.int32, logits, stream, torch)
+    if k < 0:
+        raise ValueError("k must not be negative, got %d" % k)
+    # one block of memory for the outputs, a part of it each: an allocation costs
+    # twice what a view does
+    n = T * k
+    ints = logits.new_empty((3 * n + E,), dtype=torch.int32)
+    weights = logits.new_empty((T, k), dtype=torch.float32)
+    experts = ints.as_strided((T, k), (k, 1), 0)
+    places = ints.as_strided((T, k), (k, 1), n)
+    tokens = ints.as_strided((n,), (1,), 2 * n)
+    ends = ints.as_strided((E,), (1,), 3 * n)
+    if stream is not None:
+        _used_by(ints, stream, logits.device)
+        _used_by(weights, stream, logits.device)
+    at = ints.data_ptr()
     _launch("dense_gemm_route",
-            (fmt, T, E, k, logits.data_ptr(), _ld(logits), r, weights.data_ptr(), experts.data_ptr(),
-             places.data_ptr(), ends.data_ptr(), tokens.data_ptr()),
+            (fmt, T, E, k, logits.data_ptr(), _ld(logits), r, weights.data_ptr(), at, at + 4 * n,
+             at + 12 * n, at + 8 * n),
             ("dense_gemm_route_workspace_size", T, E, k), workspace, stream, dev, torch)
     return Routes(weights, experts, places, ends, tokens)
 
@@ -933,23 +946,27 @@ def route_grad(logits, experts, dweights, score="softmax", renorm=True, scale=1.
     _check_dense(experts, torch.int32, dev, (T, k), "experts")
     _check_dense(dweights, torch.float32, dev, (T, k), "dweights")
     if D is None:
-        D = _new((T, E), logits.dtype, logits, stream, torch)
+        D = logits.new_empty((T, E))
+        ldd = max(E, 1)
+        if stream is not None:
+            _used_by(D, stream, logits.device)
     else:
-        _check_like(D, logits.dtype, dev, 2, "D", (T, E))
+        ldd = _check_rows(D, logits.dtype, dev, (T, E), "D")
     r = Routing(None, _score(score), bool(renorm), scale, 1, 1, 1)
-    _call_rows("dense_gemm_route_grad",
-               (fmt, T, E, k, logits.data_ptr(), _ld(logits), r, experts.data_ptr(),
-                dweights.data_ptr(), D.data_ptr(), _ld(D)), stream, dev, torch)
+    _run(_lib.dense_gemm_route_grad, "dense_gemm_route_grad",
+         (fmt, T, E, k, logits.data_ptr(), _ld(logits), r, experts.data_ptr(), dweights.data_ptr(),
+          D.data_ptr(), ldd), stream, dev)
     return D
 
 
 def _check_choices(places, weights, dev, torch):
     if places.dim() != 2:
         raise ValueError("places must be 2-D")
-    _check_dense(places, torch.int32, dev, places.shape, "places")
+    shape = places.shape
+    _check_dense(places, torch.int32, dev, shape, "places")
     if weights is not None:
-        _check_dense(weights, torch.float32, dev, places.shape, "weights")
-    return places.shape
+        _check_dense(weights, torch.float32, dev, shape, "weights")
+    return shape
 
 
 def combine_rows(H, places, weights=None, residual=None, D=None, stream=None):
@@ -964,17 +981,20 @@ def combine_rows(H, places, weights=None, residual=None, D=None, stream=None):
     fmt, dtype, dev = _check_first(H)
     R, N = H.shape
     T, k = _check_choices(places, weights, dev, torch)
+    res, ldr = None, 0
     if residual is not None:
-        _check_like(residual, dtype, dev, 2, "residual", (T, N))
+        ldr = _check_rows(residual, dtype, dev, (T, N), "residual")
+        res = residual.data_ptr()
     if D is None:
-        D = _new((T, N), dtype, H, stream, torch)
+        D = H.new_empty((T, N))
+        ldd = max(N, 1)
+        if stream is not None:
+            _used_by(D, stream, H.device)
     else:
-        _check_like(D, dtype, dev, 2, "D", (T, N))
-    _call_rows("dense_gemm_combine",
-               (fmt[1], T, N, k, H.data_ptr(), _ld(H), R, places.data_ptr(),
-                None if weights is None else weights.data_ptr(),
-                None if residual is None else residual.data_ptr(),
-                0 if residual is None else _ld(residual), D.data_ptr(), _ld(D)), stream, dev, torch)
+        ldd = _check_rows(D, dtype, dev, (T, N), "D")
+    _run(_lib.dense_gemm_combine, "dense_gemm_combine",
+         (fmt[1], T, N, k, H.data_ptr(), _ld(H), R, places.data_ptr(),
+          None if weights is None else weights.data_ptr(), res, ldr, D.data_ptr(), ldd), stream, dev)
     return D
 
 
@@ -990,14 +1010,19 @@ def combine_rows_grad(dY, H, places, weights=None, dh=None, stream=None):
     fmt, dtype, dev = _check_first(H)
     R, N = H.shape
     T, k = _check_choices(places, weights, dev, torch)
-    _check_like(dY, dtype, dev, 2, "dY", (T, N))
+    ldy = _check_rows(dY, dtype, dev, (T, N), "dY")
     if dh is None:
-        dh = _new((R, N), dtype, H, stream, torch)
+        dh = H.new_empty((R, N))
+        ldh = max(N, 1)
+        if stream is not None:
+            _used_by(dh, stream, H.device)
     else:
-        _check_like(dh, dtype, dev, 2, "dh", (R, N))
-    dweights = _new((T, k), torch.float32, H, stream, torch)
-    _call_rows("dense_gemm_combine_grad",
-               (fmt[1], T, N, k, dY.data_ptr(), _ld(dY), H.data_ptr(), _ld(H), R, places.data_ptr(),
-                None if weights is None else weights.data_ptr(), dh.data_ptr(), _ld(dh),
-                dweights.data_ptr()), stream, dev, torch)
+        ldh = _check_rows(dh, dtype, dev, (R, N), "dh")
+    dweights = H.new_empty((T, k), dtype=torch.float32)
+    if stream is not None:
+        _used_by(dweights, stream, H.device)
+    _run(_lib.dense_gemm_combine_grad, "dense_gemm_combine_grad",
+         (fmt[1], T, N, k, dY.data_ptr(), ldy, H.data_ptr(), _ld(H), R, places.data_ptr(),
+          None if weights is None else weights.data_ptr(), dh.data_ptr(), ldh, dweights.data_ptr()),
+         stream, dev)
     return dh, dweights

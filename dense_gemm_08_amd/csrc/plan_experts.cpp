@@ -103,10 +103,12 @@ RoutePlan route_plan(int64_t T, int64_t E) {
   return p;
 }
 
-// A wave holds 4096 elements of a row, four waves 16384, sixteen 65536.  Rows
-// that fit a wave take four where there are too few of them for every SIMD.
+// Sixteen lanes hold 1024 elements of a row, a wave 4096, four waves 16384,
+// sixteen 65536.  Short rows in number go to 16 lanes, rows that fit a wave to
+// four where there are too few of them for every SIMD.
 int row_lanes(int64_t rows, int64_t cols, int64_t cus) {
   if (cols > 16384) return 1024;
+  if (cols <= 1024 && rows >= 32 * cus) return 16;
   return cols > 4096 || (cols > 512 && rows < 4 * cus) ? 256 : 64;
 }
 
@@ -245,12 +247,21 @@ dense_gemm_status i8_plan(int64_t M, int64_t N, int64_t K, const void* A, int64_
   return DENSE_GEMM_OK;
 }
 
+// With int8 values a K step holds twice the products for the same bytes, and 128
+// x 128 tiles, which move twice the bytes of 256 x 256 ones per product, fall
+// further behind than their 16-bit estimate (79) says: 110 decides as measured on
+// all of these but the last, us, 256 against 128: 16 groups of 256, N = K = 4096,
+// 79 and 94; of 1024 235 and 331, K = 2048 144 and 197; 32 of 512, N = 2048, K =
+// 4096, 130 and 167; 64 of 256, N = K = 2048, 87 and 107; 4 of 512, N = 512, K =
+// 4096, 47 and 22; 48 of 300, N = 1400, K = 2000, 111 and 96; 128 of 200, N =
+// 1024, K = 4096, 137 and 191.
 dense_gemm_status i8_grouped_plan(int64_t M, int64_t N, int64_t K, const void* A, int64_t lda,
                                   const void* B, int64_t ldb, const dense_gemm_groups& g, int64_t cus,
                                   GroupedPlan* out) {
   const int64_t K2 = pairs(K);
   dense_gemm_groups even = {g.ends, g.count, g.stride == 0 ? 0 : 8};
-  const dense_gemm_status st = grouped_plan(NT, M, N, K2, kAligned, K2 + 8, kAligned, K2 + 8, even, cus, out);
+  const dense_gemm_status st = grouped_plan(NT, M, N, K2, kAligned, K2 + 8, kAligned, K2 + 8, even, cus, out,
+                                            kNarrowStepI8);
   if (st != DENSE_GEMM_OK) return st;
   out->a_direct = K == 0 || direct_i8(A, lda, 0, K, out->small);
   out->b_direct = K == 0 || direct_i8(B, ldb, g.stride, K, out->small);

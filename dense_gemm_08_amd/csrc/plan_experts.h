@@ -36,7 +36,8 @@ RoutePlan route_plan(int64_t T, int64_t E);
 
 // ---- rows ----
 
-// Lanes that share a row of `cols` elements, of `rows` rows: 64, 256 or 1024.
+// Lanes that share a row of `cols` elements, of `rows` rows: 16, 64, 256 or
+// 1024.
 int row_lanes(int64_t rows, int64_t cols, int64_t cus);
 
 dense_gemm_status quantize_validate(int fmt, int64_t R, int64_t K, const void* X, int64_t ldx,

@@ -200,7 +200,7 @@ dense_gemm_status layer_plan(int layout, int64_t M, int64_t N, int64_t K, const 
 
 dense_gemm_status grouped_plan(int layout, int64_t M, int64_t N, int64_t K, const void* A,
                                int64_t lda, const void* B, int64_t ldb, const dense_gemm_groups& g,
-                               int64_t cus, GroupedPlan* out) {
+                               int64_t cus, GroupedPlan* out, int64_t narrow_step) {
   const int64_t K8 = round8(K), N8 = round8(N);
   // The ends are not known here: the tile follows the rows of an average
   // group (of those that can have any) and the number of tiles.  Measured
@@ -236,7 +236,7 @@ dense_gemm_status grouped_plan(int layout, int64_t M, int64_t N, int64_t K, cons
   const int64_t est256 = (M + BM / 2 * active) / BM * ((N + BN - 1) / BN);
   const int64_t est128 = (M + BM / 4 * active) / (BM / 2) * ((N + BN / 2 - 1) / (BN / 2));
   const bool narrow = (est128 <= slots128 || nk <= 2 * NARROW_STEPS) &&
-                      (double)((est128 + slots128 - 1) / slots128) * (79 * nk + 650) <
+                      (double)((est128 + slots128 - 1) / slots128) * (narrow_step * nk + 650) <
                           (double)((est256 + cus - 1) / cus) * (133 * nk + 1650);
   out->small = avg <= SMALL_TILE && tiles128 <= (layout == NT ? cus : cus / 4);
   if (out->small) {

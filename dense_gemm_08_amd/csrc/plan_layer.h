@@ -66,9 +66,12 @@ dense_gemm_status layer_plan(int layout, int64_t M, int64_t N, int64_t K, const 
                              int64_t lda, const void* B, int64_t ldb, int64_t cus, CallPlan* cp);
 
 // The plan of a grouped call whose arguments passed layer_validate.
+// narrow_step: the estimated time of a K step of a round of 128 x 128 tiles, in
+// 0.01 us.
+constexpr int64_t kNarrowStep = 79, kNarrowStepI8 = 110;
 dense_gemm_status grouped_plan(int layout, int64_t M, int64_t N, int64_t K, const void* A,
                                int64_t lda, const void* B, int64_t ldb, const dense_gemm_groups& g,
-                               int64_t cus, GroupedPlan* out);
+                               int64_t cus, GroupedPlan* out, int64_t narrow_step = kNarrowStep);
 
 dense_gemm_status tn_validate(int fmt, int64_t M, int64_t N, int64_t K, const void* A, int64_t lda,
                               const void* B, int64_t ldb, const void* D, int64_t ldd,

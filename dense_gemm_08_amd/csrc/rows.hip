@@ -12,7 +12,9 @@ namespace {
 // f(W) for rows shared by W lanes.
 template <typename Launch>
 void by_lanes(int lanes, Launch&& launch) {
-  if (lanes == 64)
+  if (lanes == 16)
+    launch(std::integral_constant<int, 16>());
+  else if (lanes == 64)
     launch(std::integral_constant<int, 64>());
   else if (lanes == 256)
     launch(std::integral_constant<int, 256>());
@@ -40,7 +42,7 @@ template <typename T>
 dense_gemm_status run_combine_grad(const CombineGradParams& p, int lanes, hipStream_t stream) {
   by_lanes(lanes, [&](auto w) {
     constexpr int W = decltype(w)::value;
-    hipLaunchKernelGGL((combine_rows_grad<T, W>), dim3(row_grid(p.count, rows_per_block<W>())),
+    hipLaunchKernelGGL((combine_rows_grad<T, W>), dim3(row_grid(p.count * p.k, rows_per_block<W>())),
                        dim3(row_threads<W>()), 0, stream, p);
   });
   return launched();
@@ -110,7 +112,7 @@ dense_gemm_status dense_gemm_combine_grad(int fmt, int64_t T, int64_t N, int64_t
   const CombineGradParams p = {(const uint16_t*)DY, (const uint16_t*)H, (const int32_t*)places,
                                (const float*)weights, (uint16_t*)DH, (float*)dweights, lddy, ldh, lddh, T,
                                h_rows, (int)N, (int)k};
-  const int lanes = row_lanes(T, N, cus);
+  const int lanes = row_lanes(T * k, N, cus);
   return fmt == DENSE_GEMM_BF16 ? run_combine_grad<__bf16>(p, lanes, stream)
                                 : run_combine_grad<_Float16>(p, lanes, stream);
 }

@@ -5,8 +5,8 @@
 //
 // All of them move every element once, and memory bounds them: a lane takes
 // eight neighbouring 16-bit elements at a time (16-byte accesses at any
-// alignment) and a row is shared by 64, 256 or 1024 lanes, by its length and
-// by the number of rows.
+// alignment) and a row is shared by 16, 64, 256 or 1024 lanes, by its length
+// and by the number of rows.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -40,7 +40,7 @@ __device__ __forceinline__ void for_rows(int64_t count, Body&& body) {
 // x of the W lanes that share a row, combined by op; scratch: one X per wave.
 template <int W, typename X, typename Op>
 __device__ __forceinline__ X reduce_row(X x, X* scratch, Op&& op) {
-  x = reduce_lanes<64>(x, op);
+  x = reduce_lanes<W == 16 ? 16 : 64>(x, op);
   if constexpr (W > 64) {
     const int wave = (int)threadIdx.x >> 6;
     if ((threadIdx.x & 63) == 0) scratch[wave] = x;
@@ -118,14 +118,12 @@ __device__ __forceinline__ void quantize_row(const QuantizeParams& p, int64_t ro
   const bool finite = top < INF;
   const float most = finite ? unpack<T>(top, 0) : 0.0f;
   if (lane == 0) p.S[row] = finite ? most / 127.0f : __builtin_nanf("");
-  // x and m brought to m in [1/2, 1), by two powers of two: one alone may
-  // overflow
-  const int ex = __builtin_amdgcn_frexp_expf(most);
-  const float c0 = __builtin_ldexpf(1.0f, -(ex / 2));
-  const float c1 = __builtin_ldexpf(127.0f, -(ex - ex / 2));
-  const float unit = most > 0.0f ? __builtin_ldexpf(most, -ex) : 1.0f;
-  const float inverse = 1.0f / unit;
-  const float keep = most > 0.0f ? c0 : 0.0f;
+  // Rows whose largest value is far from 1 are brought nearer by a power of two
+  // (127 x, 1 / m and the remainder then neither overflow nor vanish; what falls
+  // below FP32's smallest is far below m / 254).
+  const bool far = most != 0.0f && !(most > 0x1p-64f && most < 0x1p64f);
+  const float pull = far ? (most < 1.0f ? 0x1p64f : 0x1p-64f) : 1.0f;
+  const float m1 = most > 0.0f ? most * pull : 1.0f, inverse = 1.0f / m1;
   int8_t* dst = p.Q + row * p.ldq;
   for (int64_t first = 0; first < p.K; first += SPAN) {
     if (p.K > SPAN) load(first);
@@ -133,12 +131,19 @@ __device__ __forceinline__ void quantize_row(const QuantizeParams& p, int64_t ro
     for (int c = 0; c < ROW_CHUNKS; ++c) {
       const int64_t k = first + (c * W + lane) * 8;
       if (k >= p.K) break;
+      float x[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[e] = unpack<T>(v[c][e >> 1], e & 1);
+      if (far || !finite) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = finite ? x[e] * pull : 0.0f;
+      }
       uint32_t b[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const float x = finite ? unpack<T>(v[c][e >> 1], e & 1) * keep * c1 : 0.0f;
-        float q = x * inverse;
-        q = fmaf(fmaf(-q, unit, x), inverse, q);
+        const float y = x[e] * 127.0f;
+        float q = y * inverse;
+        q = fmaf(fmaf(-q, m1, y), inverse, q);
         // (the sum with 1.5 * 2^23 is rounded to a whole number, which its low
         // byte holds)
         b[e] = __builtin_bit_cast(uint32_t, q + 12582912.0f);
@@ -151,7 +156,7 @@ __device__ __forceinline__ void quantize_row(const QuantizeParams& p, int64_t ro
         o[h] = lo | hi;
       }
       if (k + 8 <= p.K) {
-        *(u32x2_byte*)(dst + k) = o;
+        __builtin_nontemporal_store(o, (u32x2_byte*)(dst + k));
       } else {
 #pragma unroll
         for (int e = 0; e < 8; ++e)
@@ -243,73 +248,58 @@ struct CombineGradParams {
   int N, k;
 };
 
-constexpr int COMBINE_MOST = 64;  // choices of a token
-
 // DH[places[t][j]] = w[t][j] DY[t] and dweights[t][j] = DY[t] . H[places[t][j]],
-// the products' sums in FP32 in a fixed order.  DY's row stays in registers
-// over the choices (a longer row is taken in segments).
+// the products' sums in FP32 in a fixed order.  W lanes take one choice (t, j);
+// those of a token run side by side and share its row of DY in the caches.  (With
+// the row in registers over a loop of the token's choices, each choice waits for
+// the last one's sum: 4096 tokens, 8 choices of 2048 columns, 78 us, 56 so.)
 template <typename T, int W>
-__device__ __forceinline__ void combine_row_grad(const CombineGradParams& p, int64_t t,
-                                                 float (*sums)[COMBINE_MOST]) {
-  constexpr int SPAN = W * ROW_CHUNKS * 8, WAVES_ROW = W / 64;
-  const int lane = (int)threadIdx.x & (W - 1), wave = (int)threadIdx.x >> 6;
-  const bool live = t < p.count;
-  const int32_t* places = p.places + (live ? t : 0) * p.k;
-  const uint16_t* dy = p.DY + (live ? t : 0) * p.lddy;
-  for (int64_t first = 0; first < p.N; first += SPAN) {
-    uint32_t v[ROW_CHUNKS][4];
+__device__ __forceinline__ void combine_choice_grad(const CombineGradParams& p, int64_t choice, float* scratch) {
+  constexpr int SPAN = W * ROW_CHUNKS * 8;
+  const int lane = (int)threadIdx.x & (W - 1);
+  const bool live = choice < p.count * p.k;
+  const int64_t t = live ? (uint32_t)choice / (uint32_t)p.k : 0;  // (choices number less than 2^31)
+  const int64_t at = live ? p.places[choice] : -1;
+  const bool there = at >= 0 && at < p.h_rows;
+  const float w = there && p.weights != nullptr ? p.weights[choice] : 1.0f;
+  const uint16_t* dy = p.DY + t * p.lddy;
+  const uint16_t* h = p.H + (there ? at : 0) * p.ldh;
+  uint16_t* dh = p.DH + (there ? at : 0) * p.lddh;
+  float s = 0.0f;
+  for (int64_t first = 0; there && first < p.N; first += SPAN) {
+    uint32_t v[ROW_CHUNKS][4], x[ROW_CHUNKS][4];
 #pragma unroll
     for (int c = 0; c < ROW_CHUNKS; ++c) {
       const int64_t col = first + (c * W + lane) * 8;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) v[c][e] = 0u;
-      if (live && col < p.N) load_row<4>(dy, (int)col, p.N, v[c]);
-    }
-    for (int j = 0; j < p.k; ++j) {
-      const int64_t at = live ? places[j] : -1;
-      const bool there = at >= 0 && at < p.h_rows;
-      const float w = there && p.weights != nullptr ? p.weights[t * p.k + j] : 1.0f;
-      float s = 0.0f;
-      if (there) {
-#pragma unroll
-        for (int c = 0; c < ROW_CHUNKS; ++c) {
-          const int64_t col = first + (c * W + lane) * 8;
-          if (col >= p.N) break;
-          if (p.dweights != nullptr) {
-            uint32_t x[4];
-            load_row<4>(p.H + at * p.ldh, (int)col, p.N, x);
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-              s = fmaf(unpack<T>(v[c][e >> 1], e & 1), unpack<T>(x[e >> 1], e & 1), s);
-          }
-          if (p.DH != nullptr) {
-            uint32_t o[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              o[e] = pack2<T>(w * unpack<T>(v[c][e], 0), w * unpack<T>(v[c][e], 1));
-            store_row<4>(p.DH + at * p.lddh, (int)col, p.N, o);
-          }
-        }
+      for (int e = 0; e < 4; ++e) v[c][e] = x[c][e] = 0u;
+      if (col < p.N) {
+        load_row<4>(dy, (int)col, p.N, v[c]);
+        if (p.dweights != nullptr) load_row<4>(h, (int)col, p.N, x[c]);
       }
-      s = sum_lanes<64>(s);
-      if ((lane & 63) == 0) sums[wave][j] = (first == 0 ? 0.0f : sums[wave][j]) + s;
+    }
+#pragma unroll
+    for (int c = 0; c < ROW_CHUNKS; ++c) {
+      const int64_t col = first + (c * W + lane) * 8;
+      if (p.DH != nullptr && col < p.N) {
+        uint32_t o[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[e] = pack2<T>(w * unpack<T>(v[c][e], 0), w * unpack<T>(v[c][e], 1));
+        store_row<4>(dh, (int)col, p.N, o);
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        s = fmaf(unpack<T>(v[c][e >> 1], e & 1), unpack<T>(x[c][e >> 1], e & 1), s);
     }
   }
   if (p.dweights == nullptr) return;
-  __syncthreads();
-  if (live)
-    for (int j = lane; j < p.k; j += W) {
-      float s = 0.0f;
-#pragma unroll
-      for (int w = 0; w < WAVES_ROW; ++w) s += sums[wave / WAVES_ROW * WAVES_ROW + w][j];
-      p.dweights[t * p.k + j] = s;
-    }
-  __syncthreads();
+  s = reduce_row<W>(s, scratch, [](float a, float b) { return a + b; });
+  if (live && lane == 0) p.dweights[choice] = s;
 }
 template <typename T, int W>
 __global__ __launch_bounds__(row_threads<W>()) void combine_rows_grad(CombineGradParams p) {
-  __shared__ float sums[row_threads<W>() / 64][COMBINE_MOST];
-  for_rows<W>(p.count, [&](int64_t t) { combine_row_grad<T, W>(p, t, sums); });
+  __shared__ float scratch[W > 64 ? W / 64 : 1];
+  for_rows<W>(p.count * p.k, [&](int64_t choice) { combine_choice_grad<T, W>(p, choice, scratch); });
 }
 
 }  // namespace dg
