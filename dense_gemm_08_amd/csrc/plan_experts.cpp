@@ -3,7 +3,7 @@
 // no device code, so it also builds with the host sanitizers.
 #include "plan_experts.h"
 
-#include <cmath>
+#include <initializer_list>
 
 namespace dg {
 
