@@ -422,11 +422,11 @@ def _torch():
     return _module
 
 
-def _check_like(t, dtype, dev: int, dims: int, what: str, shape=None):
+def _check_like(t, dtype, dev: int, dims: int, what: str, shape=None, like=" like A"):
     """A tensor of this type on device number ``dev``, with ``dims``
     dimensions, a unit last stride and (where given) this shape."""
     if t.dtype is not dtype:
-        raise TypeError("%s must be %s like A, got %s" % (what, dtype, t.dtype))
+        raise TypeError("%s must be %s%s, got %s" % (what, dtype, like, t.dtype))
     if t.get_device() != dev:
         raise ValueError("operands on different devices: A on cuda:%d, %s on %s"
                          % (dev, what, t.device))
@@ -698,7 +698,7 @@ def _check_rows(t, dtype, dev: int, shape, what: str):
         ld, one = t.stride()
         if one == 1:
             return ld if shape[0] > 1 else max(shape[1], 1)
-    _check_like(t, dtype, dev, 2, what, shape)
+    _check_like(t, dtype, dev, 2, what, shape, "")
     return _ld(t)
 
 
@@ -741,6 +741,9 @@ def _i8(A, SA, B, SB, ends, bias, act, residual, preact, D, dtype, stream, works
         dtype = D.dtype
     elif dtype is None:
         dtype = torch.bfloat16
+        for t in (bias, residual, preact):
+            if t is not None:
+                dtype = t.dtype
     fmt = _FMTS.get(dtype)
     if fmt is None:
         raise TypeError("D must be float16 or bfloat16, got %s" % dtype)
@@ -760,7 +763,7 @@ def _i8(A, SA, B, SB, ends, bias, act, residual, preact, D, dtype, stream, works
     if code or bias is not None or residual is not None or preact is not None:
         epi = Epilogue(act=code)
         if bias is not None:
-            _check_like(bias, dtype, dev, 1 + len(G), "bias", G + (N,))
+            _check_like(bias, dtype, dev, 1 + len(G), "bias", G + (N,), " like D")
             epi.bias = bias.data_ptr()
             if G and G[0] > 1:
                 epi.bias_stride = bias.stride(0)
@@ -791,7 +794,8 @@ def gemm_nt_i8(A, SA, B, SB, bias=None, act="none", residual=None, preact=None, 
     """D = act(Z) + residual with Z = (A @ B.T) * SA[:, None] * SB + bias: A
     (M x K) and B (N x K) int8, SA (M) and SB (N) float32, the product exact in
     32-bit integers, the rest in FP32 with one rounding.  D, bias, residual and
-    preact are float16 or bfloat16 (``dtype``, or D's; bfloat16 by default).
+    preact are all float16 or all bfloat16 (``dtype``, where none of them says;
+    bfloat16 by default).
     K at most 131071.  Other arguments as for :func:`gemm_nt_fused`
     (``workspace``: dense_gemm_i8_workspace_size bytes)."""
     return _i8(A, SA, B, SB, None, bias, act, residual, preact, D, dtype, stream, workspace)

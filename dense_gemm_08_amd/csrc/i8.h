@@ -56,9 +56,13 @@ __device__ __forceinline__ void mfma16<I8<__bf16>>(f32x4& c, u32x4 a, u32x4 b) {
   asm("v_mfma_i32_16x16x64_i8 %0, %1, %2, %0" : "+a"(c) : "v"(a), "v"(b));
 }
 
-// A sum (its bits in a float register) times its two scales.
-__device__ __forceinline__ float scaled(float sum_bits, float sa, float sb) {
-  return (float)__builtin_bit_cast(int, sum_bits) * sa * sb;
+// A sum times its two scales.  The products are not fused with the addition that
+// follows: every kernel rounds alike, so a row's results do not depend on the
+// tiles that a call takes.
+__device__ __forceinline__ float scaled(int sum, float sa, float sb) {
+#pragma clang fp contract(off)
+  const float x = (float)sum * sa;
+  return x * sb;
 }
 
 // C scales of consecutive columns from column col of `cols` on; zeros past it.

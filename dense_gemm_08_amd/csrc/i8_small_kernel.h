@@ -188,7 +188,7 @@ __global__ __launch_bounds__(SMALL_THREADS) void gemm_small_i8(SmallI8Params p) 
   load_scales(p.s.b + group * p.s.b_stride, col, p.N, sb);
   const float sa = p.s.a[row];
 #pragma unroll
-  for (int k = 0; k < 4; ++k) x[0][k] = (float)s[k] * sa * sb[k];
+  for (int k = 0; k < 4; ++k) x[0][k] = scaled(s[k], sa, sb[k]);
   finish_row<O>(p.e, group, row, col, p.N, x);
   const uint32_t o[2] = {pack2<O>(x[0][0], x[0][1]), pack2<O>(x[0][2], x[0][3])};
   store_row<2>(p.D + (int64_t)row * p.ldd, col, p.N, o);
@@ -229,7 +229,7 @@ __global__ __launch_bounds__(I8_REDUCE_THREADS) void split_reduce_i8(I8ReducePar
   load_scales(p.s.b, col, p.N, sb);
   const float sa = p.s.a[row];
 #pragma unroll
-  for (int k = 0; k < 8; ++k) x[0][k] = (float)(k < 4 ? lo[k & 3] : hi[k & 3]) * sa * sb[k];
+  for (int k = 0; k < 8; ++k) x[0][k] = scaled(k < 4 ? lo[k & 3] : hi[k & 3], sa, sb[k]);
   finish_row<O>(p.e, 0, row, col, p.N, x);
   uint32_t o[4];
 #pragma unroll

@@ -703,7 +703,7 @@ __global__ __launch_bounds__(THREADS, (per_cu<SPLIT, TN, TM>())) void layer_gemm
 #pragma unroll
             for (int t = 0; t < R; ++t)
 #pragma unroll
-              for (int k = 0; k < 8; ++k) v[t][k] = scaled(v[t][k], sa[t], sb[k]);
+              for (int k = 0; k < 8; ++k) v[t][k] = scaled(__builtin_bit_cast(int, v[t][k]), sa[t], sb[k]);
           }
 #pragma unroll
           for (int t = 0; t < R; ++t)
