@@ -10,7 +10,6 @@
 #include <stdint.h>
 
 #include <type_traits>
-#include <utility>
 
 namespace dg {
 
@@ -96,19 +95,70 @@ __device__ __forceinline__ X sum_lanes(X x) {
   return reduce_lanes<L>(x, [](X a, X b) { return a + b; });
 }
 
-// x of the lane N places back in its row of 16, counted around.
-template <int N, typename X>
-__device__ __forceinline__ X rotated(X x) {
-  return dpp_move<0x120 + N>(x);
+// The sum of x over the lanes before this one in its row of 16.
+__device__ __forceinline__ int sum_before(int x) {
+  int s = x;
+  s += __builtin_amdgcn_update_dpp(0, s, 0x111, 0xf, 0xf, true);  // row_shr 1, 2, 4, 8
+  s += __builtin_amdgcn_update_dpp(0, s, 0x112, 0xf, 0xf, true);
+  s += __builtin_amdgcn_update_dpp(0, s, 0x114, 0xf, 0xf, true);
+  s += __builtin_amdgcn_update_dpp(0, s, 0x118, 0xf, 0xf, true);
+  return s - x;
 }
-// f(std::integral_constant<int, N>) for N = 1 .. 15.
-template <typename F, int... N>
-__device__ __forceinline__ void for_others(F&& f, std::integer_sequence<int, N...>) {
-  (f(std::integral_constant<int, N + 1>()), ...);
+// x of the next lane of the row; 0 in its last.
+__device__ __forceinline__ uint32_t from_next(uint32_t x) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x101, 0xf, 0xf, true);  // row_shl 1
 }
-template <typename F>
-__device__ __forceinline__ void for_others(F&& f) {
-  for_others(f, std::make_integer_sequence<int, 15>());
+
+template <int CTRL>
+__device__ __forceinline__ uint64_t dpp_move(uint64_t x) {
+  return dpp_move<CTRL>((uint32_t)x) | ((uint64_t)dpp_move<CTRL>((uint32_t)(x >> 32)) << 32);
+}
+
+// The values of a row of 16 lanes in descending order, by a bitonic network: in
+// each step a lane and its partner keep the larger value in the lower one of
+// them (BIT: the bit of the lane that says which it is).
+template <int CTRL, int BIT, typename X>
+__device__ __forceinline__ X sort_step(X x, int lane) {
+  const X y = dpp_move<CTRL>(x);
+  if constexpr (sizeof(X) == 4) {
+    return lane & BIT ? min(x, y) : max(x, y);
+  } else {
+    return (y > x) != ((lane & BIT) != 0) ? y : x;
+  }
+}
+template <typename X>
+__device__ __forceinline__ X sort_step_4(X x, int lane) {  // (lanes that differ in bit 2)
+  const X y = dpp_move<0x1B>(dpp_move<0x141>(x));
+  if constexpr (sizeof(X) == 4) {
+    return lane & 4 ? min(x, y) : max(x, y);
+  } else {
+    return (y > x) != ((lane & 4) != 0) ? y : x;
+  }
+}
+template <typename X>
+__device__ __forceinline__ X sorted_in_row(X x) {
+  const int lane = (int)threadIdx.x & 15;
+  x = sort_step<0xB1, 1>(x, lane);
+  x = sort_step<0x1B, 2>(x, lane);
+  x = sort_step<0xB1, 1>(x, lane);
+  x = sort_step<0x141, 4>(x, lane);
+  x = sort_step<0x4E, 2>(x, lane);
+  x = sort_step<0xB1, 1>(x, lane);
+  x = sort_step<0x140, 8>(x, lane);
+  x = sort_step_4(x, lane);
+  x = sort_step<0x4E, 2>(x, lane);
+  return sort_step<0xB1, 1>(x, lane);
+}
+// The 16 largest of two such rows, again in order.
+template <typename X>
+__device__ __forceinline__ X merged_in_row(X x, X y) {
+  const int lane = (int)threadIdx.x & 15;
+  const X z = dpp_move<0x140>(y);
+  x = z > x ? z : x;
+  x = sort_step<0x128, 8>(x, lane);  // row_ror 8
+  x = sort_step_4(x, lane);
+  x = sort_step<0x4E, 2>(x, lane);
+  return sort_step<0xB1, 1>(x, lane);
 }
 
 // Values that lanes of this wave left in LDS for each other: the accesses after

@@ -86,8 +86,9 @@ dense_gemm_status route_grad_validate(int fmt, int64_t T, int64_t E, int64_t k, 
 
 // Up to ROUTE_ALONE tokens one block makes the choice and the dispatch; beyond,
 // blocks of 64 tokens (more where they would number over ROUTE_BLOCKS: every
-// block of the second launch reads all blocks' counts).
-constexpr int64_t ROUTE_ALONE = 128, ROUTE_BLOCKS = 512;
+// block of the second launch reads all blocks' counts; but less than 2^16, which
+// those hold).
+constexpr int64_t ROUTE_ALONE = 128, ROUTE_BLOCKS = 512, ROUTE_CHUNKS = 1000;
 RoutePlan route_plan(int64_t T, int64_t E) {
   RoutePlan p;
   const int64_t chunks = (T + 63) / 64;
@@ -98,8 +99,9 @@ RoutePlan route_plan(int64_t T, int64_t E) {
     return p;
   }
   p.chunks = (chunks + ROUTE_BLOCKS - 1) / ROUTE_BLOCKS;
+  if (p.chunks > ROUTE_CHUNKS) p.chunks = ROUTE_CHUNKS;
   p.blocks = (chunks + p.chunks - 1) / p.chunks;
-  p.bytes = (size_t)((p.blocks * E * 4 + 255) & ~(int64_t)255);
+  p.bytes = (size_t)((p.blocks * ((E + 1) / 2) * 4 + 255) & ~(int64_t)255);
   return p;
 }
 

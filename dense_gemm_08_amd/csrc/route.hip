@@ -92,7 +92,7 @@ dense_gemm_status dense_gemm_route(int fmt, int64_t T, int64_t E, int64_t k, con
   p.places = (int32_t*)places;
   p.ends = (int32_t*)ends;
   p.tokens = (int32_t*)tokens;
-  p.counts = plan.blocks > 1 ? (int32_t*)workspace : nullptr;
+  p.counts = plan.blocks > 1 ? (uint32_t*)workspace : nullptr;
   p.groups = routing->groups;
   p.group_size = (int)(E / routing->groups);
   p.top_groups = routing->top_groups;
@@ -102,9 +102,11 @@ dense_gemm_status dense_gemm_route(int fmt, int64_t T, int64_t E, int64_t k, con
   // (up to 1024 experts, a group of m: e (2^20 + m) / m 2^-20 exceeds e / m by
   // less than 1 / m)
   p.group_inverse = (int)(((1 << 20) + p.group_size - 1) / p.group_size);
-  const int lanes = E <= 256 ? 16 : 64;
-  p.group_lanes = 1;
-  while (p.group_lanes < 16 && 2 * p.group_lanes * p.groups <= lanes) p.group_lanes *= 2;
+  for (int wide = 0; wide < 2; ++wide) {
+    int& n = p.group_lanes[wide];
+    n = 1;
+    while (n < 16 && 2 * n * p.groups <= (wide ? 64 : 16)) n *= 2;
+  }
   p.k_inverse = (int)(((1 << 20) + k - 1) / k);
   p.chunks = (int)plan.chunks;
   if (fmt == DENSE_GEMM_F32) return run_route<float>(p, plan, stream);

@@ -37,14 +37,14 @@ struct RouteParams {
   int32_t* places;     // T x k
   int32_t* ends;       // E
   int32_t* tokens;     // T k
-  int32_t* counts;     // choices per block and expert (null: one block)
+  uint32_t* counts;    // choices per block and expert, two in a word (null: one block)
   int64_t ld;
   int T, E, k;
   int sigmoid, renorm;
   float scale;
   int ranked;          // no bias: the logits rank the experts
   int groups, group_size, top_groups, group_top;
-  int group_lanes;     // lanes that look for a group's best: a power of two
+  int group_lanes[2];  // lanes of 16, of 64, that look for a group's best: powers of two
   int group_inverse;   // ceil(2^20 / group_size): e * that >> 20 is e's group
   int k_inverse;       // ceil(2^20 / k): i * that >> 20 is i / k for i < 64 k
   int chunks;          // chunks of 64 tokens per block
@@ -92,10 +92,12 @@ __device__ __forceinline__ float top_logit(const RouteParams& p, const float (&l
 
 // The scores of a token's experts plus their bias, -inf where one cannot be
 // chosen; with the logits themselves where these decide (RouteParams::ranked).
-// Returns by how much two of them have to differ, next to 2^-22 of their size,
-// for their order to be sure (sums of two: by twice as much): in 32 bits a
-// logistic's error is below 2^-22, a softmax's 2^-18 of the largest (the sum's,
-// above all), the bias's sum rounds by 2^-24, and a difference has two of each.
+// Returns by how much two of them have to differ, next to 2^-23 of their size,
+// for their order to be sure (sums of two: by twice as much, next to 2^-21): in
+// 32 bits a logistic's error is below 2^-22 (its exponential's, at most 2^-24, the
+// reciprocal's 2^-23, the sum's 2^-24), a softmax's 2^-18 of the largest (its
+// sum's, above all), the bias's sum rounds by 2^-24 of it, and a difference has
+// two of each.
 template <typename X, int L, int PER>
 __device__ __forceinline__ X choice_scores(const RouteParams& p, const float (&l)[PER], int lane,
                                            float top, X (&c)[PER]) {
@@ -107,7 +109,7 @@ __device__ __forceinline__ X choice_scores(const RouteParams& p, const float (&l
   }
   constexpr bool FAST = sizeof(X) == 4;
   constexpr float L2E = 1.44269504088896341f;
-  X near = (X)0x1p-20;
+  X near = (X)0x1p-21;
   if (!p.sigmoid) {
     X sum = 0;
 #pragma unroll
@@ -117,7 +119,7 @@ __device__ __forceinline__ X choice_scores(const RouteParams& p, const float (&l
       else
         c[i] = exp((X)l[i] - (X)top);
       sum += c[i];
-      if constexpr (!FAST) fence();  // (one after the other: they take many registers)
+      if constexpr (!FAST && PER > 4) fence();  // (one after the other: they take many registers)
     }
     const X part = 1 / sum_lanes<L>(sum);
 #pragma unroll
@@ -133,7 +135,7 @@ __device__ __forceinline__ X choice_scores(const RouteParams& p, const float (&l
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
       c[i] = 1 / (1 + exp(-(X)l[i]));
-      fence();
+      if constexpr (PER > 4) fence();
     }
   }
 #pragma unroll
@@ -146,9 +148,8 @@ __device__ __forceinline__ X choice_scores(const RouteParams& p, const float (&l
 }
 
 // 32-bit values as whole numbers in the same order (no NaN; both zeros alike),
-// which the lanes compare and combine in fewer instructions; and back.
+// and back.
 constexpr int KEY_NONE = (int)0x807fffff;  // -inf
-constexpr int KEY_PAD = -0x7fffffff;       // below all values
 __device__ __forceinline__ int key_of(float x) {
   const int b = __builtin_bit_cast(int, x + 0.0f);
   return b ^ ((b >> 31) & 0x7fffffff);
@@ -156,24 +157,43 @@ __device__ __forceinline__ int key_of(float x) {
 __device__ __forceinline__ float value_of(int key) {
   return __builtin_bit_cast(float, key ^ ((key >> 31) & 0x7fffffff));
 }
-
-// How many of a row's 16 keys go before this lane's: the larger ones, and of
-// equal ones those of lower lanes.
-__device__ __forceinline__ int rank_in_row(int key) {
-  const int lane = (int)threadIdx.x & 15;
-  int rank = 0;
-  for_others([&](auto n) {
-    constexpr int N = decltype(n)::value;
-    // (the key comes from lane - N, a lower one unless that counts around)
-    rank += rotated<N>(key) > (lane >= N ? key - 1 : key) ? 1 : 0;
-  });
-  return rank;
+// A value and its index as one number: the larger of two stands for the larger
+// value, of equal ones for the lower index.  0 is none (and -inf none).
+__device__ __forceinline__ uint64_t ranked_pair(float x, int index) {
+  const int key = key_of(x);
+  return key > KEY_NONE ? ((uint64_t)((uint32_t)key ^ 0x80000000u) << 32) | ~(uint32_t)index : 0;
 }
+__device__ __forceinline__ float pair_value(uint64_t pair) {
+  return pair != 0 ? value_of((int)((uint32_t)(pair >> 32) ^ 0x80000000u)) : -__builtin_inff();
+}
+__device__ __forceinline__ int pair_index(uint64_t pair) { return (int)~(uint32_t)pair; }
+
 // The 16 bits of a wave's ballot that are this lane's row's.
 __device__ __forceinline__ uint32_t row_bits(uint64_t ballot) {
   const int lane = (int)threadIdx.x & 63;
   const uint32_t half = lane < 32 ? (uint32_t)ballot : (uint32_t)(ballot >> 32);
   return lane & 16 ? half >> 16 : half & 0xffffu;
+}
+// x of lane n of this lane's row.
+__device__ __forceinline__ int in_row(int x, int n) {
+  return __builtin_amdgcn_ds_bpermute((((int)threadIdx.x & 48) | n) << 2, x);
+}
+__device__ __forceinline__ uint64_t in_row(uint64_t x, int n) {
+  return (uint32_t)in_row((int)(uint32_t)x, n) | ((uint64_t)(uint32_t)in_row((int)(uint32_t)(x >> 32), n) << 32);
+}
+
+// The larger of two numbers (32 bits: in one instruction, by the median with
+// infinity), and the two largest of three.
+__device__ __forceinline__ float larger_of(float a, float b) {
+  return __builtin_amdgcn_fmed3f(a, b, __builtin_inff());
+}
+__device__ __forceinline__ void take_top(float x, float& first, float& second) {
+  second = __builtin_amdgcn_fmed3f(x, first, second);
+  first = larger_of(first, x);
+}
+__device__ __forceinline__ void take_top(double x, double& first, double& second) {
+  second = fmax(second, fmin(first, x));
+  first = fmax(first, x);
 }
 
 // Whether a, the larger, is not surely larger than b; size: that of what they
@@ -181,40 +201,36 @@ __device__ __forceinline__ uint32_t row_bits(uint64_t ballot) {
 template <typename X>
 __device__ __forceinline__ bool too_close(X a, X b, X near, X size) {
   if (sizeof(X) == 8 || !(b > -(X)__builtin_inff())) return false;
-  return !(a - b > near + (X)0x1p-22 * size);  // (so is a difference that is no number)
+  return !(a - b > near + (X)0x1p-23 * size);  // (so is a difference that is no number)
 }
 
 // Takes the experts outside the best groups from c.  `lds`: E values of this
-// token's.  Returns whether rounding could change that.
+// token's, which receive c as it was.  Returns whether rounding could change
+// that.
 template <typename X, int L, int PER>
 __device__ __forceinline__ bool limit_groups(const RouteParams& p, int lane, X near, X* lds, X (&c)[PER]) {
   const X NONE = -(X)__builtin_inff();
 #pragma unroll
-  for (int i = 0; i < PER; ++i)
-    if (i * L + lane < p.E) lds[i * L + lane] = c[i];
+  for (int i = 0; i < PER; ++i) lds[i * L + lane] = c[i];
   wave_lds_order();
   // A group's two best, found by `share` neighbouring lanes (up to 16, a power
   // of two) where there are no more groups than lanes; else several groups a
   // lane.
   constexpr int GS = (ROUTE_MOST_GROUPS + L - 1) / L;
   X value[GS], size = 0;
-  const int share = p.group_lanes;
+  const int share = p.group_lanes[L == 64];
 #pragma unroll
   for (int n = 0; n < GS; ++n) {
     const int g = n * L + lane / share;
     X first = NONE, second = NONE;
     if (g < p.groups) {
       const X* from = lds + g * p.group_size;
-#pragma unroll 4
-      for (int i = lane & (share - 1); i < p.group_size; i += share) {
-        const X x = from[i];
-        second = fmax(second, fmin(first, x));
-        first = fmax(first, x);
-      }
+#pragma unroll 8
+      for (int i = lane & (share - 1); i < p.group_size; i += share) take_top(from[i], first, second);
     }
     auto join = [&](X f, X s) {
-      second = fmax(fmin(first, f), fmax(second, s));
-      first = fmax(first, f);
+      take_top(f, first, second);
+      second = fmax(second, s);
     };
     if (share > 1) join(dpp_move<0xB1>(first), dpp_move<0xB1>(second));
     if (share > 2) join(dpp_move<0x4E>(first), dpp_move<0x4E>(second));
@@ -225,57 +241,60 @@ __device__ __forceinline__ bool limit_groups(const RouteParams& p, int lane, X n
     if (first > NONE) size = fmax(size, fmax(fabs(first), two ? fabs(second) : (X)0));
     if (share > 1) break;
   }
+  const bool exact = sizeof(X) == 8 || (p.ranked && p.group_top == 1);
+  if (!exact) size = max_lanes<L>(size);
   bool unsure = false;
-  if (p.ranked && p.group_top == 1) near = size = 0;
-  const bool exact = p.ranked && p.group_top == 1;
-  size = max_lanes<L>(size);
-  uint64_t stays = 0;  // bit (group * share)
-  if (sizeof(X) == 4 && L == 16 && p.groups <= 16) {
-    // the groups ranked all at once, each by the first of its lanes
-    const bool first = (lane & (share - 1)) == 0;
-    const int key = first ? key_of((float)value[0]) : KEY_PAD;
-    const int rank = rank_in_row(key);
-    const bool stay = first && key > KEY_NONE && rank < p.top_groups;
-    stays = row_bits(__ballot(stay));
-    const int least = min_lanes<16>(stay ? key : 0x7fffffff);
-    const int next = max_lanes<16>(stay ? KEY_PAD : key);
-    if (!exact && next > KEY_NONE) unsure = too_close((X)value_of(least), (X)value_of(next), 2 * near, 4 * size);
-  } else {
-    X least = 0;
-    for (int n = 0; n <= p.top_groups; ++n) {
-      X m = value[0];
-      int at = lane / share;
+  if constexpr (sizeof(X) == 4 && L == 16) {
+    if (p.groups <= 16) {
+      // the groups put in order all at once, each by the first of its lanes
+      const uint64_t own = (lane & (share - 1)) == 0 ? ranked_pair(value[0], lane) : 0;
+      const uint64_t order = sorted_in_row(own);
+      const uint64_t last = in_row(order, p.top_groups - 1), next = in_row(order, p.top_groups);
+      const uint32_t stays = row_bits(__ballot(own != 0 && own >= last));  // bit (group * share)
+      if (!exact) unsure = too_close(pair_value(last), pair_value(next), 2 * near, 4 * size);
+      auto keep = [&](int i, int g) {
+        const int stay = (int)(stays << (31 - g * share)) >> 31;  // all bits, or none
+        c[i] = __builtin_bit_cast(float, (__builtin_bit_cast(int, c[i]) & stay) |
+                                             (__builtin_bit_cast(int, (float)NONE) & ~stay));
+      };
+      if (p.group_size % L == 0) {  // (an element's group is the same one in all lanes)
 #pragma unroll
-      for (int i = 1; i < GS; ++i)
-        if (share == 1 && value[i] > m) {
-          m = value[i];
-          at = i * L + lane;
-        }
-      const X best = max_lanes<L>(m);
-      if (!(best > NONE)) break;
-      if (n == p.top_groups) {
-        unsure = !exact && too_close(least, best, 2 * near, 4 * size);
-        break;
+        for (int i = 0; i < PER; ++i) keep(i, min(i * L * p.group_inverse >> 20, p.groups - 1));
+      } else {
+#pragma unroll
+        for (int i = 0; i < PER; ++i) keep(i, min((i * L + lane) * p.group_inverse >> 20, p.groups - 1));
       }
-      least = best;
-      const int g = min_lanes<L>(m == best ? at : 1 << 30);
-      stays |= 1ull << (g * share & 63);
-#pragma unroll
-      for (int i = 0; i < GS; ++i)
-        if ((share > 1 ? lane / share : i * L + lane) == g) value[i] = NONE;
+      return unsure;
     }
   }
-  auto keep = [&](int i, int g) {
-    const int bit = g * share & 63;
-    const bool stay = (bit < 32 ? (uint32_t)stays : (uint32_t)(stays >> 32)) >> (bit & 31) & 1;
-    if (!stay) c[i] = NONE;
-  };
-  if (p.group_size % L == 0) {  // (an element's group is the same one in all lanes)
+  uint64_t stays = 0;
+  X least = 0;
+  for (int n = 0; n <= p.top_groups; ++n) {
+    X m = value[0];
+    int at = lane / share;
 #pragma unroll
-    for (int i = 0; i < PER; ++i) keep(i, i * L * p.group_inverse >> 20);
-  } else {
+    for (int i = 1; i < GS; ++i)
+      if (share == 1 && value[i] > m) {
+        m = value[i];
+        at = i * L + lane;
+      }
+    const X best = max_lanes<L>(m);
+    if (!(best > NONE)) break;
+    if (n == p.top_groups) {
+      unsure = !exact && too_close(least, best, 2 * near, 4 * size);
+      break;
+    }
+    least = best;
+    const int g = min_lanes<L>(m == best ? at : 1 << 30);
+    stays |= 1ull << (g & 63);
 #pragma unroll
-    for (int i = 0; i < PER; ++i) keep(i, (i * L + lane) * p.group_inverse >> 20);
+    for (int i = 0; i < GS; ++i)
+      if ((share > 1 ? lane / share : i * L + lane) == g) value[i] = NONE;
+  }
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const int g = (i * L + lane) * p.group_inverse >> 20 & 63;
+    if (!(stays >> g & 1)) c[i] = NONE;
   }
   return unsure;
 }
@@ -302,7 +321,14 @@ __device__ __forceinline__ bool pick_in_turn(const RouteParams& p, int lane, X n
     if (!p.ranked && j > 0) unsure |= too_close(before, best, near, (X)fmax(fabs(before), fabs(best)));
     before = best;
     if (j == p.k) break;
-    const int e = min_lanes<L>(m == best ? at * L + lane : 1 << 30);
+    int e;
+    const uint64_t who = __ballot(m == best);
+    if (L == 64 && __popcll(who) == 1) {  // (one lane has it)
+      const int w = __builtin_ctzll(who);
+      e = __builtin_amdgcn_readlane(at, w) * 64 + w;
+    } else {
+      e = min_lanes<L>(m == best ? at * L + lane : 1 << 30);
+    }
     if (lane == 0) sel[j] = best > NONE ? e : -1;
 #pragma unroll
     for (int i = 0; i < PER; ++i)
@@ -314,67 +340,50 @@ __device__ __forceinline__ bool pick_in_turn(const RouteParams& p, int lane, X n
 
 // The same in 32 bits for up to 15 of a row of 16 lanes, all at once: none of
 // the k + 1 best is below the (k + 1)-th largest of the lanes' maxima, and few
-// others are not (256 experts, 8 chosen: 14 expected).  These candidates are
-// gathered in LDS in the order of their index, two a lane at most, and ranked by
-// comparing each with all: about 350 instructions where 9 maxima in turn take
-// about 900.  `lds`: 64 words of this token's.  *done is false, for the whole
+// others are not (256 experts, 8 chosen: 14 expected).  These candidates' indices
+// are gathered in LDS and put in order, two a lane at most, by a bitonic network.
+// `lds`: the values c of this token, by expert.  *done is false, for the whole
 // wave, if some token has more than 32.
 template <int PER>
 __device__ __forceinline__ bool pick_at_once(const RouteParams& p, int lane, float near, const float (&c)[PER],
-                                             float* lds, int* sel, bool* done) {
-  int key[PER], m = KEY_NONE;
+                                             const float* lds, int* sel, bool* done) {
+  float m = c[0];
 #pragma unroll
-  for (int i = 0; i < PER; ++i) {
-    key[i] = key_of(c[i]);
-    m = max(m, key[i]);
-  }
-  const int limit = max(min_lanes<16>(rank_in_row(m) <= p.k ? m : 0x7fffffff), KEY_NONE + 1);
-  u32x2* cand = (u32x2*)lds;  // (key, expert)
-  cand[lane] = cand[lane + 16] = (u32x2){(uint32_t)KEY_PAD, 0u};
-  wave_lds_order();
-  const uint32_t below = (1u << lane) - 1;
-  int total = 0;
+  for (int i = 1; i < PER; ++i) m = larger_of(m, c[i]);
+  const float limit = value_of(max(in_row(sorted_in_row(key_of(m)), p.k), KEY_NONE + 1));
+  uint32_t bits = 0;
 #pragma unroll
-  for (int i = 0; i < PER; ++i) {
-    const bool is = key[i] >= limit;
-    const uint32_t row = row_bits(__ballot(is));
-    const int at = total + __popc(row & below);
-    if (is && at < 32) cand[at] = (u32x2){(uint32_t)key[i], (uint32_t)(i * 16 + lane)};
-    total += __popc(row);
-  }
+  for (int i = PER - 1; i >= 0; --i) bits = bits + bits + (c[i] >= limit ? 1 : 0);
+  const int count = __popc(bits), total = sum_lanes<16>(count);
+  int at = sum_before(count);
   *done = __ballot(total > 32) == 0;
   if (!*done) return false;
+  while (__ballot(bits != 0) != 0) {
+    if (bits != 0) {
+      sel[at++] = __builtin_ctz(bits) * 16 + lane;
+      bits &= bits - 1;
+    }
+  }
   wave_lds_order();
-  const u32x2 x = cand[lane], y = cand[lane + 16];
-  const int a = (int)x[0], b = (int)y[0];
-  int rank_a = rank_in_row(a), rank_b = 32;
+  uint64_t best = 0, more = 0;
+  if (lane < total) {
+    const int e = sel[lane];
+    best = ranked_pair(lds[e], e);
+  }
+  best = sorted_in_row(best);
   if (__ballot(total > 16) != 0) {
-    // (all of the second sixteen come after the first in the order of experts)
-    rank_a += b > a ? 1 : 0;
-    rank_b = rank_in_row(b) + (a >= b ? 1 : 0);
-    for_others([&](auto n) {
-      constexpr int N = decltype(n)::value;
-      rank_a += rotated<N>(b) > a ? 1 : 0;
-      rank_b += rotated<N>(a) >= b ? 1 : 0;
-    });
+    if (lane + 16 < total) {
+      const int e = sel[lane + 16];
+      more = ranked_pair(lds[e], e);
+    }
+    best = merged_in_row(best, sorted_in_row(more));
   }
-  // in order: the experts to sel, the keys (of which the next one counts) to lds
-  int* sorted = (int*)lds;
   wave_lds_order();
-  sorted[lane] = KEY_NONE;
-  if (lane < p.k) sel[lane] = -1;
-  wave_lds_order();
-  if (a > KEY_NONE && rank_a <= p.k) {
-    sorted[rank_a] = a;
-    if (rank_a < p.k) sel[rank_a] = (int)x[1];
-  }
-  if (b > KEY_NONE && rank_b <= p.k) {
-    sorted[rank_b] = b;
-    if (rank_b < p.k) sel[rank_b] = (int)y[1];
-  }
+  if (lane < p.k) sel[lane] = best != 0 ? pair_index(best) : -1;
   wave_lds_order();
   if (p.ranked) return false;
-  const float v = value_of(sorted[lane]), w = value_of(sorted[lane < 15 ? lane + 1 : 15]);
+  const uint64_t next = from_next((uint32_t)best) | ((uint64_t)from_next((uint32_t)(best >> 32)) << 32);
+  const float v = pair_value(best), w = pair_value(next);
   return max_lanes<16>(lane < p.k && too_close(v, w, near, fmaxf(fabsf(v), fabsf(w))) ? 1 : 0) != 0;
 }
 
@@ -530,7 +539,6 @@ __global__ __launch_bounds__(ROUTE_THREADS) void route_choose(RouteParams p) {
   // a wave's scores, by token (in 64 bits one token's)
   __shared__ __attribute__((aligned(16))) float area[WAVES_RT][(TPW < 2 ? 2 : TPW) * MOST];
   __shared__ int sel[AT_ONCE][ROUTE_MOST_K];  // the chosen, in order
-  __shared__ int again[AT_ONCE], agains;
   __shared__ uint64_t mask[MOST];
   __shared__ int32_t base[MOST], scratch[WAVES_RT];
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
@@ -538,10 +546,10 @@ __global__ __launch_bounds__(ROUTE_THREADS) void route_choose(RouteParams p) {
     base[e] = 0;
     mask[e] = 0;
   }
-  if (threadIdx.x == 0) agains = 0;
   __syncthreads();
   const int first = (int)blockIdx.x * p.chunks * 64, tokens = min(p.T - first, p.chunks * 64);
   for (int t0 = 0; t0 < tokens; t0 += AT_ONCE) {
+    uint64_t again;
     {
       // (the lane is read anew for each pass: what derives from it, biases and
       // groups among it, would otherwise be kept in registers over the loop)
@@ -562,45 +570,52 @@ __global__ __launch_bounds__(ROUTE_THREADS) void route_choose(RouteParams p) {
         }
       }
       if constexpr (L == 16) {
-        if (p.k < 16)
-          unsure |= pick_at_once<PER>(p, lane, near, c, area[wave] + sub * MOST, sel[slot], &done);
+        if (p.k < 16) {
+          float* lds = area[wave] + sub * MOST;
+          if (p.top_groups == p.groups || (p.ranked && p.group_top > 1)) {
+            wave_lds_order();
+#pragma unroll
+            for (int i = 0; i < PER; ++i) lds[i * L + lane] = c[i];
+            wave_lds_order();
+          }
+          unsure |= pick_at_once<PER>(p, lane, near, c, lds, sel[slot], &done);
+        }
       }
       if (!done) unsure |= pick_in_turn<float, L, PER>(p, lane, near, c, sel[slot]);
-      if (t < p.T) {
-        if (broken || !unsure)
-          finish_token<F, L, PER>(p, t, lane, l, top, broken, sel[slot], base);
-        else if (lane == 0)
-          again[atomicAdd(&agains, 1)] = slot;
-      }
+      unsure = unsure && !broken && t < p.T;
+      if (t < p.T && !unsure) finish_token<F, L, PER>(p, t, lane, l, top, broken, sel[slot], base);
+      again = __ballot(unsure);
     }
-    __syncthreads();
-    // the tokens whose choice 32 bits do not settle, a wave each
-    for (int i = wave; i < agains; i += WAVES_RT) {
+    // the wave's tokens whose choice 32 bits do not settle, one by one
+    while (again != 0) {
       constexpr int WIDE = MOST / 64;
-      const int l64 = opaque_tid() & 63, which = again[i];
+      const int lane = opaque_tid() & 63, first_lane = __builtin_ctzll(again);
+      again &= L == 64 ? 0 : ~(0xffffull << (first_lane & 48));
+      const int which = wave * TPW + first_lane / L;
       const int64_t t = (int64_t)first + t0 + which;
       float l[WIDE];
       double c[WIDE];
-      load_logits<F, 64, WIDE>(p, t, l64, l);
+      load_logits<F, 64, WIDE>(p, t, lane, l);
       const float top = top_logit<64, WIDE>(p, l);
-      choice_scores<double, 64, WIDE>(p, l, l64, top, c);
+      choice_scores<double, 64, WIDE>(p, l, lane, top, c);
       if (p.top_groups < p.groups) {
-        limit_groups<double, 64, WIDE>(p, l64, 0.0, (double*)area[wave], c);
+        limit_groups<double, 64, WIDE>(p, lane, 0.0, (double*)area[wave], c);
         if (p.ranked) {
 #pragma unroll
           for (int k = 0; k < WIDE; ++k) c[k] = c[k] > -(double)__builtin_inff() ? (double)l[k] : c[k];
         }
       }
-      pick_in_turn<double, 64, WIDE>(p, l64, 0.0, c, sel[which]);
-      finish_token<F, 64, WIDE>(p, t, l64, l, top, false, sel[which], base);
+      pick_in_turn<double, 64, WIDE>(p, lane, 0.0, c, sel[which]);
+      finish_token<F, 64, WIDE>(p, t, lane, l, top, false, sel[which], base);
     }
-    __syncthreads();
-    if (threadIdx.x == 0) agains = 0;
-    __syncthreads();
   }
+  __syncthreads();
   if (p.counts != nullptr) {
-    for (int e = threadIdx.x; e < p.E; e += ROUTE_THREADS)
-      p.counts[(int64_t)blockIdx.x * p.E + e] = base[e];
+    // (a block's tokens, and so an expert's choices, number less than 2^16)
+    const int words = (p.E + 1) / 2;
+    for (int i = threadIdx.x; i < words; i += ROUTE_THREADS)
+      p.counts[(int64_t)blockIdx.x * words + i] =
+          (uint32_t)base[2 * i] | (2 * i + 1 < p.E ? (uint32_t)base[2 * i + 1] << 16 : 0u);
     return;
   }
   const int total = scan_experts(base, p.E, scratch);
@@ -623,33 +638,42 @@ __global__ __launch_bounds__(ROUTE_THREADS) static void route_place(RouteParams 
     mask[e] = 0;
   }
   __syncthreads();
-  // threads e, e + R, .. share expert e's column of the counts, 16 loads in
-  // flight
+  // threads i, i + R, .. share the column of the experts 2 i and 2 i + 1, 16 loads
+  // in flight: all blocks read all counts, from L2 (in 32 bits each, 64 MB for
+  // 16384 tokens and 256 experts, 8.7 us for 7.8)
+  const int words = (p.E + 1) / 2;
   int R = 64;
-  while (R < p.E) R *= 2;
-  const int e = (int)threadIdx.x & (R - 1), step = ROUTE_THREADS / R;
-  if (e < p.E) {
-    int all = 0, mine = 0;
+  while (R < words) R *= 2;
+  const int i = (int)threadIdx.x & (R - 1), step = ROUTE_THREADS / R;
+  if (i < words) {
+    int all[2] = {0, 0}, mine[2] = {0, 0};
     for (int i0 = (int)threadIdx.x / R; i0 < blocks; i0 += 16 * step) {
-      const int32_t* c = p.counts + (int64_t)i0 * p.E + e;
-      int v[16];
+      const uint32_t* c = p.counts + (int64_t)i0 * words + i;
+      uint32_t v[16];
 #pragma unroll
-      for (int u = 0; u < 16; ++u) v[u] = i0 + u * step < blocks ? c[u * step * p.E] : 0;
+      for (int u = 0; u < 16; ++u) v[u] = i0 + u * step < blocks ? c[u * step * words] : 0;
 #pragma unroll
       for (int u = 0; u < 16; ++u) {
-        all += v[u];
-        mine += i0 + u * step < b ? v[u] : 0;
+        const uint32_t w = i0 + u * step < b ? v[u] : 0;
+        all[0] += v[u] & 0xffff;
+        all[1] += v[u] >> 16;
+        mine[0] += w & 0xffff;
+        mine[1] += w >> 16;
       }
     }
-    atomicAdd(&base[e], all);
-    atomicAdd(&before[e], mine);
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      if (2 * i + h < p.E) {
+        atomicAdd(&base[2 * i + h], all[h]);
+        atomicAdd(&before[2 * i + h], mine[h]);
+      }
   }
   __syncthreads();
   const int total = scan_experts(base, p.E, scratch);
   if (b == 0)
-    for (int i = threadIdx.x; i < p.E; i += ROUTE_THREADS) p.ends[i] = i + 1 < p.E ? base[i + 1] : total;
+    for (int e = threadIdx.x; e < p.E; e += ROUTE_THREADS) p.ends[e] = e + 1 < p.E ? base[e + 1] : total;
   __syncthreads();
-  for (int i = threadIdx.x; i < p.E; i += ROUTE_THREADS) base[i] += before[i];
+  for (int e = threadIdx.x; e < p.E; e += ROUTE_THREADS) base[e] += before[e];
   __syncthreads();
   place_chunk(p, first, held, base, mask);
   for (int t0 = first + 64; t0 < end; t0 += 64) place_chunk(p, t0, load_experts(p, t0), base, mask);

@@ -210,9 +210,9 @@ def route_bytes(T, E, k):
 
 def test_route_workspace():
     assert route_bytes(0, 64, 2) == 0 and route_bytes(128, 1024, 64) == 0
-    assert route_bytes(129, 64, 2) == 3 * 64 * 4            # 3 blocks of 64 tokens
-    assert route_bytes(16384, 256, 8) == 256 * 256 * 4
-    assert route_bytes(40000, 8, 2) == 313 * 8 * 4 // 256 * 256 + 256   # 2 chunks a block
+    assert route_bytes(129, 64, 2) == 512                   # 3 blocks of 64 tokens, 32 words each
+    assert route_bytes(16384, 256, 8) == 256 * 256 * 2
+    assert route_bytes(40000, 7, 2) == 313 * 4 * 4 // 256 * 256 + 256   # 2 chunks a block
     assert lib().dense_gemm_route_workspace_size(8, 8, 2, None) == S.BAD_ARG
     assert lib().dense_gemm_route_workspace_size(8, 0, 2, ctypes.byref(SIZE())) == S.BAD_ARG
 
