@@ -914,6 +914,8 @@ def route(logits, k, score="softmax", bias=None, groups=1, top_groups=1, group_t
         r.bias = bias.data_ptr()
     if k < 0:
         raise ValueError("k must not be negative, got %d" % k)
+    if k > 64:  # (before memory is taken for it)
+        raise DenseGemmError(Status.TOO_LARGE, "dense_gemm_route")
     # one block of memory for the outputs, a part of it each: an allocation costs
     # twice what a view does
     n = T * k

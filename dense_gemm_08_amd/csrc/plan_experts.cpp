@@ -39,7 +39,7 @@ dense_gemm_status check_routing(int fmt, int64_t T, int64_t E, int64_t k, const 
   if ((!valid_fmt(fmt) && fmt != DENSE_GEMM_F32) || r == nullptr) return DENSE_GEMM_BAD_ARG;
   if (T < 0 || E < 0 || k < 0) return DENSE_GEMM_INVALID_DIM;
   if (E == 0 || k == 0 || k > E) return DENSE_GEMM_BAD_ARG;
-  if (E > ROUTE_MOST_EXPERTS || k > ROUTE_MOST_K || T > kLayerMaxDim / k) return DENSE_GEMM_TOO_LARGE;
+  if (E > ROUTE_MOST_EXPERTS || k > ROUTE_MOST_K || T > kRouteMostRows / k) return DENSE_GEMM_TOO_LARGE;
   if ((r->score != DENSE_GEMM_SOFTMAX && r->score != DENSE_GEMM_SIGMOID) || (r->renorm & ~1) != 0)
     return DENSE_GEMM_BAD_ARG;
   if (T == 0) return DENSE_GEMM_OK;

@@ -16,6 +16,9 @@ constexpr int ROUTE_MOST_EXPERTS = 1024;
 constexpr int ROUTE_MOST_K = 64;
 constexpr int ROUTE_MOST_GROUPS = 64;
 constexpr int ROUTE_THREADS = 1024;
+// Choices (tokens times k): the kernels look a block's tokens past the end in 32
+// bits.
+constexpr int64_t kRouteMostRows = kMaxDim - (1 << 20);
 
 struct RoutePlan {
   int64_t chunks;  // chunks of 64 tokens per block

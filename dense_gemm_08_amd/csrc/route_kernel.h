@@ -678,7 +678,8 @@ __global__ __launch_bounds__(ROUTE_THREADS) static void route_place(RouteParams 
   place_chunk(p, first, held, base, mask);
   for (int t0 = first + 64; t0 < end; t0 += 64) place_chunk(p, t0, load_experts(p, t0), base, mask);
   // the rows behind the last expert's
-  for (int i = total + b * ROUTE_THREADS + (int)threadIdx.x; i < p.T * p.k; i += blocks * ROUTE_THREADS)
+  for (int64_t i = (int64_t)total + b * ROUTE_THREADS + (int)threadIdx.x; i < (int64_t)p.T * p.k;
+       i += blocks * ROUTE_THREADS)
     p.tokens[i] = -1;
 }
 

@@ -87,10 +87,11 @@ dense_gemm_status dense_gemm_combine(int fmt, int64_t T, int64_t N, int64_t k, c
                      (const uint16_t*)residual, (uint16_t*)Y, ldh, ldr, ldy, T, h_rows, (int)N, (int)k, 1};
   while (p.lanes < 256 && p.lanes * 8 < N) p.lanes *= 2;
   const int64_t pieces = (N + p.lanes * 8 - 1) / (p.lanes * 8);
-  // (a grid's threads number less than 2^32 in each direction and in all)
+  // (fewer than 2^32 threads, and fewer than 2^16 rows of workgroups)
   const unsigned x = row_grid(T, 256 / p.lanes);
-  const int64_t most = ((int64_t)1 << 23) / x;
-  const dim3 grid(x, (unsigned)(pieces < most ? pieces : most));
+  int64_t y = ((int64_t)1 << 23) / x;
+  if (y > 65535) y = 65535;
+  const dim3 grid(x, (unsigned)(pieces < y ? pieces : y));
   if (fmt == DENSE_GEMM_BF16)
     hipLaunchKernelGGL(combine_rows<__bf16>, grid, dim3(256), 0, stream, p);
   else

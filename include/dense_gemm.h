@@ -479,7 +479,7 @@ dense_gemm_status dense_gemm_i8_workspace_size(int64_t M, int64_t N, int64_t K, 
  * R floats.  A row of zeros gets zeros and scale 0, one that holds an infinity
  * or NaN zeros and the scale NaN, and one whose index lies outside [0, x_rows)
  * zeros and scale 0.  Without rows, R may not exceed x_rows
- * (DENSE_GEMM_BAD_ARG). */
+ * (DENSE_GEMM_BAD_ARG).  Q and S must overlap neither X nor rows. */
 dense_gemm_status dense_gemm_quantize_i8(int fmt, int64_t R, int64_t K, const void* X, int64_t ldx,
                                          int64_t x_rows, const void* rows, void* Q, int64_t ldq,
                                          void* S, hipStream_t stream);
@@ -513,9 +513,10 @@ dense_gemm_status dense_gemm_quantize_i8(int fmt, int64_t R, int64_t K, const vo
  *   tokens   T k int32: the token of every row in the experts' order, within an
  *            expert in the tokens' order; -1 from ends[E - 1] on
  *   places   T x k int32: the row of every choice in that order
- * All 4-byte aligned, without gaps.  1 <= k <= 64, k at most the experts that
- * can stay, E <= 1024, groups <= 64 and a divisor of E.  Every output is
- * written whole and depends on the inputs alone.  T == 0 writes the ends. */
+ * All 4-byte aligned, without gaps, and overlapping nothing.  1 <= k <= 64, k at
+ * most the experts that can stay, E <= 1024, groups <= 64 and a divisor of E, T k
+ * <= 2^31 - 2^20.  Every output is written whole and depends on the inputs alone.
+ * T == 0 writes the ends. */
 typedef enum dense_gemm_score { DENSE_GEMM_SOFTMAX = 0, DENSE_GEMM_SIGMOID = 1 } dense_gemm_score;
 
 typedef struct dense_gemm_routing {

@@ -182,7 +182,8 @@ def test_route_refusals():
     assert route(T=-1) == S.INVALID_DIM and route(E=-1) == S.INVALID_DIM and route(k=-1) == S.INVALID_DIM
     assert route(E=0) == S.BAD_ARG and route(k=0) == S.BAD_ARG and route(k=17) == S.BAD_ARG
     assert route(E=1025) == S.TOO_LARGE and route(E=128, k=65) == S.TOO_LARGE
-    assert route(T=1 << 31) == S.TOO_LARGE and route(T=(1 << 30) + 1) == S.TOO_LARGE    # T k past 2^31
+    # T k stays 2^20 below 2^31
+    assert route(T=(1 << 31) - (1 << 20) + 1, k=1) == S.TOO_LARGE and route(T=1 << 30) == S.TOO_LARGE
     assert route(score=2) == S.BAD_ARG and route(renorm=2) == S.BAD_ARG
     for kw in (dict(groups=0), dict(groups=3), dict(groups=4, top_groups=0), dict(groups=4, top_groups=5),
                dict(groups=4, top_groups=2, group_top=0), dict(groups=4, top_groups=2, group_top=3),

@@ -287,6 +287,9 @@ def test_python_refusals():
         with pytest.raises(dg.DenseGemmError) as err:
             call()
         assert err.value.status == S.BAD_ARG
+    with pytest.raises(dg.DenseGemmError) as err:
+        dg.route(l, 1 << 40)
+    assert err.value.status == S.TOO_LARGE
     small = torch.empty(16, dtype=torch.uint8, device="cuda")
     with pytest.raises(dg.DenseGemmError) as err:
         dg.route(logits(200, 16, "f32"), 2, workspace=small)

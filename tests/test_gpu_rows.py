@@ -159,6 +159,38 @@ def test_quantize_into_given_outputs():
         assert (wide == 99).all()  # nothing beside the columns was written
 
 
+def test_more_rows_than_a_launch_has_workgroups():
+    # 2^21 workgroups of 16 rows, and some more rows in turn
+    R, K = (1 << 25) + 1000, 8
+    g = torch.Generator(device="cuda").manual_seed(5)
+    x = torch.randn((R, K), generator=g, device="cuda", dtype=torch.float16)
+    print("quantize_rows", R, K, flush=True)
+    Q, S = dg.quantize_rows(x)
+    for lo in range(0, R, 1 << 23):
+        part = x[lo:lo + (1 << 23)].double()
+        m = part.abs().amax(1, keepdim=True)
+        assert torch.equal(Q[lo:lo + (1 << 23)], torch.round(part * 127 / m).to(torch.int8))
+        assert torch.equal(S[lo:lo + (1 << 23)], (m[:, 0] / 127).float())
+
+
+def test_very_long_rows():
+    # more pieces of a row than a grid has rows of workgroups; segments of a row
+    N = 65535 * 2048 + 5003
+    h = (torch.arange(N, device="cuda") % 1021).to(torch.float16).view(1, N)
+    p = torch.zeros((1, 1), dtype=torch.int32, device="cuda")
+    w = torch.full((1, 1), 2.0, device="cuda")
+    print("combine", N, flush=True)
+    assert torch.equal(dg.combine_rows(h, p, w), 2 * h)
+    dh, dw = dg.combine_rows_grad(h, h, p, w)
+    assert torch.equal(dh, 2 * h)
+    total = float((h.double() ** 2).sum())
+    # (a lane's sum of N / 1024 products, and the lanes')
+    assert abs(float(dw) - total) <= (N / 1024 + 16) * 2.0 ** -24 * total
+    Q, S = dg.quantize_rows(h)
+    assert float(S) == torch.tensor(1020 / 127, dtype=torch.float64).float().item()
+    assert torch.equal(Q[0], torch.round((torch.arange(N, device="cuda") % 1021).double() * 127 / 1020).to(torch.int8))
+
+
 def choices(T, k, R, seed=0, missing=0.0):
     g = torch.Generator().manual_seed(T * 31 + k + seed)
     p = torch.randperm(max(R, T * k), generator=g)[:T * k].view(T, k).to(torch.int32)
