@@ -716,25 +716,47 @@ def _run(fn, name, args, stream, dev):
         raise DenseGemmError(st, name)
 
 
+def _matrix(t, dtype, what: str):
+    """(rows, columns, leading dimension, device number) of a 2-D device tensor
+    of this type (or of one of these) with unit column stride."""
+    shape = t.shape
+    if len(shape) == 2:
+        rows, cols = shape
+        ld, one = t.stride()
+        dev = t.get_device()
+        if (t.dtype is dtype or dtype is None) and dev >= 0 and (one == 1 or cols <= 1):
+            return rows, cols, (ld if rows > 1 else max(cols, 1)), dev
+    if dtype is not None and t.dtype is not dtype:
+        raise TypeError("%s must be %s, got %s" % (what, dtype, t.dtype))
+    if t.get_device() < 0:
+        raise ValueError("%s must be a device tensor" % what)
+    raise ValueError("%s must be 2-D with unit column stride" % what)
+
+
 def _i8(A, SA, B, SB, ends, bias, act, residual, preact, D, dtype, stream, workspace):
     if _lib is None:
         load_library()
     torch = _torch()
     int8, f32 = torch.int8, torch.float32
-    if A.dtype is not int8:
-        raise TypeError("A must be int8, got %s" % A.dtype)
-    if not A.is_cuda:
-        raise ValueError("A must be a device tensor")
-    if A.dim() != 2 or (A.stride(1) != 1 and A.shape[1] > 1):
-        raise ValueError("A must be 2-D with unit column stride")
-    dev = A.get_device()
+    M, K, lda, dev = _matrix(A, int8, "A")
     code = ACTS.get(act)
     if code is None:
         raise ValueError("act must be one of %s, got %r" % (", ".join(ACTS), act))
-    M, K = A.shape
-    _check_like(B, int8, dev, 2 if ends is None else 3, "B")
-    N = B.shape[-2]
-    if B.shape[-1] != K:
+    groups, G, stride = None, (), 0
+    if ends is None:
+        N, Kb, ldb, devb = _matrix(B, int8, "B")
+        if devb != dev:
+            raise ValueError("operands on different devices: A on cuda:%d, B on cuda:%d" % (dev, devb))
+    else:
+        _check_like(B, int8, dev, 3, "B")
+        _check_ends(ends, dev, torch)
+        count, N, Kb = B.shape
+        G = (count,)
+        if ends.shape[0] != count:
+            raise ValueError("%d group ends for %d matrices B" % (ends.shape[0], count))
+        stride, ldb = _stack(B)
+        groups = Groups(ends.data_ptr(), count, stride)
+    if Kb != K:
         raise ValueError("inner dimensions differ: A is %s, B is %s"
                          % (tuple(A.shape), tuple(B.shape)))
     if D is not None:
@@ -747,16 +769,6 @@ def _i8(A, SA, B, SB, ends, bias, act, residual, preact, D, dtype, stream, works
     fmt = _FMTS.get(dtype)
     if fmt is None:
         raise TypeError("D must be float16 or bfloat16, got %s" % dtype)
-    groups, G, sb_stride = None, (), N
-    if ends is None:
-        ldb = _ld(B)
-    else:
-        _check_ends(ends, dev, torch)
-        G = (B.shape[0],)
-        if ends.shape[0] != G[0]:
-            raise ValueError("%d group ends for %d matrices B" % (ends.shape[0], G[0]))
-        stride, ldb = _stack(B)
-        groups = Groups(ends.data_ptr(), G[0], stride)
     _check_dense(SA, f32, dev, (M,), "SA")
     _check_dense(SB, f32, dev, G + (N,), "SB")
     epi = None
@@ -780,10 +792,10 @@ def _i8(A, SA, B, SB, ends, bias, act, residual, preact, D, dtype, stream, works
             _used_by(D, stream, A.device)
     else:
         ldd = _check_rows(D, dtype, dev, (M, N), "D")
-    a, lda, b = A.data_ptr(), _ld(A), B.data_ptr()
+    a, b = A.data_ptr(), B.data_ptr()
     _launch("dense_gemm_i8",
-            (fmt[1], M, N, K, a, lda, SA.data_ptr(), b, ldb, SB.data_ptr(), sb_stride, D.data_ptr(),
-             ldd, epi, groups),
+            (fmt[1], M, N, K, a, lda, SA.data_ptr(), b, ldb, SB.data_ptr(), N, D.data_ptr(), ldd, epi,
+             groups),
             ("dense_gemm_i8_workspace_size", M, N, K, a, lda, b, ldb, groups, 0), workspace, stream,
             dev, torch)
     return D
@@ -819,8 +831,10 @@ def quantize_rows(X, rows=None, Q=None, S=None, stream=None):
     if _lib is None:
         load_library()
     torch = _torch()
-    fmt, _, dev = _check_first(X)
-    T, K = X.shape
+    fmt = _FMTS.get(X.dtype)
+    if fmt is None:
+        raise TypeError("X must be float16 or bfloat16, got %s" % X.dtype)
+    T, K, ldx, dev = _matrix(X, None, "X")
     R, index = T, None
     if rows is not None:
         if rows.dim() != 1:
@@ -842,7 +856,7 @@ def quantize_rows(X, rows=None, Q=None, S=None, stream=None):
     else:
         _check_dense(S, torch.float32, dev, (R,), "S")
     _run(_lib.dense_gemm_quantize_i8, "dense_gemm_quantize_i8",
-         (fmt[1], R, K, X.data_ptr(), _ld(X), T, index, Q.data_ptr(), ldq, S.data_ptr()), stream, dev)
+         (fmt[1], R, K, X.data_ptr(), ldx, T, index, Q.data_ptr(), ldq, S.data_ptr()), stream, dev)
     return Q, S
 
 
@@ -858,6 +872,7 @@ class Routes(NamedTuple):
 
 
 def _check_logits(logits, torch):
+    """(dense_gemm_fmt, tokens, experts, leading dimension, device number)."""
     if logits.dtype is torch.float32:
         fmt = 2
     else:
@@ -865,11 +880,7 @@ def _check_logits(logits, torch):
         if known is None:
             raise TypeError("logits must be float32, float16 or bfloat16, got %s" % logits.dtype)
         fmt = known[1]
-    if not logits.is_cuda:
-        raise ValueError("logits must be a device tensor")
-    if logits.dim() != 2 or (logits.stride(1) != 1 and logits.shape[1] > 1):
-        raise ValueError("logits must be 2-D with unit column stride")
-    return fmt, logits.get_device()
+    return (fmt,) + _matrix(logits, None, "logits")
 
 
 def _score(score):
@@ -906,8 +917,7 @@ def route(logits, k, score="softmax", bias=None, groups=1, top_groups=1, group_t
     if _lib is None:
         load_library()
     torch = _torch()
-    fmt, dev = _check_logits(logits, torch)
-    T, E = logits.shape
+    fmt, T, E, ld, dev = _check_logits(logits, torch)
     r = Routing(None, _score(score), bool(renorm), scale, groups, top_groups, group_top)
     if bias is not None:
         _check_dense(bias, torch.float32, dev, (E,), "bias")
@@ -930,7 +940,7 @@ def route(logits, k, score="softmax", bias=None, groups=1, top_groups=1, group_t
         _used_by(weights, stream, logits.device)
     at = ints.data_ptr()
     _launch("dense_gemm_route",
-            (fmt, T, E, k, logits.data_ptr(), _ld(logits), r, weights.data_ptr(), at, at + 4 * n,
+            (fmt, T, E, k, logits.data_ptr(), ld, r, weights.data_ptr(), at, at + 4 * n,
              at + 12 * n, at + 8 * n),
             ("dense_gemm_route_workspace_size", T, E, k), workspace, stream, dev, torch)
     return Routes(weights, experts, places, ends, tokens)
@@ -944,8 +954,7 @@ def route_grad(logits, experts, dweights, score="softmax", renorm=True, scale=1.
     if _lib is None:
         load_library()
     torch = _torch()
-    fmt, dev = _check_logits(logits, torch)
-    T, E = logits.shape
+    fmt, T, E, ld, dev = _check_logits(logits, torch)
     if experts.dim() != 2:
         raise ValueError("experts must be 2-D")
     k = experts.shape[1]
@@ -960,7 +969,7 @@ def route_grad(logits, experts, dweights, score="softmax", renorm=True, scale=1.
         ldd = _check_rows(D, logits.dtype, dev, (T, E), "D")
     r = Routing(None, _score(score), bool(renorm), scale, 1, 1, 1)
     _run(_lib.dense_gemm_route_grad, "dense_gemm_route_grad",
-         (fmt, T, E, k, logits.data_ptr(), _ld(logits), r, experts.data_ptr(), dweights.data_ptr(),
+         (fmt, T, E, k, logits.data_ptr(), ld, r, experts.data_ptr(), dweights.data_ptr(),
           D.data_ptr(), ldd), stream, dev)
     return D
 
@@ -984,8 +993,11 @@ def combine_rows(H, places, weights=None, residual=None, D=None, stream=None):
     if _lib is None:
         load_library()
     torch = _torch()
-    fmt, dtype, dev = _check_first(H)
-    R, N = H.shape
+    dtype = H.dtype
+    fmt = _FMTS.get(dtype)
+    if fmt is None:
+        raise TypeError("H must be float16 or bfloat16, got %s" % dtype)
+    R, N, ldh, dev = _matrix(H, None, "H")
     T, k = _check_choices(places, weights, dev, torch)
     res, ldr = None, 0
     if residual is not None:
@@ -999,7 +1011,7 @@ def combine_rows(H, places, weights=None, residual=None, D=None, stream=None):
     else:
         ldd = _check_rows(D, dtype, dev, (T, N), "D")
     _run(_lib.dense_gemm_combine, "dense_gemm_combine",
-         (fmt[1], T, N, k, H.data_ptr(), _ld(H), R, places.data_ptr(),
+         (fmt[1], T, N, k, H.data_ptr(), ldh, R, places.data_ptr(),
           None if weights is None else weights.data_ptr(), res, ldr, D.data_ptr(), ldd), stream, dev)
     return D
 
@@ -1013,22 +1025,25 @@ def combine_rows_grad(dY, H, places, weights=None, dh=None, stream=None):
     if _lib is None:
         load_library()
     torch = _torch()
-    fmt, dtype, dev = _check_first(H)
-    R, N = H.shape
+    dtype = H.dtype
+    fmt = _FMTS.get(dtype)
+    if fmt is None:
+        raise TypeError("H must be float16 or bfloat16, got %s" % dtype)
+    R, N, ldh, dev = _matrix(H, None, "H")
     T, k = _check_choices(places, weights, dev, torch)
     ldy = _check_rows(dY, dtype, dev, (T, N), "dY")
     if dh is None:
         dh = H.new_empty((R, N))
-        ldh = max(N, 1)
+        lddh = max(N, 1)
         if stream is not None:
             _used_by(dh, stream, H.device)
     else:
-        ldh = _check_rows(dh, dtype, dev, (R, N), "dh")
+        lddh = _check_rows(dh, dtype, dev, (R, N), "dh")
     dweights = H.new_empty((T, k), dtype=torch.float32)
     if stream is not None:
         _used_by(dweights, stream, H.device)
     _run(_lib.dense_gemm_combine_grad, "dense_gemm_combine_grad",
-         (fmt[1], T, N, k, dY.data_ptr(), ldy, H.data_ptr(), _ld(H), R, places.data_ptr(),
-          None if weights is None else weights.data_ptr(), dh.data_ptr(), ldh, dweights.data_ptr()),
+         (fmt[1], T, N, k, dY.data_ptr(), ldy, H.data_ptr(), ldh, R, places.data_ptr(),
+          None if weights is None else weights.data_ptr(), dh.data_ptr(), lddh, dweights.data_ptr()),
          stream, dev)
     return dh, dweights
