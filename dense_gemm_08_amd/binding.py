@@ -926,10 +926,19 @@ def route(logits, k, score="softmax", bias=None, groups=1, top_groups=1, group_t
         raise ValueError("k must not be negative, got %d" % k)
     if k > 64:  # (before memory is taken for it)
         raise DenseGemmError(Status.TOO_LARGE, "dense_gemm_route")
-    # one block of memory for the outputs, a part of it each: an allocation costs
-    # twice what a view does
+    # One block of memory for the outputs, a part of it each (an allocation costs
+    # twice what a view does), and behind them the workspace, which is small beside
+    # them: half a word per 64 tokens and expert.
     n = T * k
-    ints = logits.new_empty((3 * n + E,), dtype=torch.int32)
+    used = -(-(3 * n + E) // 64) * 64
+    need = 0
+    if workspace is None or workspace is True:
+        size = ctypes.c_size_t()
+        st = _lib.dense_gemm_route_workspace_size(T, E, k, ctypes.byref(size))
+        if st != 0:
+            raise DenseGemmError(st, "dense_gemm_route_workspace_size")
+        need = size.value
+    ints = logits.new_empty((used + need // 4,), dtype=torch.int32)
     weights = logits.new_empty((T, k), dtype=torch.float32)
     experts = ints.as_strided((T, k), (k, 1), 0)
     places = ints.as_strided((T, k), (k, 1), n)
@@ -939,10 +948,12 @@ def route(logits, k, score="softmax", bias=None, groups=1, top_groups=1, group_t
         _used_by(ints, stream, logits.device)
         _used_by(weights, stream, logits.device)
     at = ints.data_ptr()
-    _launch("dense_gemm_route",
-            (fmt, T, E, k, logits.data_ptr(), ld, r, weights.data_ptr(), at, at + 4 * n,
-             at + 12 * n, at + 8 * n),
-            ("dense_gemm_route_workspace_size", T, E, k), workspace, stream, dev, torch)
+    args = (fmt, T, E, k, logits.data_ptr(), ld, r, weights.data_ptr(), at, at + 4 * n, at + 12 * n,
+            at + 8 * n)
+    if workspace is None or workspace is True:
+        _run(_lib.dense_gemm_route, "dense_gemm_route", args + (at + 4 * used, need), stream, dev)
+    else:
+        _launch("dense_gemm_route", args, None, workspace, stream, dev, torch)
     return Routes(weights, experts, places, ends, tokens)
 
 

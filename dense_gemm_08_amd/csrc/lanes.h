@@ -114,51 +114,65 @@ __device__ __forceinline__ uint64_t dpp_move(uint64_t x) {
   return dpp_move<CTRL>((uint32_t)x) | ((uint64_t)dpp_move<CTRL>((uint32_t)(x >> 32)) << 32);
 }
 
-// The values of a row of 16 lanes in descending order, by a bitonic network: in
-// each step a lane and its partner keep the larger value in the lower one of
-// them (BIT: the bit of the lane that says which it is).
-template <int CTRL, int BIT, typename X>
-__device__ __forceinline__ X sort_step(X x, int lane) {
-  const X y = dpp_move<CTRL>(x);
+template <int S>
+__device__ __forceinline__ uint64_t across(uint64_t x, int which) {
+  return across<S>((uint32_t)x, which) | ((uint64_t)across<S>((uint32_t)(x >> 32), which) << 32);
+}
+
+// x of the lane whose number differs in bit D alone (D 16 and 32: of the wave).
+template <int D, typename X>
+__device__ __forceinline__ X other(X x) {
+  if constexpr (D == 1) return dpp_move<0xB1>(x);
+  if constexpr (D == 2) return dpp_move<0x4E>(x);
+  if constexpr (D == 4) return dpp_move<0x1B>(dpp_move<0x141>(x));  // mirrored by 8, then by 4
+  if constexpr (D == 8) return dpp_move<0x128>(x);                  // row_ror 8
+  const bool high = ((int)threadIdx.x & D) != 0;
+  const X a = across<D>(x, 0), b = across<D>(x, 1);
+  return high ? a : b;
+}
+// x of the lane mirrored within blocks of N lanes.
+template <int N, typename X>
+__device__ __forceinline__ X mirrored(X x) {
+  if constexpr (N == 2) return dpp_move<0xB1>(x);
+  if constexpr (N == 4) return dpp_move<0x1B>(x);
+  if constexpr (N == 8) return dpp_move<0x141>(x);
+  if constexpr (N == 16) return dpp_move<0x140>(x);
+  if constexpr (N == 32) return other<16>(dpp_move<0x140>(x));
+  if constexpr (N == 64) return other<32>(other<16>(dpp_move<0x140>(x)));
+}
+
+// A step of a bitonic network that sorts in descending order: of a lane and its
+// partner (which holds y), the lower one, whose bit BIT is clear, keeps the
+// larger value.
+template <int BIT, typename X>
+__device__ __forceinline__ X sort_step(X x, X y) {
+  const bool upper = ((int)threadIdx.x & BIT) != 0;
   if constexpr (sizeof(X) == 4) {
-    return lane & BIT ? min(x, y) : max(x, y);
+    return upper ? min(x, y) : max(x, y);
   } else {
-    return (y > x) != ((lane & BIT) != 0) ? y : x;
+    return (y > x) != upper ? y : x;
   }
 }
-template <typename X>
-__device__ __forceinline__ X sort_step_4(X x, int lane) {  // (lanes that differ in bit 2)
-  const X y = dpp_move<0x1B>(dpp_move<0x141>(x));
-  if constexpr (sizeof(X) == 4) {
-    return lane & 4 ? min(x, y) : max(x, y);
-  } else {
-    return (y > x) != ((lane & 4) != 0) ? y : x;
-  }
+// A bitonic run of 2 D lanes in descending order.
+template <int D, typename X>
+__device__ __forceinline__ X sort_bitonic(X x) {
+  x = sort_step<D>(x, other<D>(x));
+  if constexpr (D > 1) x = sort_bitonic<D / 2>(x);
+  return x;
 }
-template <typename X>
-__device__ __forceinline__ X sorted_in_row(X x) {
-  const int lane = (int)threadIdx.x & 15;
-  x = sort_step<0xB1, 1>(x, lane);
-  x = sort_step<0x1B, 2>(x, lane);
-  x = sort_step<0xB1, 1>(x, lane);
-  x = sort_step<0x141, 4>(x, lane);
-  x = sort_step<0x4E, 2>(x, lane);
-  x = sort_step<0xB1, 1>(x, lane);
-  x = sort_step<0x140, 8>(x, lane);
-  x = sort_step_4(x, lane);
-  x = sort_step<0x4E, 2>(x, lane);
-  return sort_step<0xB1, 1>(x, lane);
+// The values of N neighbouring lanes in descending order.
+template <int N, typename X>
+__device__ __forceinline__ X sorted_lanes(X x) {
+  if constexpr (N > 2) x = sorted_lanes<N / 2>(x);
+  x = sort_step<N / 2>(x, mirrored<N>(x));
+  if constexpr (N > 2) x = sort_bitonic<N / 4>(x);
+  return x;
 }
-// The 16 largest of two such rows, again in order.
+// The 16 largest of two rows that are in order, in order.
 template <typename X>
 __device__ __forceinline__ X merged_in_row(X x, X y) {
-  const int lane = (int)threadIdx.x & 15;
-  const X z = dpp_move<0x140>(y);
-  x = z > x ? z : x;
-  x = sort_step<0x128, 8>(x, lane);  // row_ror 8
-  x = sort_step_4(x, lane);
-  x = sort_step<0x4E, 2>(x, lane);
-  return sort_step<0xB1, 1>(x, lane);
+  const X z = mirrored<16>(y);
+  return sort_bitonic<8>(z > x ? z : x);
 }
 
 // Values that lanes of this wave left in LDS for each other: the accesses after

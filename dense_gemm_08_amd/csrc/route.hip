@@ -22,25 +22,27 @@ void set_routing(RouteParams& p, const void* logits, int64_t ld, int64_t T, int6
   p.scale = r.scale;
 }
 
-// f(lanes per token, experts per lane) for E experts: 16 lanes up to 256
-// experts, a wave beyond.
-template <typename F, typename Launch>
+// f(lanes per token, experts per lane) for E experts: 16 lanes up to 512 experts
+// for the choice (4096 tokens of 512: 16.4 us, 28 with a wave a token), up to 256
+// for the gradient (16384 of 512: 20.7, 17.3 so), a wave beyond.
+template <int MOST16, typename Launch>
 void by_experts(int64_t E, Launch&& launch) {
+  using std::integral_constant;
   if (E <= 64)
-    launch(std::integral_constant<int, 16>(), std::integral_constant<int, 4>());
+    launch(integral_constant<int, 16>(), integral_constant<int, 4>());
   else if (E <= 128)
-    launch(std::integral_constant<int, 16>(), std::integral_constant<int, 8>());
+    launch(integral_constant<int, 16>(), integral_constant<int, 8>());
   else if (E <= 256)
-    launch(std::integral_constant<int, 16>(), std::integral_constant<int, 16>());
+    launch(integral_constant<int, 16>(), integral_constant<int, 16>());
   else if (E <= 512)
-    launch(std::integral_constant<int, 64>(), std::integral_constant<int, 8>());
+    launch(integral_constant<int, MOST16 == 512 ? 16 : 64>(), integral_constant<int, MOST16 == 512 ? 32 : 8>());
   else
-    launch(std::integral_constant<int, 64>(), std::integral_constant<int, 16>());
+    launch(integral_constant<int, 64>(), integral_constant<int, 16>());
 }
 
 template <typename F>
 dense_gemm_status run_route(const RouteParams& p, const RoutePlan& plan, hipStream_t stream) {
-  by_experts<F>(p.E, [&](auto lanes, auto per) {
+  by_experts<512>(p.E, [&](auto lanes, auto per) {
     hipLaunchKernelGGL((route_choose<F, decltype(lanes)::value, decltype(per)::value>),
                        dim3((unsigned)plan.blocks), dim3(ROUTE_THREADS), 0, stream, p);
   });
@@ -51,7 +53,7 @@ dense_gemm_status run_route(const RouteParams& p, const RoutePlan& plan, hipStre
 
 template <typename F>
 dense_gemm_status run_grad(const RouteGradParams& p, hipStream_t stream) {
-  by_experts<F>(p.E, [&](auto lanes, auto per) {
+  by_experts<256>(p.E, [&](auto lanes, auto per) {
     constexpr int tokens = ROUTE_GRAD_THREADS / decltype(lanes)::value;
     const int64_t blocks = ((int64_t)p.T + tokens - 1) / tokens, most = 1 << 16;
     hipLaunchKernelGGL((route_grad<F, decltype(lanes)::value, decltype(per)::value>),

@@ -3,7 +3,7 @@
 // dispatch (the order of the chosen rows by expert), with the weights'
 // gradient.
 //
-// A token is handled by L neighbouring lanes (16, or a wave for many experts),
+// A token is handled by L neighbouring lanes (16, or a wave beyond 512 experts),
 // PER logits a lane in registers.  The
 // dispatch is a counting sort: a workgroup takes 64 tokens at a time and marks
 // in a 64-bit word per expert which of them chose it (LDS atomics of an OR,
@@ -16,6 +16,14 @@
 // errors of their scores; such a token's choice is made again in 64 bits, by a
 // wave, so that it does not depend on how a 32-bit exponential rounds.  Without
 // them the logits themselves are compared, which is exact.
+//
+// Bound by instructions and their latencies, not by memory: 16384 tokens of 256
+// FP32 logits (17 MB, 3 us), 8 chosen, take 9 us ranked by their logits, 14.5 with
+// a logistic and a bias, 19 with 4 of 8 groups; VALU busy half of that.  Of the
+// last two, 3 to 4 us are the handful of tokens whose choice 32 bits do not settle
+// and whose waves end last.  (One expert after the other found by a maximum over
+// all, with the 64-bit form in line: 79.)  route_place then takes 7.7 us, most of
+// it the counts of all blocks from L2 and the barriers of a counting sort.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -174,12 +182,16 @@ __device__ __forceinline__ uint32_t row_bits(uint64_t ballot) {
   const uint32_t half = lane < 32 ? (uint32_t)ballot : (uint32_t)(ballot >> 32);
   return lane & 16 ? half >> 16 : half & 0xffffu;
 }
-// x of lane n of this lane's row.
-__device__ __forceinline__ int in_row(int x, int n) {
+// x of lane n (the same in all lanes) of this lane's row, or of the wave.
+template <int L>
+__device__ __forceinline__ int at_lane(int x, int n) {
+  if constexpr (L == 64) return __builtin_amdgcn_readlane(x, n);
   return __builtin_amdgcn_ds_bpermute((((int)threadIdx.x & 48) | n) << 2, x);
 }
-__device__ __forceinline__ uint64_t in_row(uint64_t x, int n) {
-  return (uint32_t)in_row((int)(uint32_t)x, n) | ((uint64_t)(uint32_t)in_row((int)(uint32_t)(x >> 32), n) << 32);
+template <int L>
+__device__ __forceinline__ uint64_t at_lane(uint64_t x, int n) {
+  return (uint32_t)at_lane<L>((int)(uint32_t)x, n) |
+         ((uint64_t)(uint32_t)at_lane<L>((int)(uint32_t)(x >> 32), n) << 32);
 }
 
 // The larger of two numbers (32 bits: in one instruction, by the median with
@@ -204,6 +216,11 @@ __device__ __forceinline__ bool too_close(X a, X b, X near, X size) {
   return !(a - b > near + (X)0x1p-23 * size);  // (so is a difference that is no number)
 }
 
+// Where expert e's value lies in LDS: a gap every 16, so that groups whose sizes
+// are powers of two do not begin in the same few banks (256 experts in 8 groups:
+// 5 of 6 LDS cycles were conflicts).
+__device__ __forceinline__ constexpr int lds_at(int e) { return e + (e >> 4); }
+
 // Takes the experts outside the best groups from c.  `lds`: E values of this
 // token's, which receive c as it was.  Returns whether rounding could change
 // that.
@@ -211,7 +228,7 @@ template <typename X, int L, int PER>
 __device__ __forceinline__ bool limit_groups(const RouteParams& p, int lane, X near, X* lds, X (&c)[PER]) {
   const X NONE = -(X)__builtin_inff();
 #pragma unroll
-  for (int i = 0; i < PER; ++i) lds[i * L + lane] = c[i];
+  for (int i = 0; i < PER; ++i) lds[lds_at(i * L + lane)] = c[i];
   wave_lds_order();
   // A group's two best, found by `share` neighbouring lanes (up to 16, a power
   // of two) where there are no more groups than lanes; else several groups a
@@ -224,9 +241,10 @@ __device__ __forceinline__ bool limit_groups(const RouteParams& p, int lane, X n
     const int g = n * L + lane / share;
     X first = NONE, second = NONE;
     if (g < p.groups) {
-      const X* from = lds + g * p.group_size;
+      const int end = (g + 1) * p.group_size;
 #pragma unroll 8
-      for (int i = lane & (share - 1); i < p.group_size; i += share) take_top(from[i], first, second);
+      for (int e = g * p.group_size + (lane & (share - 1)); e < end; e += share)
+        take_top(lds[lds_at(e)], first, second);
     }
     auto join = [&](X f, X s) {
       take_top(f, first, second);
@@ -244,16 +262,19 @@ __device__ __forceinline__ bool limit_groups(const RouteParams& p, int lane, X n
   const bool exact = sizeof(X) == 8 || (p.ranked && p.group_top == 1);
   if (!exact) size = max_lanes<L>(size);
   bool unsure = false;
-  if constexpr (sizeof(X) == 4 && L == 16) {
-    if (p.groups <= 16) {
+  if constexpr (sizeof(X) == 4) {
+    if (p.groups <= L) {
       // the groups put in order all at once, each by the first of its lanes
       const uint64_t own = (lane & (share - 1)) == 0 ? ranked_pair(value[0], lane) : 0;
-      const uint64_t order = sorted_in_row(own);
-      const uint64_t last = in_row(order, p.top_groups - 1), next = in_row(order, p.top_groups);
-      const uint32_t stays = row_bits(__ballot(own != 0 && own >= last));  // bit (group * share)
+      const uint64_t order = sorted_lanes<L>(own);
+      // (top_groups < groups <= L)
+      const uint64_t last = at_lane<L>(order, p.top_groups - 1), next = at_lane<L>(order, p.top_groups);
+      const uint64_t in = __ballot(own != 0 && own >= last);
+      const uint64_t stays = L == 64 ? in : row_bits(in);  // bit (group * share)
       if (!exact) unsure = too_close(pair_value(last), pair_value(next), 2 * near, 4 * size);
       auto keep = [&](int i, int g) {
-        const int stay = (int)(stays << (31 - g * share)) >> 31;  // all bits, or none
+        const int stay = L == 16 ? (int)((uint32_t)stays << (31 - g * share)) >> 31  // all bits, or none
+                                 : -(int)(stays >> (g * share) & 1);
         c[i] = __builtin_bit_cast(float, (__builtin_bit_cast(int, c[i]) & stay) |
                                              (__builtin_bit_cast(int, (float)NONE) & ~stay));
       };
@@ -347,10 +368,11 @@ __device__ __forceinline__ bool pick_in_turn(const RouteParams& p, int lane, X n
 template <int PER>
 __device__ __forceinline__ bool pick_at_once(const RouteParams& p, int lane, float near, const float (&c)[PER],
                                              const float* lds, int* sel, bool* done) {
+  static_assert(ROUTE_MOST_K >= 32, "sel holds the candidates first");
   float m = c[0];
 #pragma unroll
   for (int i = 1; i < PER; ++i) m = larger_of(m, c[i]);
-  const float limit = value_of(max(in_row(sorted_in_row(key_of(m)), p.k), KEY_NONE + 1));
+  const float limit = value_of(max(at_lane<16>(sorted_lanes<16>(key_of(m)), p.k), KEY_NONE + 1));
   uint32_t bits = 0;
 #pragma unroll
   for (int i = PER - 1; i >= 0; --i) bits = bits + bits + (c[i] >= limit ? 1 : 0);
@@ -365,18 +387,19 @@ __device__ __forceinline__ bool pick_at_once(const RouteParams& p, int lane, flo
     }
   }
   wave_lds_order();
-  uint64_t best = 0, more = 0;
+  uint64_t best = 0;
   if (lane < total) {
     const int e = sel[lane];
-    best = ranked_pair(lds[e], e);
+    best = ranked_pair(lds[lds_at(e)], e);
   }
-  best = sorted_in_row(best);
+  best = sorted_lanes<16>(best);
   if (__ballot(total > 16) != 0) {
+    uint64_t more = 0;
     if (lane + 16 < total) {
       const int e = sel[lane + 16];
-      more = ranked_pair(lds[e], e);
+      more = ranked_pair(lds[lds_at(e)], e);
     }
-    best = merged_in_row(best, sorted_in_row(more));
+    best = merged_in_row(best, sorted_lanes<16>(more));
   }
   wave_lds_order();
   if (lane < p.k) sel[lane] = best != 0 ? pair_index(best) : -1;
@@ -535,9 +558,9 @@ __device__ __forceinline__ int32_t scan_experts(int32_t* x, int E, int32_t* scra
 template <typename F, int L, int PER>
 __global__ __launch_bounds__(ROUTE_THREADS) void route_choose(RouteParams p) {
   constexpr int TPW = 64 / L, WAVES_RT = ROUTE_THREADS / 64;
-  constexpr int AT_ONCE = ROUTE_THREADS / L, MOST = L * PER;
+  constexpr int AT_ONCE = ROUTE_THREADS / L, MOST = L * PER, ROOM = lds_at(MOST);
   // a wave's scores, by token (in 64 bits one token's)
-  __shared__ __attribute__((aligned(16))) float area[WAVES_RT][(TPW < 2 ? 2 : TPW) * MOST];
+  __shared__ __attribute__((aligned(16))) float area[WAVES_RT][(TPW < 2 ? 2 : TPW) * ROOM];
   __shared__ int sel[AT_ONCE][ROUTE_MOST_K];  // the chosen, in order
   __shared__ uint64_t mask[MOST];
   __shared__ int32_t base[MOST], scratch[WAVES_RT];
@@ -562,20 +585,22 @@ __global__ __launch_bounds__(ROUTE_THREADS) void route_choose(RouteParams p) {
       const float near = choice_scores<float, L, PER>(p, l, lane, top, c);
       bool unsure = false, done = false;
       if (p.top_groups < p.groups) {
-        unsure = limit_groups<float, L, PER>(p, lane, near, area[wave] + sub * MOST, c);
+        unsure = limit_groups<float, L, PER>(p, lane, near, area[wave] + sub * ROOM, c);
         if (p.ranked && p.group_top > 1) {
           // (sums of scores chose the groups; within them the logits rank)
 #pragma unroll
           for (int i = 0; i < PER; ++i) c[i] = c[i] > -__builtin_inff() ? l[i] : c[i];
         }
       }
+      // (a wave of 64 lanes a token finds them in turn: the network of its
+      // candidates would spill registers, 1024 experts, 4096 tokens 65 us against 45)
       if constexpr (L == 16) {
         if (p.k < 16) {
-          float* lds = area[wave] + sub * MOST;
+          float* lds = area[wave] + sub * ROOM;
           if (p.top_groups == p.groups || (p.ranked && p.group_top > 1)) {
             wave_lds_order();
 #pragma unroll
-            for (int i = 0; i < PER; ++i) lds[i * L + lane] = c[i];
+            for (int i = 0; i < PER; ++i) lds[lds_at(i * L + lane)] = c[i];
             wave_lds_order();
           }
           unsure |= pick_at_once<PER>(p, lane, near, c, lds, sel[slot], &done);

