@@ -1031,8 +1031,10 @@ def combine_rows_grad(dY, H, places, weights=None, dh=None, stream=None):
     """(dh, dweights), the gradients of :func:`combine_rows`: dh[places[t, j]] =
     weights[t, j] * dY[t] and dweights[t, j] = dY[t] . H[places[t, j]] (T x k
     float32).  Rows of dh (like H) that no place names are not written: with dh
-    None they hold whatever the allocator returned.  A place outside H writes no
-    row and a dweights of 0."""
+    None they hold whatever the allocator returned.  Places other than -1 are to
+    differ, as :func:`route`'s do: products are not summed, an element of a row
+    named twice is one of the two.  A place outside H writes no row and a dweights
+    of 0."""
     if _lib is None:
         load_library()
     torch = _torch()

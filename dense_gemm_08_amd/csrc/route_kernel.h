@@ -256,11 +256,12 @@ __device__ __forceinline__ bool limit_groups(const RouteParams& p, int lane, X n
     if (share > 8) join(dpp_move<0x140>(first), dpp_move<0x140>(second));
     const bool two = p.group_top > 1 && second > NONE;
     value[n] = two ? first + second : first;
+    // (a sum below FP32's range is still a group's that can be chosen)
+    if (sizeof(X) == 4 && two) value[n] = fmax(value[n], -(X)3.402823466e38f);
     if (first > NONE) size = fmax(size, fmax(fabs(first), two ? fabs(second) : (X)0));
     if (share > 1) break;
   }
   const bool exact = sizeof(X) == 8 || (p.ranked && p.group_top == 1);
-  if (!exact) size = max_lanes<L>(size);
   bool unsure = false;
   if constexpr (sizeof(X) == 4) {
     if (p.groups <= L) {
@@ -271,7 +272,11 @@ __device__ __forceinline__ bool limit_groups(const RouteParams& p, int lane, X n
       const uint64_t last = at_lane<L>(order, p.top_groups - 1), next = at_lane<L>(order, p.top_groups);
       const uint64_t in = __ballot(own != 0 && own >= last);
       const uint64_t stays = L == 64 ? in : row_bits(in);  // bit (group * share)
-      if (!exact) unsure = too_close(pair_value(last), pair_value(next), 2 * near, 4 * size);
+      // (the size of the two in question: others may be masked by huge biases)
+      if (!exact) {
+        size = max_lanes<L>(own == last || own == next ? size : (X)0);
+        unsure = too_close(pair_value(last), pair_value(next), 2 * near, 4 * size);
+      }
       auto keep = [&](int i, int g) {
         const int stay = L == 16 ? (int)((uint32_t)stays << (31 - g * share)) >> 31  // all bits, or none
                                  : -(int)(stays >> (g * share) & 1);
@@ -288,6 +293,7 @@ __device__ __forceinline__ bool limit_groups(const RouteParams& p, int lane, X n
       return unsure;
     }
   }
+  if (!exact) size = max_lanes<L>(size);
   uint64_t stays = 0;
   X least = 0;
   for (int n = 0; n <= p.top_groups; ++n) {
@@ -501,7 +507,7 @@ __device__ __forceinline__ void place_chunk(const RouteParams& p, int t0, const 
 #pragma unroll
   for (int u = 0; u < HELD; ++u) {
     const int i = u * ROUTE_THREADS + (int)threadIdx.x;
-    t[u] = (int)((uint32_t)(i * p.k_inverse) >> 20);
+    t[u] = (int)((uint32_t)i * (uint32_t)p.k_inverse >> 20);
     if (h.e[u] >= 0) atomicOr((unsigned long long*)&mask[h.e[u]], 1ull << t[u]);
     if (n <= (u + 1) * ROUTE_THREADS) break;
   }

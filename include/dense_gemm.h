@@ -564,8 +564,8 @@ dense_gemm_status dense_gemm_combine(int fmt, int64_t T, int64_t N, int64_t k, c
  *     dweights[t][j]   = sum_n DY[t][n] * H[places[t][j]][n]   (FP32)
  * Either may be null (H is read for dweights alone, and dweights needs N > 0:
  * DENSE_GEMM_BAD_ARG).  Rows of DH that no place names are left as they were;
- * the places of dense_gemm_route name each row once (of one named twice, either
- * may stay).  A place outside [0, h_rows) writes no row and a dweights of 0.
+ * the places of dense_gemm_route name each row once (of one named twice, each
+ * element is one of the two).  A place outside [0, h_rows) writes no row and a dweights of 0.
  * DH must overlap neither H nor DY. */
 dense_gemm_status dense_gemm_combine_grad(int fmt, int64_t T, int64_t N, int64_t k, const void* DY,
                                           int64_t lddy, const void* H, int64_t ldh, int64_t h_rows,

@@ -186,6 +186,33 @@ def test_scores_that_underflow():
     run(l, 4, "beside a large one")
 
 
+@pytest.mark.parametrize("E", [16, 64, 256, 512, 1024])
+def test_masks_of_the_lowest_value(E):
+    # in the logits these can still be chosen, in the bias too, where the sums of
+    # two for a group pass FP32's range
+    k, low = 6, torch.finfo(torch.float32).min
+    for dtype in TYPES:
+        l = logits(90, E, dtype)
+        l[:, ::3] = torch.finfo(TYPES[dtype]).min
+        l[4] = torch.finfo(TYPES[dtype]).min
+        for kw in (dict(), dict(renorm=False), dict(score="sigmoid", bias=biases(E)),
+                   dict(score="sigmoid", groups=4, top_groups=2, group_top=2)):
+            run(l, k, "lowest logits", **kw)
+        l = logits(90, E, dtype, seed=1)
+        for off in (E // 4 - 1, E // 2, 3 * E // 4 + 1, E):  # (one group stays, two, none whole)
+            bias = biases(E)
+            bias[E - off:] = low
+            for groups in (4, 8) if E < 512 else (4, 32):
+                for top in (2, groups - 1):
+                    if E // groups * top >= k:
+                        r = run(l, k, "lowest biases", score="sigmoid", bias=bias, groups=groups, top_groups=top,
+                                group_top=2)
+                        assert int(r.ends[-1]) == 90 * k
+        bias[:E // 4] = 0.5 * low
+        bias[E // 4:E // 2] = 0.75 * low
+        run(l, k, "low biases", bias=bias, groups=4, top_groups=2, group_top=2)
+
+
 def test_strides():
     for dtype in TYPES:
         for E, ld in ((48, 51), (256, 300), (130, 133)):
