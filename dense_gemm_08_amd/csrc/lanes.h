@@ -95,14 +95,19 @@ __device__ __forceinline__ X sum_lanes(X x) {
   return reduce_lanes<L>(x, [](X a, X b) { return a + b; });
 }
 
-// The sum of x over the lanes before this one in its row of 16.
-__device__ __forceinline__ int sum_before(int x) {
-  int s = x;
-  s += __builtin_amdgcn_update_dpp(0, s, 0x111, 0xf, 0xf, true);  // row_shr 1, 2, 4, 8
-  s += __builtin_amdgcn_update_dpp(0, s, 0x112, 0xf, 0xf, true);
-  s += __builtin_amdgcn_update_dpp(0, s, 0x114, 0xf, 0xf, true);
-  s += __builtin_amdgcn_update_dpp(0, s, 0x118, 0xf, 0xf, true);
-  return s - x;
+// The sum of x over the lanes up to this one in its row of 16, and in the wave.
+__device__ __forceinline__ int sum_up_to_row(int x) {
+  x += __builtin_amdgcn_update_dpp(0, x, 0x111, 0xf, 0xf, true);  // row_shr 1, 2, 4, 8
+  x += __builtin_amdgcn_update_dpp(0, x, 0x112, 0xf, 0xf, true);
+  x += __builtin_amdgcn_update_dpp(0, x, 0x114, 0xf, 0xf, true);
+  x += __builtin_amdgcn_update_dpp(0, x, 0x118, 0xf, 0xf, true);
+  return x;
+}
+__device__ __forceinline__ int sum_up_to(int x) {
+  x = sum_up_to_row(x);
+  x += __builtin_amdgcn_update_dpp(0, x, 0x142, 0xa, 0xf, false);  // row_bcast 15, into rows 1 and 3
+  x += __builtin_amdgcn_update_dpp(0, x, 0x143, 0xc, 0xf, false);  // row_bcast 31, into rows 2 and 3
+  return x;
 }
 // x of the next lane of the row; 0 in its last.
 __device__ __forceinline__ uint32_t from_next(uint32_t x) {

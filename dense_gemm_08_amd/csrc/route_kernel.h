@@ -383,7 +383,7 @@ __device__ __forceinline__ bool pick_at_once(const RouteParams& p, int lane, flo
 #pragma unroll
   for (int i = PER - 1; i >= 0; --i) bits = bits + bits + (c[i] >= limit ? 1 : 0);
   const int count = __popc(bits), total = sum_lanes<16>(count);
-  int at = sum_before(count);
+  int at = sum_up_to_row(count) - count;
   *done = __ballot(total > 32) == 0;
   if (!*done) return false;
   while (__ballot(bits != 0) != 0) {
@@ -499,9 +499,9 @@ __device__ __forceinline__ HeldExperts load_experts(const RouteParams& p, int t0
 
 // The order of those tokens' chosen rows: each choice's place, and its token
 // there.  base[e]: the place of the first of them that chose e, moved on past the
-// last at the end; mask: E words of zeros, left so.
+// last at the end if there are more; mask: E words of zeros, then left so.
 __device__ __forceinline__ void place_chunk(const RouteParams& p, int t0, const HeldExperts& h, int32_t* base,
-                                            uint64_t* mask) {
+                                            uint64_t* mask, bool more) {
   const int n = min(64, p.T - t0) * p.k;
   int t[HELD];
 #pragma unroll
@@ -523,6 +523,7 @@ __device__ __forceinline__ void place_chunk(const RouteParams& p, int t0, const 
     }
     p.places[(int64_t)t0 * p.k + i] = at;
   }
+  if (!more) return;
   __syncthreads();
   for (int e = threadIdx.x; e < p.E; e += ROUTE_THREADS) {
     base[e] += __popcll(mask[e]);
@@ -531,31 +532,23 @@ __device__ __forceinline__ void place_chunk(const RouteParams& p, int t0, const 
   __syncthreads();
 }
 
-// The running sums of x[0 .. E) over the block's threads, exclusive, written
-// over x; the total is returned.  scratch: one value per wave.
-__device__ __forceinline__ int32_t scan_experts(int32_t* x, int E, int32_t* scratch) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
-  int32_t carry = 0;
-  for (int e0 = 0; e0 < E; e0 += blockDim.x) {
-    const int e = e0 + threadIdx.x;
-    const int32_t v = e < E ? x[e] : 0;
-    int32_t s = v;
+// The sum of v over the block's threads up to this one; *total: over all.
+// scratch: one value per wave.
+__device__ __forceinline__ int32_t scan_threads(int32_t v, int32_t* scratch, int32_t* total) {
+  constexpr int WAVES_RT = ROUTE_THREADS / 64;
+  static_assert(ROUTE_MOST_EXPERTS <= ROUTE_THREADS, "a thread per expert");
+  const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  v = sum_up_to(v);
+  if ((threadIdx.x & 63) == 63) scratch[wave] = v;
+  __syncthreads();
+  *total = 0;
 #pragma unroll
-    for (int d = 1; d < 64; d *= 2) {
-      const int32_t y = __shfl_up(s, d);
-      if (lane >= d) s += y;
-    }
-    if (lane == 63) scratch[wave] = s;
-    __syncthreads();
-    int32_t before = carry;
-    for (int w = 0; w < waves; ++w) {
-      if (w < wave) before += scratch[w];
-      carry += scratch[w];
-    }
-    if (e < E) x[e] = before + s - v;
-    __syncthreads();
+  for (int w = 0; w < WAVES_RT; ++w) {
+    const int32_t x = scratch[w];
+    *total += x;
+    v += w < wave ? x : 0;
   }
-  return carry;
+  return v;
 }
 
 // The choice: a block takes `chunks` times 64 tokens.  A lone block also makes
@@ -649,10 +642,15 @@ __global__ __launch_bounds__(ROUTE_THREADS) void route_choose(RouteParams p) {
           (uint32_t)base[2 * i] | (2 * i + 1 < p.E ? (uint32_t)base[2 * i + 1] << 16 : 0u);
     return;
   }
-  const int total = scan_experts(base, p.E, scratch);
-  for (int e = threadIdx.x; e < p.E; e += ROUTE_THREADS) p.ends[e] = e + 1 < p.E ? base[e + 1] : total;
+  const int e = threadIdx.x, own = e < p.E ? base[e] : 0;
+  int32_t total;
+  const int32_t end = scan_threads(own, scratch, &total);
+  if (e < p.E) {
+    p.ends[e] = end;
+    base[e] = end - own;
+  }
   __syncthreads();
-  for (int t0 = 0; t0 < p.T; t0 += 64) place_chunk(p, t0, load_experts(p, t0), base, mask);
+  for (int t0 = 0; t0 < p.T; t0 += 64) place_chunk(p, t0, load_experts(p, t0), base, mask, t0 + 64 < p.T);
   for (int i = total + (int)threadIdx.x; i < p.T * p.k; i += ROUTE_THREADS) p.tokens[i] = -1;
 }
 
@@ -664,50 +662,63 @@ __global__ __launch_bounds__(ROUTE_THREADS) static void route_place(RouteParams 
   const int b = blockIdx.x, blocks = gridDim.x;
   const int first = b * p.chunks * 64, end = min(p.T, first + p.chunks * 64);
   const HeldExperts held = load_experts(p, first);
-  for (int e = threadIdx.x; e < p.E; e += ROUTE_THREADS) {
-    base[e] = before[e] = 0;
-    mask[e] = 0;
+  if (threadIdx.x < p.E) {
+    base[threadIdx.x] = before[threadIdx.x] = 0;
+    mask[threadIdx.x] = 0;
   }
-  __syncthreads();
-  // threads i, i + R, .. share the column of the experts 2 i and 2 i + 1, 16 loads
-  // in flight: all blocks read all counts, from L2 (in 32 bits each, 64 MB for
-  // 16384 tokens and 256 experts, 8.7 us for 7.8)
+  // Threads i, i + R, .. share the column of the experts 2 i and 2 i + 1: the rows
+  // of the blocks before this one and those from its own on, 16 loads of each in
+  // flight, which read zeros past their last row.  All blocks read all counts;
+  // what bounds that is the instructions per count, a dot product's (unpacked and
+  // added with checks of their row, 16384 tokens and 256 experts took 3.7 us of
+  // 7.6; in 32 bits each 8.7 in all).
   const int words = (p.E + 1) / 2;
   int R = 64;
   while (R < words) R *= 2;
   const int i = (int)threadIdx.x & (R - 1), step = ROUTE_THREADS / R;
+  uint32_t sum[2][2] = {};
   if (i < words) {
-    int all[2] = {0, 0}, mine[2] = {0, 0};
-    for (int i0 = (int)threadIdx.x / R; i0 < blocks; i0 += 16 * step) {
-      const uint32_t* c = p.counts + (int64_t)i0 * words + i;
-      uint32_t v[16];
+    typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+    const uint32_t row = (uint32_t)words * 4, rows[2] = {(uint32_t)b, (uint32_t)(blocks - b)};
+    const __amdgpu_buffer_rsrc_t r[2] = {
+        __builtin_amdgcn_make_buffer_rsrc(p.counts, 0, (int)(rows[0] * row), 0x00020000),
+        __builtin_amdgcn_make_buffer_rsrc(p.counts + (int64_t)b * words, 0, (int)(rows[1] * row), 0x00020000)};
+    uint32_t at = (uint32_t)((int)threadIdx.x / R * words + i) * 4;
+    for (uint32_t n = 0; n < max(rows[0], rows[1]); n += 16 * step, at += 16 * step * row) {
+      uint32_t v[2][16];
 #pragma unroll
-      for (int u = 0; u < 16; ++u) v[u] = i0 + u * step < blocks ? c[u * step * words] : 0;
+      for (int h = 0; h < 2; ++h)
 #pragma unroll
-      for (int u = 0; u < 16; ++u) {
-        const uint32_t w = i0 + u * step < b ? v[u] : 0;
-        all[0] += v[u] & 0xffff;
-        all[1] += v[u] >> 16;
-        mine[0] += w & 0xffff;
-        mine[1] += w >> 16;
-      }
+        for (int u = 0; u < 16; ++u)
+          v[h][u] = n < rows[h] ? __builtin_amdgcn_raw_buffer_load_b32(r[h], (int)(at + u * step * row), 0, 0) : 0u;
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int u = 0; u < 16; ++u) {
+          const u16x2 x = __builtin_bit_cast(u16x2, v[h][u]);
+          sum[h][0] = __builtin_amdgcn_udot2(x, (u16x2){1, 0}, sum[h][0], false);
+          sum[h][1] = __builtin_amdgcn_udot2(x, (u16x2){0, 1}, sum[h][1], false);
+        }
     }
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-      if (2 * i + h < p.E) {
-        atomicAdd(&base[2 * i + h], all[h]);
-        atomicAdd(&before[2 * i + h], mine[h]);
-      }
   }
   __syncthreads();
-  const int total = scan_experts(base, p.E, scratch);
-  if (b == 0)
-    for (int e = threadIdx.x; e < p.E; e += ROUTE_THREADS) p.ends[e] = e + 1 < p.E ? base[e + 1] : total;
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+    if (i < words && 2 * i + h < p.E) {
+      atomicAdd(&before[2 * i + h], (int)sum[0][h]);
+      atomicAdd(&base[2 * i + h], (int)sum[1][h]);
+    }
   __syncthreads();
-  for (int e = threadIdx.x; e < p.E; e += ROUTE_THREADS) base[e] += before[e];
+  const int e = threadIdx.x, earlier = e < p.E ? before[e] : 0, own = e < p.E ? base[e] + earlier : 0;
+  int32_t total;
+  const int32_t last = scan_threads(own, scratch, &total);
+  if (e < p.E) {
+    if (b == 0) p.ends[e] = last;
+    base[e] = last - own + earlier;
+  }
   __syncthreads();
-  place_chunk(p, first, held, base, mask);
-  for (int t0 = first + 64; t0 < end; t0 += 64) place_chunk(p, t0, load_experts(p, t0), base, mask);
+  place_chunk(p, first, held, base, mask, first + 64 < end);
+  for (int t0 = first + 64; t0 < end; t0 += 64) place_chunk(p, t0, load_experts(p, t0), base, mask, t0 + 64 < end);
   // the rows behind the last expert's
   for (int64_t i = (int64_t)total + b * ROUTE_THREADS + (int)threadIdx.x; i < (int64_t)p.T * p.k;
        i += blocks * ROUTE_THREADS)
