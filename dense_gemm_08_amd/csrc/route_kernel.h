@@ -19,11 +19,12 @@
 //
 // Bound by instructions and their latencies, not by memory: 16384 tokens of 256
 // FP32 logits (17 MB, 3 us), 8 chosen, take 9 us ranked by their logits, 14.5 with
-// a logistic and a bias, 19 with 4 of 8 groups; VALU busy half of that.  Of the
-// last two, 3 to 4 us are the handful of tokens whose choice 32 bits do not settle
-// and whose waves end last.  (One expert after the other found by a maximum over
-// all, with the 64-bit form in line: 79.)  route_place then takes 7.7 us, most of
-// it the counts of all blocks from L2 and the barriers of a counting sort.
+// a logistic and a bias, 18.6 with 4 of 8 groups: 5 to read and to mark what is
+// broken, 2.6 the scores, 3.2 the groups, 2 the choice, 1 the weights; VALU busy
+// 0.67 of that.  3 to 5 us of the last two are the handful of tokens whose choice
+// 32 bits do not settle (each 5 us of its wave), whose waves end last.  (One expert
+// after the other found by a maximum over all, with the 64-bit form in line: 79.)
+// route_place then takes 5.6 us.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -132,7 +133,7 @@ __device__ __forceinline__ X choice_scores(const RouteParams& p, const float (&l
     const X part = 1 / sum_lanes<L>(sum);
 #pragma unroll
     for (int i = 0; i < PER; ++i) c[i] *= part;
-    near = part * (X)0x1p-16;
+    near = part * (X)0x1p-17;
   } else if constexpr (FAST) {
     float e[PER];
 #pragma unroll
