@@ -62,6 +62,15 @@ def test_tokens(T):
         assert r.ends.shape == (E,) and int(r.ends[-1]) == T * k
 
 
+@pytest.mark.parametrize("E,T", [(7, 40000), (130, 18001), (300, 9000), (513, 4160), (1024, 5000)])
+def test_many_blocks(E, T):
+    # (the blocks' counts in several passes of the placing launch, every row width;
+    # two chunks a block past 32768 tokens)
+    l = logits(T, E, "f16")
+    l[::3, E // 2:] = -math.inf
+    run(l, min(E, 5), "many blocks", score="sigmoid", bias=biases(E))
+
+
 def test_many_tokens():
     l = logits(1 << 20, 4, "bf16")
     run(l, 1, "a million tokens")
