@@ -716,6 +716,17 @@ def _run(fn, name, args, stream, dev):
         raise DenseGemmError(st, name)
 
 
+def _zeros(like, shape, stream):
+    """Zeros of this shape with the type and device of ``like``, written on the
+    launch stream."""
+    t = like.new_empty(shape)
+    if stream is None:
+        return t.zero_()
+    _used_by(t, stream, like.device)
+    with _module.cuda.stream(_stream_object(stream, like.device)):
+        return t.zero_()
+
+
 def _matrix(t, dtype, what: str):
     """(rows, columns, leading dimension, device number) of a 2-D device tensor
     of this type (or of one of these) with unit column stride."""
@@ -1030,11 +1041,11 @@ def combine_rows(H, places, weights=None, residual=None, D=None, stream=None):
 def combine_rows_grad(dY, H, places, weights=None, dh=None, stream=None):
     """(dh, dweights), the gradients of :func:`combine_rows`: dh[places[t, j]] =
     weights[t, j] * dY[t] and dweights[t, j] = dY[t] . H[places[t, j]] (T x k
-    float32).  Rows of dh (like H) that no place names are not written: with dh
-    None they hold whatever the allocator returned.  Places other than -1 are to
-    differ, as :func:`route`'s do: products are not summed, an element of a row
-    named twice is one of the two.  A place outside H writes no row and a dweights
-    of 0."""
+    float32).  Rows of dh (like H) that no place names are zeros; with a ``dh`` of
+    the caller's they are not written, which saves the pass that clears it.  Places
+    other than -1 are to differ, as :func:`route`'s do: products are not summed, an
+    element of a row named twice is one of the two.  A place outside H writes no row
+    and a dweights of 0."""
     if _lib is None:
         load_library()
     torch = _torch()
@@ -1046,10 +1057,8 @@ def combine_rows_grad(dY, H, places, weights=None, dh=None, stream=None):
     T, k = _check_choices(places, weights, dev, torch)
     ldy = _check_rows(dY, dtype, dev, (T, N), "dY")
     if dh is None:
-        dh = H.new_empty((R, N))
+        dh = _zeros(H, (R, N), stream)
         lddh = max(N, 1)
-        if stream is not None:
-            _used_by(dh, stream, H.device)
     else:
         lddh = _check_rows(dh, dtype, dev, (R, N), "dh")
     dweights = H.new_empty((T, k), dtype=torch.float32)
