@@ -1038,14 +1038,16 @@ def combine_rows(H, places, weights=None, residual=None, D=None, stream=None):
     return D
 
 
-def combine_rows_grad(dY, H, places, weights=None, dh=None, stream=None):
+def combine_rows_grad(dY, H, places, weights=None, dh=None, stream=None, only=None):
     """(dh, dweights), the gradients of :func:`combine_rows`: dh[places[t, j]] =
     weights[t, j] * dY[t] and dweights[t, j] = dY[t] . H[places[t, j]] (T x k
     float32).  Rows of dh (like H) that no place names are zeros; with a ``dh`` of
     the caller's they are not written, which saves the pass that clears it.  Places
     other than -1 are to differ, as :func:`route`'s do: products are not summed, an
     element of a row named twice is one of the two.  A place outside H writes no row
-    and a dweights of 0."""
+    and a dweights of 0.  ``only``: "dh" or "dweights", the other one is not formed
+    and returned as None ("dh" reads dY alone, of H the shape counts; dweights of
+    rows without columns are refused)."""
     if _lib is None:
         load_library()
     torch = _torch()
@@ -1056,16 +1058,26 @@ def combine_rows_grad(dY, H, places, weights=None, dh=None, stream=None):
     R, N, ldh, dev = _matrix(H, None, "H")
     T, k = _check_choices(places, weights, dev, torch)
     ldy = _check_rows(dY, dtype, dev, (T, N), "dY")
-    if dh is None:
-        dh = _zeros(H, (R, N), stream)
-        lddh = max(N, 1)
+    if only not in (None, "dh", "dweights"):
+        raise ValueError("only must be None, 'dh' or 'dweights', got %r" % (only,))
+    to, lddh, dweights, dw = None, 0, None, None
+    if only == "dweights":
+        if dh is not None:
+            raise ValueError("dh is given, and dweights are to be formed alone")
     else:
-        lddh = _check_rows(dh, dtype, dev, (R, N), "dh")
-    dweights = H.new_empty((T, k), dtype=torch.float32)
-    if stream is not None:
-        _used_by(dweights, stream, H.device)
+        if dh is None:
+            dh = _zeros(H, (R, N), stream)
+            lddh = max(N, 1)
+        else:
+            lddh = _check_rows(dh, dtype, dev, (R, N), "dh")
+        # (null would say that dh is not wanted, and an empty one has no address)
+        to = dh.data_ptr() or places.data_ptr()
+    if only != "dh":
+        dweights = H.new_empty((T, k), dtype=torch.float32)
+        if stream is not None:
+            _used_by(dweights, stream, H.device)
+        dw = dweights.data_ptr()
     _run(_lib.dense_gemm_combine_grad, "dense_gemm_combine_grad",
          (fmt[1], T, N, k, dY.data_ptr(), ldy, H.data_ptr(), ldh, R, places.data_ptr(),
-          None if weights is None else weights.data_ptr(), dh.data_ptr(), lddh, dweights.data_ptr()),
-         stream, dev)
+          None if weights is None else weights.data_ptr(), to, lddh, dw), stream, dev)
     return dh, dweights

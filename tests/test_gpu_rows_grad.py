@@ -1,4 +1,5 @@
-"""What combine_rows_grad leaves where no place leads, on the GPU."""
+"""What combine_rows_grad leaves where no place leads, and its results one by one, on
+the GPU."""
 import pytest
 
 import dense_gemm_08_amd as dg
@@ -62,3 +63,48 @@ def test_they_are_cleared_at_every_replay():
         _experts.check_combine_grad(dh, dw, dy, h, p, w, torch.zeros_like(h), "replay %d" % rep)
         dh.fill_(9.0)
         assert torch.equal(dg.combine_rows_grad(dy, h, p, w)[1], dw)
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("T,N,k", [(1, 1, 1), (3, 7, 1), (33, 129, 5), (130, 1024, 8), (4, 4097, 3), (2, 16400, 9),
+                                   (9000, 40, 3)])
+def test_each_result_alone(T, N, k, dtype):
+    # every number of lanes a row; the same bits as both together
+    R = T * k + 3
+    h, dy = values(R, N, dtype), values(T, N, dtype, seed=1)
+    p, w = choices(T, k, R, missing=0.2)
+    print("combine_grad alone", T, N, k, dtype, flush=True)
+    for ww in (w, None):
+        before = torch.full((R, N), 3.0, dtype=h.dtype, device="cuda")
+        dh, dw = dg.combine_rows_grad(dy, h, p, ww, dh=before.clone())
+        nan = torch.full_like(h, float("nan"))  # (h is not read)
+        a, none = dg.combine_rows_grad(dy, nan, p, ww, dh=before.clone(), only="dh")
+        assert none is None and torch.equal(a, dh)
+        a, none = dg.combine_rows_grad(dy, nan, p, ww, only="dh")
+        _experts.check_combine_grad(a, dw, dy, h, p, ww, torch.zeros_like(h), "dh alone")
+        none, b = dg.combine_rows_grad(dy, h, p, ww, only="dweights")
+        assert none is None and torch.equal(b, dw)
+
+
+def test_alone_where_there_is_little():
+    h, dy = values(6, 24, "bf16"), values(3, 24, "bf16", seed=1)
+    p = torch.tensor([[0, 5], [1, 3], [2, 4]], dtype=torch.int32, device="cuda")
+    # rows of no columns have a gradient of the rows, as they have a sum
+    assert dg.combine_rows(h[:, :0], p).shape == (3, 0)
+    dh, none = dg.combine_rows_grad(dy[:, :0], h[:, :0], p, only="dh")
+    assert dh.shape == (6, 0) and none is None
+    # no rows at all, no tokens
+    dh, none = dg.combine_rows_grad(dy, h[:0], p, only="dh")
+    assert dh.shape == (0, 24) and none is None
+    none, dw = dg.combine_rows_grad(dy, h[:0], p, only="dweights")
+    assert (dw == 0).all()
+    dh, none = dg.combine_rows_grad(dy[:0], h, p[:0], only="dh")
+    assert (dh == 0).all() and dh.shape == h.shape
+    none, dw = dg.combine_rows_grad(dy[:0], h, p[:0], only="dweights")
+    assert dw.shape == (0, 2)
+    with pytest.raises(ValueError):
+        dg.combine_rows_grad(dy, h, p, only="weights")
+    with pytest.raises(ValueError):
+        dg.combine_rows_grad(dy, h, p, dh=h, only="dweights")
+    with pytest.raises(dg.DenseGemmError):
+        dg.combine_rows_grad(dy[:, :0], h[:, :0], p, only="dweights")
