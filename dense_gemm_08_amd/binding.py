@@ -874,7 +874,7 @@ def quantize_rows(X, rows=None, Q=None, S=None, stream=None):
 class Routes(NamedTuple):
     """What :func:`route` returns, on the device: ``weights`` (T x k float32),
     ``experts`` and ``places`` (T x k int32), ``ends`` (E int32) and ``tokens``
-    (T k int32)."""
+    (T k int32), each in memory of its own."""
     weights: Any
     experts: Any
     places: Any
@@ -935,37 +935,34 @@ def route(logits, k, score="softmax", bias=None, groups=1, top_groups=1, group_t
         r.bias = bias.data_ptr()
     if k < 0:
         raise ValueError("k must not be negative, got %d" % k)
-    if k > 64:  # (before memory is taken for it)
+    if k > 64 or T * k >= 1 << 31:  # (before memory is taken for it)
         raise DenseGemmError(Status.TOO_LARGE, "dense_gemm_route")
-    # One block of memory for the outputs, a part of it each (an allocation costs
-    # twice what a view does), and behind them the workspace, which is small beside
-    # them: half a word per 64 tokens and expert.
-    n = T * k
-    used = -(-(3 * n + E) // 64) * 64
-    need = 0
-    if workspace is None or workspace is True:
-        size = ctypes.c_size_t()
-        st = _lib.dense_gemm_route_workspace_size(T, E, k, ctypes.byref(size))
+    # (each result in memory of its own; like one that there is, and by a number, an
+    # allocation takes two thirds of the time)
+    experts = logits.new_empty((T, k), dtype=torch.int32)
+    weights = torch.empty_like(experts, dtype=torch.float32)
+    places = torch.empty_like(experts)
+    ends = experts.new_empty(E)
+    tokens = experts.new_empty(T * k)
+    out = Routes(weights, experts, places, ends, tokens)
+    if stream is not None:
+        for t in out:
+            _used_by(t, stream, logits.device)
+    args = (fmt, T, E, k, logits.data_ptr(), ld, r, weights.data_ptr(), experts.data_ptr(),
+            places.data_ptr(), ends.data_ptr(), tokens.data_ptr())
+    if workspace is None and T > 128:  # (up to there the call needs none)
+        need = ctypes.c_size_t()
+        st = _lib.dense_gemm_route_workspace_size(T, E, k, need)
         if st != 0:
             raise DenseGemmError(st, "dense_gemm_route_workspace_size")
-        need = size.value
-    ints = logits.new_empty((used + need // 4,), dtype=torch.int32)
-    weights = logits.new_empty((T, k), dtype=torch.float32)
-    experts = ints.as_strided((T, k), (k, 1), 0)
-    places = ints.as_strided((T, k), (k, 1), n)
-    tokens = ints.as_strided((n,), (1,), 2 * n)
-    ends = ints.as_strided((E,), (1,), 3 * n)
-    if stream is not None:
-        _used_by(ints, stream, logits.device)
-        _used_by(weights, stream, logits.device)
-    at = ints.data_ptr()
-    args = (fmt, T, E, k, logits.data_ptr(), ld, r, weights.data_ptr(), at, at + 4 * n, at + 12 * n,
-            at + 8 * n)
-    if workspace is None or workspace is True:
-        _run(_lib.dense_gemm_route, "dense_gemm_route", args + (at + 4 * used, need), stream, dev)
+        ws = experts.new_empty(need.value // 4)
+        if stream is not None:
+            _used_by(ws, stream, logits.device)
+        _run(_lib.dense_gemm_route, "dense_gemm_route", args + (ws.data_ptr(), need.value), stream, dev)
     else:
-        _launch("dense_gemm_route", args, None, workspace, stream, dev, torch)
-    return Routes(weights, experts, places, ends, tokens)
+        _launch("dense_gemm_route", args, ("dense_gemm_route_workspace_size", T, E, k), workspace, stream,
+                dev, torch)
+    return out
 
 
 def route_grad(logits, experts, dweights, score="softmax", renorm=True, scale=1.0, D=None, stream=None):
