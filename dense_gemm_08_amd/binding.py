@@ -1008,7 +1008,12 @@ def combine_rows(H, places, weights=None, residual=None, D=None, stream=None):
     with FP32 sums and one rounding: the experts' rows back to their tokens, by
     the ``places`` (T x k int32) and ``weights`` (T x k float32; None: ones, as
     for the gradient of rows gathered by ``tokens``) of :func:`route`.  A place
-    outside H adds its weight times zero.  ``residual`` may be D itself."""
+    outside H adds its weight times zero.  ``residual`` may be D itself.
+
+    Places may name a row more than once, but :func:`combine_rows_grad` does not
+    form the gradient of such a row.  That is a sum over the choices that name it,
+    and this function's: of dY in place of H, with places (R x m, m the most choices
+    of a row) the tokens of each row's choices, -1 behind them, and their weights."""
     if _lib is None:
         load_library()
     torch = _torch()
@@ -1040,9 +1045,10 @@ def combine_rows_grad(dY, H, places, weights=None, dh=None, stream=None, only=No
     weights[t, j] * dY[t] and dweights[t, j] = dY[t] . H[places[t, j]] (T x k
     float32).  Rows of dh (like H) that no place names are zeros; with a ``dh`` of
     the caller's they are not written, which saves the pass that clears it.  Places
-    other than -1 are to differ, as :func:`route`'s do: products are not summed, an
-    element of a row named twice is one of the two.  A place outside H writes no row
-    and a dweights of 0.  ``only``: "dh" or "dweights", the other one is not formed
+    inside H are to differ, as :func:`route`'s do.  A row named twice gets no gradient
+    here: each of its elements is that of one choice or another, not their sum, nor
+    the same one at every call (:func:`combine_rows` says what forms it; dweights
+    are not concerned).  A place outside H writes no row and a dweights of 0.  ``only``: "dh" or "dweights", the other one is not formed
     and returned as None ("dh" reads dY alone, of H the shape counts; dweights of
     rows without columns are refused)."""
     if _lib is None:

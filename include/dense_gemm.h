@@ -553,7 +553,8 @@ dense_gemm_status dense_gemm_route_grad(int fmt, int64_t T, int64_t E, int64_t k
  * or _BF16), residual (or null) and Y T x N; places T x k int32, weights T x k
  * floats (null: ones, e.g. for the gradient of rows that were gathered by
  * `tokens`).  1 <= k <= 64.  A place outside [0, h_rows) adds its weight times
- * zero.  residual may be Y itself; Y must overlap nothing else. */
+ * zero.  Places may name a row more than once (but see the gradient).  residual
+ * may be Y itself; Y must overlap nothing else. */
 dense_gemm_status dense_gemm_combine(int fmt, int64_t T, int64_t N, int64_t k, const void* H,
                                      int64_t ldh, int64_t h_rows, const void* places,
                                      const void* weights, const void* residual, int64_t ldr, void* Y,
@@ -563,10 +564,13 @@ dense_gemm_status dense_gemm_combine(int fmt, int64_t T, int64_t N, int64_t k, c
  *     DH[places[t][j]] = round( weights[t][j] * DY[t] )
  *     dweights[t][j]   = sum_n DY[t][n] * H[places[t][j]][n]   (FP32)
  * Either may be null (H is read for dweights alone, and dweights needs N > 0:
- * DENSE_GEMM_BAD_ARG).  Rows of DH that no place names are left as they were;
- * the places of dense_gemm_route name each row once (of one named twice, each
- * element is one of the two).  A place outside [0, h_rows) writes no row and a dweights of 0.
- * DH must overlap neither H nor DY. */
+ * DENSE_GEMM_BAD_ARG).  Rows of DH that no place names are left as they were.
+ * Places inside H are to differ, as those of dense_gemm_route do: of a row named
+ * twice each element is one of the two products, not their sum, and not the same
+ * one at every call.  (The sum is a dense_gemm_combine of DY: its places, for each
+ * row of H, the tokens of the choices that name the row, its weights theirs.)  A
+ * place outside [0, h_rows) writes no row and a dweights of 0.  DH must overlap
+ * neither H nor DY. */
 dense_gemm_status dense_gemm_combine_grad(int fmt, int64_t T, int64_t N, int64_t k, const void* DY,
                                           int64_t lddy, const void* H, int64_t ldh, int64_t h_rows,
                                           const void* places, const void* weights, void* DH,

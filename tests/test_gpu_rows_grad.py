@@ -3,7 +3,7 @@ the GPU."""
 import pytest
 
 import dense_gemm_08_amd as dg
-from tests import _experts
+from tests import _experts, _layer
 from tests.test_gpu_rows import choices, values
 
 torch = pytest.importorskip("torch")
@@ -108,3 +108,37 @@ def test_alone_where_there_is_little():
         dg.combine_rows_grad(dy, h, p, dh=h, only="dweights")
     with pytest.raises(dg.DenseGemmError):
         dg.combine_rows_grad(dy[:, :0], h[:, :0], p, only="dweights")
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("T,N,k,R", [(4, 24, 2, 3), (40, 130, 3, 17), (50, 1024, 1, 9), (9, 40, 6, 1)])
+def test_rows_named_more_than_once_get_their_gradient_by_a_combination(T, N, k, R, dtype):
+    # what combine_rows' docstring says to do where places repeat
+    g = torch.Generator().manual_seed(T + N)
+    p = torch.randint(-1, R, (T, k), generator=g, dtype=torch.int32)
+    w = torch.rand((T, k), generator=g)
+    h, dy = values(R, N, dtype), values(T, N, dtype, seed=1)
+    of = [[(t, j) for t in range(T) for j in range(k) if p[t, j] == r] for r in range(R)]
+    m = max(len(x) for x in of)
+    assert 1 < m <= 64
+    places = torch.full((R, m), -1, dtype=torch.int32)
+    weights = torch.zeros((R, m))
+    for r, x in enumerate(of):
+        for i, (t, j) in enumerate(x):
+            places[r, i], weights[r, i] = t, w[t, j]
+    p, w, places, weights = p.cuda(), w.cuda(), places.cuda(), weights.cuda()
+    dh = dg.combine_rows(dy, places, weights)
+    _experts.check_combine(dh, dy, places, weights, None, "sums of the choices")
+    # the same sums from the definition
+    rows, there = _experts.rows64(h, p)
+    hd = h.double().requires_grad_()
+    y = (torch.where(there[:, :, None], hd[p.long().clamp(min=0)], torch.zeros_like(rows)) * w.double()[:, :, None]).sum(1)
+    y.backward(dy.double())
+    terms, _ = _experts.rows64(dy, places)
+    S = (terms * weights.double()[:, :, None]).abs().sum(1)
+    off = (dh.double() - hd.grad).abs()
+    assert (off <= m * 2.0 ** -24 * S * 1.02 + _layer.rounding(hd.grad, h.dtype) * 1.01).all()
+    # the weights' gradient does not mind
+    _, dw = dg.combine_rows_grad(dy, h, p, w, only="dweights")
+    s, S = (rows * dy.double()[:, None, :]).sum(2), (rows * dy.double()[:, None, :]).abs().sum(2)
+    _layer.assert_close(dw, s, S * (N + 16) * 2.0 ** -24 * 1.01 + 2.0 ** -24 * s.abs(), "dweights")
