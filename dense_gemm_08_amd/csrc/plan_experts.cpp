@@ -235,6 +235,12 @@ dense_gemm_status i8_validate(int fmt, int64_t M, int64_t N, int64_t K, const vo
   return s;
 }
 
+// The 16-bit plan as it stands.  Its estimate of a K step of 128 x 128 tiles over
+// several rounds (79) is below what int8 takes, but where 110 would choose 256 x 256
+// tiles instead the two are as fast, us, 128 against 256: 8192 x 8192 x 1024 91 and
+// 97, x 1536 118 and 119, x 1664 124 and 123; 4096 x 4096 x 1024 25.1 and 25.2;
+// 16384 x 4096 x 1024 91 and 91; 5000 x 5000 x 1500 67 and 66; 3000 x 5000 x 1024
+// 26.1 and 25.6.
 dense_gemm_status i8_plan(int64_t M, int64_t N, int64_t K, const void* A, int64_t lda, const void* B,
                           int64_t ldb, int64_t cus, CallPlan* cp) {
   const int64_t K2 = pairs(K);
@@ -252,11 +258,19 @@ dense_gemm_status i8_plan(int64_t M, int64_t N, int64_t K, const void* A, int64_
 // With int8 values a K step holds twice the products for the same bytes, and 128
 // x 128 tiles, which move twice the bytes of 256 x 256 ones per product, fall
 // further behind than their 16-bit estimate (79) says: 110 decides as measured on
-// all of these but the last, us, 256 against 128: 16 groups of 256, N = K = 4096,
-// 79 and 94; of 1024 235 and 331, K = 2048 144 and 197; 32 of 512, N = 2048, K =
-// 4096, 130 and 167; 64 of 256, N = K = 2048, 87 and 107; 4 of 512, N = 512, K =
-// 4096, 47 and 22; 48 of 300, N = 1400, K = 2000, 111 and 96; 128 of 200, N =
-// 1024, K = 4096, 137 and 191.
+// all of these, us, 256 against 128: 16 groups of 256, N = K = 4096, 79 and 94; of
+// 1024 235 and 331, K = 2048 144 and 197; 32 of 512, N = 2048, K = 4096, 130 and
+// 167; 64 of 256, N = K = 2048, 87 and 107; 4 of 512, N = 512, K = 4096, 47 and 22;
+// 48 of 300, N = 1400, K = 2000, 111 and 96; 128 of 200, N = 1024, K = 4096, 137
+// and 191 (79 would take 128 there).
+// The other two limits are the 16-bit products' as they stand.  Up to 192 rows a
+// group on average 128 x 128 tiles: 16 groups of 128, N = K = 4096, 51 against 57
+// in 256 x 256 tiles, 64 of 128, N = K = 2048, 57 and 72; past 128 rows int8 would
+// be faster in those: 16 of 160, 75 and 58, 64 of 192, N = K = 2048, 89 and 77, 128
+// of 160, N = 1024, K = 4096, 183 and 133.  The small-output kernel for few tiles:
+// 8 groups of 1 to 16 rows, N = K = 4096, 34 to 37 against 35 in 128 x 128 tiles, 16
+// of 4, N = K = 2048, 25 against 21; not taken: 32 groups, N = K = 2048, 45 to 48
+// against 31.
 dense_gemm_status i8_grouped_plan(int64_t M, int64_t N, int64_t K, const void* A, int64_t lda,
                                   const void* B, int64_t ldb, const dense_gemm_groups& g, int64_t cus,
                                   GroupedPlan* out) {

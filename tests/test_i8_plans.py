@@ -48,3 +48,28 @@ def test_tiles_of_groups():
         assert tile(*call) == 256
     for call in ((2048, 512, 4096, 4), (14400, 1400, 2000, 48), (8192, 2048, 2048, 64)):
         assert tile(*call) == 128
+
+
+def test_tiles_of_groups_follow_what_was_measured():
+    # every shape whose two times stand beside the estimate, and the limits by rows
+    # a group and by the number of tiles
+    def tile(*call):
+        return _i8_cases.plans([("grouped",) + call])[0].tile_m
+    measured = {(4096, 4096, 4096, 16): 256, (16384, 4096, 4096, 16): 256, (16384, 4096, 2048, 16): 256,
+                (16384, 2048, 4096, 32): 256, (16384, 2048, 2048, 64): 256, (2048, 512, 4096, 4): 128,
+                (14400, 1400, 2000, 48): 128, (25600, 1024, 4096, 128): 256}
+    for call, want in measured.items():
+        assert tile(*call) == want, call
+    for call in ((2048, 4096, 4096, 16), (8192, 2048, 2048, 64), (2560, 4096, 4096, 16), (12288, 2048, 2048, 64),
+                 (20480, 1024, 4096, 128), (32, 2048, 2048, 32), (256, 2048, 2048, 32)):
+        assert tile(*call) == 128, call
+    for call in ((8, 4096, 4096, 8), (128, 4096, 4096, 8), (64, 2048, 2048, 16)):
+        assert tile(*call) == 16, call
+
+
+def test_tiles_of_one_matrix_are_the_16_bit_ones():
+    shapes = ((8192, 8192, 1024), (8192, 8192, 1536), (8192, 8192, 1664), (4096, 4096, 1024), (16384, 4096, 1024),
+              (5000, 5000, 1500), (3000, 5000, 1024))
+    for s, p in zip(shapes, _i8_cases.plans([("i8",) + s for s in shapes])):
+        assert (p.tile_m, p.tile_n, p.parts) == (128, 128, 1), s
+    assert _i8_cases.plans([("i8", 4096, 4096, 2048)])[0].tile_m == 256
