@@ -87,7 +87,17 @@ dense_gemm_status route_grad_validate(int fmt, int64_t T, int64_t E, int64_t k, 
 // Up to ROUTE_ALONE tokens one block makes the choice and the dispatch; beyond,
 // blocks of 64 tokens (more where they would number over ROUTE_BLOCKS: every
 // block of the second launch reads all blocks' counts; but less than 2^16, which
-// those hold).
+// those hold).  64 are the bits of the word that ranks an expert's tokens, and give
+// each CU a block at 16384 tokens.
+// Measured (logistic, bias, 8 chosen, FP32; us on the GPU), one block against two
+// launches: 64 experts, 80 tokens 10.6 and 10.2, 128 11.3 and 10.2, 256 19.7 and
+// 10.4; 256 experts 14.9 and 12.6, 16.6 and 13.2, 33 and 17; 1024 experts 56 and 49,
+// 87 and 49, 169 and 49.  What one block saves is the host's: 11.6 us a call where
+// two launches and their workspace take 16.5, so from 65 to 128 tokens it is the
+// faster of the two up to 64 experts or so in eager calls, and the slower of 1024.
+// ROUTE_BLOCKS 256, 512 and 1024 (BF16): 65536 tokens of 64 experts 29, 32 and 44, of
+// 256 42, 48 and 70, of 1024 296, 317 and 394; 131072 of 256 72, 76 and 98; 32768 of
+// 256, which 512 leaves at 64 a block, 27.5 and 33.8.
 constexpr int64_t ROUTE_ALONE = 128, ROUTE_BLOCKS = 512, ROUTE_CHUNKS = 1000;
 RoutePlan route_plan(int64_t T, int64_t E) {
   RoutePlan p;
@@ -108,6 +118,13 @@ RoutePlan route_plan(int64_t T, int64_t E) {
 // Sixteen lanes hold 1024 elements of a row, a wave 4096, four waves 16384,
 // sixteen 65536.  Short rows in number go to 16 lanes, rows that fit a wave to
 // four where there are too few of them for every SIMD.
+// Measured, us, rows x columns quantised (BF16), with the lanes: 65536 x 256 10 (16)
+// and 25 (64), 16384 x 1024 7.4 and 10.2, 1024 x 1024 4.3 and 3.1; 16384 x 4096 31.3
+// (64) and 33.9 (256), 1024 x 4096 4.7 and 4.4, 256 x 2048 3.5 and 3.1, 1 x 4096 4.0
+// and 3.0; 8192 x 8192 50 (64), 30 (256) and 68 (1024), 8192 x 16384 62 (256) and 82
+// (1024), 4096 x 32768 99 and 72.  The combined rows' gradient alike, choices x
+// columns: 16384 x 512 8.2 (16) and 14.4 (64), 32 x 4096 5.4 (64) and 4.8 (256), 16384
+// x 4096 52 and 64, 16384 x 8192 137 and 131 (but 8192 x 8192 52 and 60).
 int row_lanes(int64_t rows, int64_t cols, int64_t cus) {
   if (cols > 16384) return 1024;
   if (cols <= 1024 && rows >= 32 * cus) return 16;
