@@ -12,9 +12,9 @@
 // rings, the schedule and the tile choice are those of the 16-bit products with
 // half the K.
 //
-// Measured on the MI355X: 8192 x 5120 x 17408 560 us, 2610 TOP/s (the 16-bit
+// Measured on the MI355X: 8192 x 5120 x 17408 562 us, 2600 TOP/s (the 16-bit
 // product 1104 us; the board's power limits both, MFMA busy 0.76); 3000 x 5000 x
-// 4000 with GELU and Z 66 us, of which the K steps take 43 and the one round's
+// 4000 with GELU and Z 67 us, of which the K steps take 43 and the one round's
 // epilogue, 60 MB written by all CUs at once, most of the rest.
 #pragma once
 
