@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import enum
+import functools
 import os
 from typing import Any, NamedTuple
 
@@ -901,6 +902,16 @@ def _score(score):
     return code
 
 
+@functools.lru_cache(maxsize=64)
+def _route_workspace_size(T: int, E: int, k: int) -> int:
+    """dense_gemm_route_workspace_size, for shapes met lately without a call."""
+    need = ctypes.c_size_t()
+    st = _lib.dense_gemm_route_workspace_size(T, E, k, ctypes.byref(need))
+    if st != 0:
+        raise DenseGemmError(st, "dense_gemm_route_workspace_size")
+    return need.value
+
+
 def route(logits, k, score="softmax", bias=None, groups=1, top_groups=1, group_top=1, renorm=True,
           scale=1.0, stream=None, workspace=None):
     """The k experts of each token from its router logits (T x E, float32,
@@ -951,14 +962,11 @@ def route(logits, k, score="softmax", bias=None, groups=1, top_groups=1, group_t
     args = (fmt, T, E, k, logits.data_ptr(), ld, r, weights.data_ptr(), experts.data_ptr(),
             places.data_ptr(), ends.data_ptr(), tokens.data_ptr())
     if workspace is None and T > 128:  # (up to there the call needs none)
-        need = ctypes.c_size_t()
-        st = _lib.dense_gemm_route_workspace_size(T, E, k, need)
-        if st != 0:
-            raise DenseGemmError(st, "dense_gemm_route_workspace_size")
-        ws = experts.new_empty(need.value // 4)
+        need = _route_workspace_size(T, E, k)
+        ws = experts.new_empty(need // 4)
         if stream is not None:
             _used_by(ws, stream, logits.device)
-        _run(_lib.dense_gemm_route, "dense_gemm_route", args + (ws.data_ptr(), need.value), stream, dev)
+        _run(_lib.dense_gemm_route, "dense_gemm_route", args + (ws.data_ptr(), need), stream, dev)
     else:
         _launch("dense_gemm_route", args, ("dense_gemm_route_workspace_size", T, E, k), workspace, stream,
                 dev, torch)

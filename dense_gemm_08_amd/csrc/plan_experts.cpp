@@ -92,9 +92,10 @@ dense_gemm_status route_grad_validate(int fmt, int64_t T, int64_t E, int64_t k, 
 // Measured (logistic, bias, 8 chosen, FP32; us on the GPU), one block against two
 // launches: 64 experts, 80 tokens 10.6 and 10.2, 128 11.3 and 10.2, 256 19.7 and
 // 10.4; 256 experts 14.9 and 12.6, 16.6 and 13.2, 33 and 17; 1024 experts 56 and 49,
-// 87 and 49, 169 and 49.  What one block saves is the host's: 11.6 us a call where
-// two launches and their workspace take 16.5, so from 65 to 128 tokens it is the
-// faster of the two up to 64 experts or so in eager calls, and the slower of 1024.
+// 87 and 49, 169 and 49.  What one block saves is the host's: 11.5 us a call where
+// two launches and their workspace take 15.8, so from 65 to 128 tokens it is the
+// faster of the two for 64 experts in eager calls, about even for 256, and the
+// slower for 1024.
 // ROUTE_BLOCKS 256, 512 and 1024 (BF16): 65536 tokens of 64 experts 29, 32 and 44, of
 // 256 42, 48 and 70, of 1024 296, 317 and 394; 131072 of 256 72, 76 and 98; 32768 of
 // 256, which 512 leaves at 64 a block, 27.5 and 33.8.

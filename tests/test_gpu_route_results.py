@@ -48,3 +48,16 @@ def test_a_result_changed_in_place_leaves_what_autograd_saved(T):
     want = torch.full_like(x, 2.0)
     want[T - 4:] = 0.0
     assert torch.equal(x.grad, want)
+
+
+def test_too_many_choices_are_refused_before_memory_is_taken():
+    # 2^25 tokens of 64 choices, by a view: their results would be 32 GB
+    l = torch.zeros((1, 64), dtype=torch.bfloat16, device="cuda").expand(1 << 25, 64)
+    torch.cuda.synchronize()
+    torch.cuda.reset_peak_memory_stats()
+    before = torch.cuda.memory_allocated()
+    for k in (64, 65):
+        with pytest.raises(dg.DenseGemmError) as err:
+            dg.route(l, k)
+        assert err.value.status == dg.Status.TOO_LARGE
+    assert torch.cuda.max_memory_allocated() == before
